@@ -12,8 +12,13 @@ The entry points mirror include/dsv4attn.h:
   dsv4_attn_strerror;
 include/dsv4kvstore.h (the cache write before the step):
   dsv4_kv_store;
-and include/dsv4topk.h (the top-k selection that makes the C4 index lists):
-  dsv4_topk, dsv4_topk_max_length.
+include/dsv4topk.h (the top-k selection that makes the C4 index lists):
+  dsv4_topk, dsv4_topk_max_length;
+and include/dsv4gqa.h (the cache of the grouped-query model that drafts the
+tokens dsv4_attn_verify checks: its write, its one-token attention and the
+eviction of its rows):
+  make_gqa_cache, dsv4_gqa_store, dsv4_gqa_decode, dsv4_gqa_evict,
+  dsv4_gqa_decode_workspace_size, dsv4_gqa_evict_workspace_size.
 """
 from __future__ import annotations
 
@@ -28,15 +33,21 @@ LIB_PATH = os.path.join(_PKG, "libdsv4attn.so")
 
 DSV4_KV_BF16 = 0
 DSV4_KV_FP8_PACKED = 1
+DSV4_GQA_BF16 = 0
+DSV4_GQA_F16 = 1
+DSV4_GQA_E4M3 = 2
 DEV_ERR = {
     "SWA_PAGE": 0x01, "EXTRA_PAGE": 0x02, "INDEX_RANGE": 0x04, "POSITION": 0x08,
     "PLAN": 0x10, "TIMEOUT": 0x20, "REQ_ROW": 0x40, "STORE_ROW": 0x80, "TOPK_LENGTH": 0x100,
+    "GQA_PAGE": 0x200, "GQA_LENGTH": 0x400,
 }
 EXPORTED = [
     "dsv4_attn_swa", "dsv4_attn_c4_sparse", "dsv4_attn_c128_dense", "dsv4_attn_verify",
     "dsv4_attn_plan", "dsv4_attn_workspace_size", "dsv4_attn_get_device_error",
     "dsv4_attn_strerror", "dsv4_attn_c4_sparse_noalloc", "dsv4_kv_store",
     "dsv4_topk", "dsv4_topk_max_length",
+    "dsv4_gqa_store", "dsv4_gqa_decode", "dsv4_gqa_decode_workspace_size", "dsv4_gqa_evict",
+    "dsv4_gqa_evict_workspace_size",
 ]
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -51,6 +62,27 @@ class KvPool(ctypes.Structure):
         ("page_table_rows", ctypes.c_int32),
         ("page_table_stride", ctypes.c_int32),
         ("page_size", ctypes.c_int32),
+    ]
+
+
+class GqaCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p),
+        ("page_table_rows", ctypes.c_int32),
+        ("page_table_stride", ctypes.c_int32),
+        ("page_table_width", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("format", ctypes.c_int32),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
     ]
 
 
@@ -88,6 +120,17 @@ def load_library(path=LIB_PATH):
     lib.dsv4_topk.restype = ctypes.c_int
     lib.dsv4_topk_max_length.argtypes = [I32]
     lib.dsv4_topk_max_length.restype = I32
+    I64, PG = ctypes.c_int64, ctypes.c_void_p
+    lib.dsv4_gqa_store.argtypes = [P, I64, I64, P, I64, I64, I32, I32, P, P, PG, P, P, I64, P, P]
+    lib.dsv4_gqa_decode.argtypes = [P, I64, I32, I32, I32, P, P, PG, I32, I32, P, F32, P, P, I64, F32,
+                                    P, P, P, SZ, P]
+    lib.dsv4_gqa_evict.argtypes = [I32, P, P, P, PG, I32, I32, I32, I32, P, P, P, P, I64, P, P, SZ, P]
+    for name in ("dsv4_gqa_store", "dsv4_gqa_decode", "dsv4_gqa_evict"):
+        getattr(lib, name).restype = ctypes.c_int
+    lib.dsv4_gqa_decode_workspace_size.argtypes = [PG, I32, I32, I32, I32]
+    lib.dsv4_gqa_decode_workspace_size.restype = SZ
+    lib.dsv4_gqa_evict_workspace_size.argtypes = [PG, I32, I32, I32]
+    lib.dsv4_gqa_evict_workspace_size.restype = SZ
     return lib
 
 
@@ -290,6 +333,250 @@ def dsv4_topk(scores, lengths, k, *, max_length=None, out=None, stream=None):
     _check(lib().dsv4_topk(_ptr(scores), rows, scores.stride(0), _ptr(lengths), max_length, k, _ptr(out),
                            _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- the grouped-query cache
+_GQA_TYPES = {torch.bfloat16: DSV4_GQA_BF16, torch.float16: DSV4_GQA_F16, torch.float8_e4m3fn: DSV4_GQA_E4M3}
+
+
+def make_gqa_cache(k_pages, v_pages, page_table, *, k_scale=None, v_scale=None):
+    """dsv4_gqa_cache for K and V pools [pages, KV heads, page_size, head_dim]
+    (bf16, f16 or float8_e4m3fn; any strides whose rows are contiguous, so
+    token-major pages are passed as pages.transpose(1, 2)) and their int32
+    page table [request rows, logical pages].  k_scale, v_scale: fp32
+    [KV heads] of an e4m3 cache.  Keep the descriptor as long as the pools:
+    building it costs more than passing it."""
+    if k_pages.dim() != 4 or k_pages.dtype not in _GQA_TYPES:
+        raise Dsv4Error("k_pages must be a [pages, KV heads, page_size, head_dim] tensor of bf16, f16 or float8_e4m3fn")
+    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or v_pages.stride() != k_pages.stride():
+        raise Dsv4Error("v_pages must have the shape, type and strides of k_pages")
+    if k_pages.stride(3) != 1:
+        raise Dsv4Error("the head_dim values of a cache row must be contiguous")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise Dsv4Error("page_table must be an int32 [request rows, logical pages] tensor with contiguous rows")
+    pages, heads, page_size, dim = k_pages.shape
+    for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if x is None:
+            continue
+        if k_pages.dtype != torch.float8_e4m3fn:
+            raise Dsv4Error(f"{name} goes with a float8_e4m3fn cache")
+        if x.dtype != torch.float32 or x.shape != (heads,) or not x.is_contiguous():
+            raise Dsv4Error(f"{name} must be a contiguous fp32 tensor of {heads} entries")
+    keep = (k_pages, v_pages, page_table, k_scale, v_scale)
+    if any(x is not None and x.device != k_pages.device for x in keep):
+        raise Dsv4Error("the tensors of a cache must be on one device")
+    es = k_pages.element_size()
+    c = GqaCache()
+    c.k, c.v = k_pages.data_ptr(), v_pages.data_ptr()
+    c.num_pages = pages
+    # (a dimension of one entry may have any stride)
+    c.page_stride, c.head_stride, c.row_stride = (k_pages.stride(i) * es if k_pages.shape[i] > 1 else 0
+                                                  for i in range(3))
+    c.page_table = page_table.data_ptr()
+    c.page_table_rows, c.page_table_width = page_table.shape
+    c.page_table_stride = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+    c.num_kv_heads, c.head_dim, c.page_size = heads, dim, page_size
+    c.format = _GQA_TYPES[k_pages.dtype]
+    c.k_scale = None if k_scale is None else k_scale.data_ptr()
+    c.v_scale = None if v_scale is None else v_scale.data_ptr()
+    c._keep = keep
+    c._ref = ctypes.addressof(c)
+    c._index = k_pages.get_device()
+    c._dtype = k_pages.dtype
+    c._tracked = (c.page_table_rows, heads)
+    c._slots = page_table.shape[1] * page_size
+    c._scale = 1.0 / math.sqrt(dim)
+    return c
+
+
+def _raw(x):
+    return None if x is None else x.data_ptr()
+
+
+def _i32(name, x, n, index):
+    if x.dtype != torch.int32 or x.numel() != n or not x.is_contiguous() or x.get_device() != index:
+        raise Dsv4Error(f"{name} must be a contiguous int32 tensor of {n} entries on the cache's device")
+    return x.data_ptr()
+
+
+def _tracked(name, x, dtype, cache):
+    """[request rows, KV heads, width] contiguous: its pointer."""
+    if x.dtype != dtype or x.dim() != 3 or tuple(x.shape[:2]) != cache._tracked or not x.is_contiguous() \
+            or x.get_device() != cache._index:
+        raise Dsv4Error(f"{name} must be a contiguous {dtype} [{cache._tracked[0]}, {cache._tracked[1]}, width] tensor "
+                        "on the cache's device")
+    return x.data_ptr()
+
+
+def _raw_stream(stream, index):
+    """The stream's handle; the cache's device has to be the current one, as for every launch."""
+    if index < 0 or index != torch.cuda.current_device():
+        raise Dsv4Error("the cache must be on the current CUDA device")
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _scratch(workspace, need, cache, stream):
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=cache._keep[0].device)
+        if stream is not None:
+            workspace.record_stream(stream)     # freed here, still read there
+    elif not workspace.is_contiguous() or workspace.get_device() != cache._index:
+        raise Dsv4Error("workspace must be a contiguous tensor on the cache's device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def dsv4_gqa_store(k, v, req_rows, slots, cache, *, weights=None, positions=None, token_positions=None, stream=None):
+    """Write new rows k, v ([n, KV heads, head_dim], bf16 or f16, rows
+    contiguous) to slot slots[i] of page-table row req_rows[i] (int32 [n]
+    each), packed for an e4m3 cache.  weights (fp32 [request rows, KV heads,
+    width]) starts at 0 there, positions (int32, same shape) at
+    token_positions[i]."""
+    n = k.shape[0]
+    shape = (n, cache.num_kv_heads, cache.head_dim)
+    index = cache._index
+    if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype:
+        raise Dsv4Error("k and v must be bf16 or f16, both alike")
+    if cache._dtype not in (k.dtype, torch.float8_e4m3fn):
+        raise Dsv4Error("k and v must have the cache's type")
+    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.stride(2) != 1 or v.stride(2) != 1 \
+            or k.get_device() != index or v.get_device() != index:
+        raise Dsv4Error(f"k and v must be {list(shape)} tensors with contiguous rows on the cache's device")
+    rp, sp = _i32("req_rows", req_rows, n, index), _i32("slots", slots, n, index)
+    if (positions is None) != (token_positions is None):
+        raise Dsv4Error("positions and token_positions go together")
+    wp = pp = tp = None
+    width = 0
+    if weights is not None:
+        wp, width = _tracked("weights", weights, torch.float32, cache), weights.shape[2]
+    if positions is not None:
+        pp, tp = _tracked("positions", positions, torch.int32, cache), _i32("token_positions", token_positions, n, index)
+        if weights is not None and positions.shape[2] != width:
+            raise Dsv4Error("weights and positions must have one width")
+        width = positions.shape[2]
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    if n <= 1 or shape[1] == 1:         # a dimension of one entry may have any stride
+        kt, vt = (0, 0) if n <= 1 else (kt, vt)
+        kh, vh = (0, 0) if shape[1] == 1 else (kh, vh)
+    rc = lib().dsv4_gqa_store(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _GQA_TYPES[k.dtype], n, rp, sp, cache._ref,
+                              wp, pp, width, tp, _raw_stream(stream, index))
+    if rc:
+        _check(rc)
+
+
+def dsv4_gqa_decode_workspace_size(cache, batch, num_heads, max_len=None, weights=False):
+    return lib().dsv4_gqa_decode_workspace_size(cache._ref, batch, num_heads,
+                                                cache._slots if max_len is None else max_len, int(weights))
+
+
+def dsv4_gqa_decode(q, lens, cache, *, sink=None, scale=None, window=0, max_len=None, req_pool_indices=None,
+                    weights=None, weights_out=None, decay=1.0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token per request over its cached rows: q
+    [batch, heads, head_dim] (bf16 or f16; a slice of a wider projection is
+    fine), lens int32 [batch].  Returns (out, lse).  With weights (fp32
+    [request rows, KV heads, width]) every cached row's weight is accumulated
+    into weights_out, by default in place."""
+    if q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16) or q.get_device() != cache._index:
+        raise Dsv4Error("q must be a bf16 or f16 [batch, heads, head_dim] tensor on the cache's device")
+    batch, heads, dim = q.shape
+    if cache._dtype not in (q.dtype, torch.float8_e4m3fn):
+        raise Dsv4Error("q must have the cache's type")
+    if dim != cache.head_dim or q.stride(2) != 1 or (heads > 1 and q.stride(1) != dim):
+        raise Dsv4Error(f"q's rows must be heads of {cache.head_dim} contiguous values, one behind the other")
+    index = cache._index
+    lp = _i32("lens", lens, batch, index)
+    rp = None if req_pool_indices is None else _i32("req_pool_indices", req_pool_indices, batch, index)
+    if rp is None and batch > cache.page_table_rows:
+        raise Dsv4Error("without req_pool_indices the page table needs a row for every request")
+    if sink is not None and (sink.dtype != torch.float32 or sink.numel() != heads or not sink.is_contiguous()
+                             or sink.get_device() != index):
+        raise Dsv4Error(f"sink must be a contiguous fp32 tensor of {heads} entries on the cache's device")
+    if max_len is None:
+        max_len = cache._slots
+    wp = op = None
+    width = 0
+    if weights is not None:
+        wp, width = _tracked("weights", weights, torch.float32, cache), weights.shape[2]
+        op = wp
+        if weights_out is not None:
+            op = _tracked("weights_out", weights_out, torch.float32, cache)
+            if weights_out.shape[2] != width:
+                raise Dsv4Error("weights and weights_out must have one width")
+        if max_len > width:
+            raise Dsv4Error("weights must be at least max_len wide")
+    elif weights_out is not None:
+        raise Dsv4Error("weights_out goes with weights")
+    if out is None:
+        out = torch.empty(batch, heads, dim, dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.get_device() != index:
+        raise Dsv4Error("out must be a contiguous tensor like q")
+    if lse is None:
+        lse = torch.empty(batch, heads, dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or lse.numel() != batch * heads or not lse.is_contiguous() \
+            or lse.get_device() != index:
+        raise Dsv4Error("lse must be a contiguous fp32 [batch, heads] tensor on the cache's device")
+    if batch == 0:
+        return out, lse
+    need = 0 if workspace is not None else dsv4_gqa_decode_workspace_size(cache, batch, heads, max_len, wp is not None)
+    workspace, have = _scratch(workspace, need, cache, stream)
+    rc = lib().dsv4_gqa_decode(q.data_ptr(), q.stride(0) if batch > 1 else heads * dim, _GQA_TYPES[q.dtype], batch,
+                               heads, lp, rp, cache._ref, window, max_len, _raw(sink),
+                               cache._scale if scale is None else scale, wp, op, width, decay, out.data_ptr(),
+                               lse.data_ptr(), workspace.data_ptr(), have, _raw_stream(stream, index))
+    if rc:
+        _check(rc)
+    return out, lse
+
+
+def dsv4_gqa_evict_workspace_size(cache, batch, max_len, keep):
+    return lib().dsv4_gqa_evict_workspace_size(cache._ref, batch, cache._slots if max_len is None else max_len, keep)
+
+
+def dsv4_gqa_evict(lens, cache, weights, keep, *, seq_lens=None, positions=None, first=0, recent=0,
+                   req_pool_indices=None, max_len=None, weights_out=None, positions_out=None, lens_out=None,
+                   workspace=None, stream=None):
+    """Cut every request with more than `keep` cached rows (lens int32
+    [batch]) to the `keep` that matter per KV head: positions below `first`,
+    the `recent` newest of seq_lens tokens, then the largest weights.  Rows
+    that stay but stand behind the bound move into the freed slots, with their
+    weights and positions (in place unless weights_out / positions_out are
+    given).  Returns lens_out (a new tensor unless given; may be lens)."""
+    batch = lens.numel()
+    index = cache._index
+    lp = _i32("lens", lens, batch, index)
+    np_ = None if seq_lens is None else _i32("seq_lens", seq_lens, batch, index)
+    rp = None if req_pool_indices is None else _i32("req_pool_indices", req_pool_indices, batch, index)
+    if rp is None and batch > cache.page_table_rows:
+        raise Dsv4Error("without req_pool_indices the page table needs a row for every request")
+    wp, width = _tracked("weights", weights, torch.float32, cache), weights.shape[2]
+    op = wp
+    if weights_out is not None:
+        op = _tracked("weights_out", weights_out, torch.float32, cache)
+    pp = qp = None
+    if positions is not None:
+        pp = qp = _tracked("positions", positions, torch.int32, cache)
+        if positions_out is not None:
+            qp = _tracked("positions_out", positions_out, torch.int32, cache)
+    elif positions_out is not None:
+        raise Dsv4Error("positions_out goes with positions")
+    if any(x is not None and x.shape[2] != width for x in (weights_out, positions, positions_out)):
+        raise Dsv4Error("weights and positions must have one width")
+    if max_len is None:
+        max_len = min(cache._slots, width)
+    if max_len > width:
+        raise Dsv4Error("weights must be at least max_len wide")
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+    ep = _i32("lens_out", lens_out, batch, index)
+    if batch == 0:
+        return lens_out
+    need = 0 if workspace is not None else dsv4_gqa_evict_workspace_size(cache, batch, max_len, keep)
+    workspace, have = _scratch(workspace, need, cache, stream)
+    rc = lib().dsv4_gqa_evict(batch, lp, np_, rp, cache._ref, max_len, keep, first, recent, wp, op, pp, qp, width, ep,
+                              workspace.data_ptr(), have, _raw_stream(stream, index))
+    if rc:
+        _check(rc)
+    return lens_out
 
 
 def run_inputs(inp, *, num_splits=0, debug_rows=None, out=None, lse=None, workspace=None, stream=None):

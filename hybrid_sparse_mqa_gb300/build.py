@@ -11,11 +11,13 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", "dsv4_attn.cu"), os.path.join(PKG, "csrc", "dsv4_kv_store.cu"),
-           os.path.join(PKG, "csrc", "dsv4_topk.cu")]
+SOURCES = [os.path.join(PKG, "csrc", name) for name in (
+    "dsv4_attn.cu", "dsv4_kv_store.cu", "dsv4_topk.cu", "dsv4_gqa_store.cu", "dsv4_gqa_decode.cu",
+    "dsv4_gqa_decode_bf16.cu", "dsv4_gqa_decode_f16.cu", "dsv4_gqa_decode_e4m3.cu", "dsv4_gqa_evict.cu")]
 DEPS = SOURCES + [os.path.join(PKG, "csrc", "dsv4_device.cuh"), os.path.join(PKG, "csrc", "dsv4_internal.h"),
                   os.path.join(ROOT, "include", "dsv4attn.h"), os.path.join(ROOT, "include", "dsv4kvstore.h"),
-                  os.path.join(ROOT, "include", "dsv4topk.h")]
+                  os.path.join(ROOT, "include", "dsv4topk.h"), os.path.join(ROOT, "include", "dsv4gqa.h"),
+                  os.path.join(PKG, "csrc", "dsv4_gqa.cuh"), os.path.join(PKG, "csrc", "dsv4_gqa_decode.cuh")]
 LIB = os.path.join(PKG, "libdsv4attn.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
@@ -39,7 +41,7 @@ def build(force=False, verbose=False):
     if not force and not needs_build():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xptxas", "-v",
+    cmd = [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xptxas", "-v", "--threads", "0",
            "-I", os.path.join(ROOT, "include"), "-Xcompiler", "-fPIC", "-shared",
            *SOURCES, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,742 @@
+// dsv4_gqa_decode.cuh - one-token attention over a paged grouped-query cache
+// (include/dsv4gqa.h states what is computed).  The kernel is a template over
+// the cache's element type, compiled once per type in
+// dsv4_gqa_decode_{bf16,f16,e4m3}.cu; dsv4_gqa_decode.cu holds the host side
+// and the kernels that join split requests and accumulate weights.
+//
+// Work: a segment is one (request, KV head, group of up to 8 NT query heads);
+// its key range is cut into tiles of TT slots.  All tiles of the batch form
+// one list, of which every CTA takes an equal contiguous share, so a ragged
+// batch is as balanced as a uniform one and a long request is split over as
+// many CTAs as it needs.  A segment that lies in one CTA's share is finished
+// there; of a cut one every CTA leaves (unnormalised output, maximum, sum) in
+// fp32 in the workspace, at most two pieces per CTA, which the join kernel
+// merges.
+//
+// In a CTA, warp w takes tiles w, w + W, ... of a piece, each through its own
+// ring of cp.async stages (no block barrier in the loop; the ring runs ahead
+// over piece boundaries).  Scores are computed transposed, S^T = K Q^T, so
+// the 16 rows of an m16n8k16 MMA are slots and its 8 columns query heads: a
+// group of 8 heads wastes nothing.  The exponentials become the B operand of
+// O^T = V^T P^T by one 8x8 transposition in registers (movmatrix).  The
+// softmax is online with a lazy reference: a tile's scores are compared with
+// the running reference by one vote, and the reference moves (and O and the
+// sums are rescaled) only when some score exceeds it by more than 2^8.
+//
+// Precision: scores, references, sums, O and the merge are fp32.  For 16-bit
+// caches P enters the MMA as the sum of two 16-bit values (the rounded value
+// and the rounded rest), so its rounding stays below 2^-16 and the output's
+// own rounding is what remains; the second MMA costs nothing measurable in a
+// kernel bound by memory.  For e4m3 caches codes are exact in f16 and P is
+// one f16 (2^-11 relative, below the output's bf16 2^-8 or equal to its f16
+// step); q is scaled by a power of two per head so that its largest value
+// lies in [2^14, 2^15), which keeps every bf16 value down to 2^-39 of it.
+#pragma once
+
+#include "dsv4_gqa.cuh"
+
+namespace dsv4 {
+namespace gqa {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -1e30f;           // reference of a head that has seen no score
+constexpr int kMaxCtas = 304;              // shares that the tile list is cut into, at most (two per SM)
+
+struct DecodeParams {
+    Cache c;
+    const void* q;
+    long long q_stride;                    // elements
+    int q_bf16;                            // q and out: bf16 (else f16)
+    int batch, heads, group, chunks;       // group: query heads per KV head; chunks of 8 NT heads each
+    const int* lens;
+    const int* req;
+    int window, max_len;
+    const float* sink;
+    float scale_log2;                      // scale * log2 e
+    void* out;
+    float* lse;
+    // workspace
+    float* part_o;                         // [2 kMaxCtas][8 NT][D]
+    float2* part_ml;                       // [2 kMaxCtas][8 NT]
+    float* lse2;                           // [batch][heads], log2 units (with weights)
+    int4* info;                            // [batch] (with weights): first tile, next request of the same row or
+                                           // -1, whether it is the row's first, rows
+    float* logits;                         // [tiles][TT][8 NT], log2 units (with weights), or null
+    // weights
+    const float* w_in;
+    float* w_out;
+    long long width;
+    float decay;
+    int min_tiles;                         // a CTA takes at least this many tiles
+    int ctas;                              // the decode grid
+    unsigned int* err;
+};
+
+// The slots lo .. n-1 that a request attends and the tiles of TT slots that
+// they touch.
+struct Range {
+    int lo, n, tiles;
+};
+template <int TT>
+__device__ __forceinline__ Range key_range(const DecodeParams& p, int n) {
+    Range r;
+    r.n = n;
+    r.lo = p.window > 0 && n > p.window ? n - p.window : 0;
+    r.tiles = n > 0 ? (n - 1) / TT - r.lo / TT + 1 : 0;
+    return r;
+}
+
+// How many CTAs share `total` tiles, and where share i begins.
+__device__ __forceinline__ int share_count(const DecodeParams& p, unsigned total) {
+    const unsigned most = total / p.min_tiles;
+    return most < 1u ? 1 : (most > (unsigned)p.ctas ? p.ctas : (int)most);
+}
+__device__ __forceinline__ unsigned share_begin(unsigned total, int ctas, int i) {
+    return static_cast<unsigned>(static_cast<unsigned long long>(total) * i / ctas);
+}
+// The share that tile t lies in.
+__device__ __forceinline__ int share_of(unsigned total, int ctas, unsigned t) {
+    int i = static_cast<int>(static_cast<unsigned long long>(t) * ctas / total);
+    while (i + 1 < ctas && share_begin(total, ctas, i + 1) <= t) ++i;
+    while (i > 0 && share_begin(total, ctas, i) > t) --i;
+    return i;
+}
+
+// ---------------------------------------------------------------- PTX
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes (low 16 bits) -> two f16 values, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(r) : "r"(codes));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_hi_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, hi;\n}\n" : "=r"(r) : "r"(codes));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
+        return pack_bf16x2(lo, hi);
+    } else {
+        __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<uint32_t*>(&v);
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (BF16)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// ---------------------------------------------------------------- shape
+// KIND: DSV4_GQA_BF16 / F16 / E4M3.  A warp's stage is TT rows of K and of V.
+template <int KIND_, int D_, int NT_>
+struct Shape {
+    static constexpr int KIND = KIND_, D = D_, NT = NT_;
+    static constexpr bool FP8 = KIND == DSV4_GQA_E4M3;
+    static constexpr bool BF16 = KIND == DSV4_GQA_BF16;      // operand type of the MMAs (e4m3: f16)
+    static constexpr int ROWB = D * (FP8 ? 1 : 2);           // bytes of a row
+    static constexpr int TT = 4096 / ROWB < 16 ? 16 : 4096 / ROWB;
+    static constexpr int MT = TT / 16;                       // 16-slot MMA tiles
+    static constexpr int DT = D / 16;                        // 16-dim tiles
+    static constexpr int HEADS = 8 * NT;                     // query heads of a segment (padded)
+    static constexpr int W = 4;                              // warps per CTA
+    static constexpr int TILE_BYTES = TT * ROWB;             // K or V of a stage
+    static constexpr int STAGES = TILE_BYTES > 4096 ? 1 : 3;
+    static constexpr int RING_BYTES = W * STAGES * 2 * TILE_BYTES;
+    static constexpr int MERGE_STRIDE = D + 4;               // floats per head of a merge row (bank spread)
+    static constexpr int MERGE_BYTES = W * 8 * MERGE_STRIDE * 4;
+    static constexpr int SMEM = RING_BYTES + MERGE_BYTES;
+    static constexpr int PPR = ROWB / 16;                    // 16-byte pieces per row
+    static constexpr int RPI = 32 / PPR;                     // rows per warp-wide copy
+};
+
+// Byte offset of 16-byte piece `piece` of row `row` in a K (V) tile.  The
+// swizzles spread what one phase of the readers' loads touches over all
+// banks: ldmatrix reads 8 rows of one piece; the e4m3 readers read rows
+// (g, g + 1) x pieces 4j .. 4j + 3 of K and rows 2t (t = 0..3) x two
+// neighbouring pieces of V.
+template <class S>
+__device__ __forceinline__ uint32_t k_offset(int row, int piece) {
+    if constexpr (!S::FP8) return row * S::ROWB + ((piece ^ (row & 7)) << 4);
+    if constexpr (S::ROWB == 64) return row * 64 + (piece << 4);
+    return row * S::ROWB + ((piece ^ ((row & 1) << 2)) << 4);
+}
+template <class S>
+__device__ __forceinline__ uint32_t v_offset(int row, int piece) {
+    if constexpr (!S::FP8) return row * S::ROWB + ((piece ^ (row & 7)) << 4);
+    const int f = ((row >> 1) & 3) << 1;
+    if constexpr (S::ROWB == 64) return (row >> 1) * 128 + (((((row & 1) << 2) | piece) ^ f) << 4);
+    return row * S::ROWB + ((piece ^ f) << 4);
+}
+
+// ---------------------------------------------------------------- the walk over tiles
+// A position in a CTA's share of the tile list.  Every warp has two: one that
+// runs ahead issuing copies and one that follows computing.
+template <int TT>
+struct Cursor {
+    int b, hc;                 // request; KV head * chunks + chunk
+    Request rq;
+    Range rg;
+    unsigned seg;              // list index of the segment's first tile
+    unsigned end;              // end of the current piece
+    unsigned begin;            // begin of the current piece
+
+    __device__ __forceinline__ void load(const DecodeParams& p) {
+        unsigned ignored = 0;
+        rq = read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, ignored);
+        rg = key_range<TT>(p, rq.n);
+    }
+    __device__ __forceinline__ void bound(unsigned t1) {
+        end = seg + rg.tiles < t1 ? seg + rg.tiles : t1;
+    }
+    // to the next segment that has tiles; false at the end of the share
+    __device__ __forceinline__ bool next_piece(const DecodeParams& p, int hcs, unsigned t1) {
+        if (end >= t1) return false;
+        seg = begin = end;
+        if (++hc == hcs) {
+            hc = 0;
+            do {
+                if (++b >= p.batch) return false;
+                load(p);
+            } while (rg.tiles == 0);
+        }
+        bound(t1);
+        return true;
+    }
+};
+
+template <class S>
+__global__ void __launch_bounds__(S::W * 32, 2) dsv4_gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
+    constexpr int D = S::D, NT = S::NT, W = S::W, TT = S::TT, MT = S::MT, DT = S::DT, HEADS = S::HEADS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float2 s_ml[W][HEADS];
+    __shared__ unsigned s_scan[W + 1];
+    __shared__ unsigned s_seg;                    // where the share begins: list index of the request's first tile
+    __shared__ int s_b;
+    __shared__ int s_ok[W][S::STAGES];            // a bit per 16-slot group: its page is in the pool
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int hcs = p.c.kv_heads * p.chunks;
+    grid_dependency_wait();
+    grid_dependents_go();
+
+    // ---- total tiles, and the request that this share begins in ----
+    unsigned err = 0, total = 0, mine0 = 0, cnt0 = 0;
+    const int rounds = (p.batch + W * 32 - 1) / (W * 32);
+    for (int k = 0; k < rounds; ++k) {
+        const int b = k * W * 32 + tid;
+        unsigned cnt = 0;
+        if (b < p.batch)
+            cnt = key_range<TT>(p, read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, err).n).tiles * hcs;
+        unsigned incl = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        unsigned base = total;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) base += s_scan[w];
+            total += s_scan[w];
+        }
+        mine0 = base + incl - cnt;
+        cnt0 = cnt;
+        __syncthreads();
+    }
+    if (err && blockIdx.x == 0) atomicOr(p.err, err);
+    const int ctas = share_count(p, total);
+    if ((int)blockIdx.x >= ctas || total == 0) return;
+    const unsigned t0 = share_begin(total, ctas, blockIdx.x), t1 = share_begin(total, ctas, blockIdx.x + 1);
+    if (t0 >= t1) return;
+    if (rounds == 1) {
+        if (t0 >= mine0 && t0 < mine0 + cnt0) {
+            s_b = tid;
+            s_seg = mine0;
+        }
+    } else {
+        unsigned run = 0;
+        for (int k = 0; k < rounds; ++k) {
+            const int b = k * W * 32 + tid;
+            unsigned cnt = 0;
+            if (b < p.batch)
+                cnt = key_range<TT>(p, read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, err).n).tiles * hcs;
+            unsigned incl = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (lane == 31) s_scan[warp] = incl;
+            __syncthreads();
+            unsigned base = run;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                if (w < warp) base += s_scan[w];
+                run += s_scan[w];
+            }
+            if (t0 >= base + incl - cnt && t0 < base + incl) {
+                s_b = b;
+                s_seg = base + incl - cnt;
+            }
+            __syncthreads();
+            if (run > t0) break;
+        }
+    }
+    __syncthreads();
+
+    Cursor<TT> cons;
+    cons.b = s_b;
+    cons.load(p);
+    cons.hc = static_cast<int>((t0 - s_seg) / cons.rg.tiles);
+    cons.seg = s_seg + cons.hc * cons.rg.tiles;
+    cons.begin = t0;
+    cons.bound(t1);
+
+    // ---- the copying side ----
+    const uint32_t ring = smem_u32(smem) + warp * (S::STAGES * 2 * S::TILE_BYTES);
+    const int lane_row = lane / S::PPR, lane_piece = lane % S::PPR;
+    const long long lane_off = lane_row * p.c.row_stride + lane_piece * 16;
+    const int page_mask = (1 << p.c.page_shift) - 1;
+    Cursor<TT> prod = cons;
+    unsigned ptile = prod.begin + warp;
+    bool more = true;
+    int page = -1;                                 // lane m < MT: page of 16-slot group m of the next tile
+    bool wanted = false;                           // that group holds slots to attend
+
+    // to the warp's next tile; loads its page ids one tile ahead of their use
+    auto settle = [&]() {
+        while (more && ptile >= prod.end) {
+            more = prod.next_piece(p, hcs, t1);
+            ptile = prod.begin + warp;
+        }
+        page = -1;
+        wanted = false;
+        if (more && lane < MT) {
+            const int slot = (prod.rg.lo / TT + static_cast<int>(ptile - prod.seg)) * TT + lane * 16;
+            wanted = slot < prod.rg.n && slot + 16 > prod.rg.lo;
+            if (wanted) page = __ldg(p.c.table + (long long)prod.rq.row * p.c.table_stride + (slot >> p.c.page_shift));
+        }
+    };
+    auto issue = [&](int stage) {
+        if (more) {
+            const int slot0 = (prod.rg.lo / TT + static_cast<int>(ptile - prod.seg)) * TT;
+            const bool ok = page >= 0 && page < p.c.num_pages;
+            if (wanted && !ok) atomicOr(p.err, DSV4_DEV_ERR_GQA_PAGE);
+            const unsigned okm = __ballot_sync(0xffffffffu, ok);
+            if (lane == 0) s_ok[warp][stage] = okm;
+            const long long head = (prod.hc / p.chunks) * p.c.head_stride + lane_off;
+            const uint32_t kd = ring + stage * 2 * S::TILE_BYTES, vd = kd + S::TILE_BYTES;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int pg = __shfl_sync(0xffffffffu, page, m);
+                const bool have = (okm >> m) & 1;
+                const int s = slot0 + m * 16;
+                const long long base =
+                    have ? pg * p.c.page_stride + (s & page_mask) * p.c.row_stride + head : 0;
+#pragma unroll
+                for (int i = 0; i < 16 / S::RPI; ++i) {
+                    const int r = i * S::RPI + lane_row;        // row in the group
+                    const bool in = have && s + r < prod.rg.n && s + r >= prod.rg.lo;
+                    const long long off = in ? base + i * S::RPI * p.c.row_stride : 0;
+                    cp_async_16(kd + k_offset<S>(m * 16 + r, lane_piece), p.c.k + off, in ? 16u : 0u);
+                    cp_async_16(vd + v_offset<S>(m * 16 + r, lane_piece), p.c.v + off, in ? 16u : 0u);
+                }
+            }
+            ptile += W;
+            settle();
+        }
+        cp_async_commit();
+    };
+
+    settle();
+#pragma unroll
+    for (int s = 0; s < S::STAGES; ++s) issue(s);
+
+    // ---- the computing side ----
+    int stage = 0;
+    float* merge = reinterpret_cast<float*>(smem + S::RING_BYTES);
+    for (bool on = true; on; on = cons.next_piece(p, hcs, t1)) {
+        const int h = cons.hc / p.chunks, chunk = cons.hc % p.chunks;
+        const int head0 = h * p.group + chunk * HEADS;
+        const int nheads = min(HEADS, p.group - chunk * HEADS);
+        // q as the B operand; head g of n-tile nt
+        uint32_t qf[DT][NT][2];
+        float smul[NT][2];                         // score factor of the two heads whose columns this thread holds
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const bool have = nt * 8 + g < nheads;
+            const uint32_t* qr = reinterpret_cast<const uint32_t*>(
+                static_cast<const uint16_t*>(p.q) + cons.b * p.q_stride + (long long)(head0 + nt * 8 + g) * D);
+            if constexpr (!S::FP8) {
+#pragma unroll
+                for (int kk = 0; kk < DT; ++kk) {
+                    qf[kk][nt][0] = have ? __ldg(qr + kk * 8 + t4) : 0u;
+                    qf[kk][nt][1] = have ? __ldg(qr + kk * 8 + t4 + 4) : 0u;
+                }
+                smul[nt][0] = smul[nt][1] = p.scale_log2;
+            } else {
+                // MMA kk = 4 j + i takes dims 16 (t + 4 j) + 4 i .. + 3 from the thread with that t
+                float amax = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < DT; ++kk) {
+                    const int d2 = (16 * (t4 + 4 * (kk >> 2)) + 4 * (kk & 3)) / 2;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        qf[kk][nt][u] = have ? __ldg(qr + d2 + u) : 0u;
+                        const float2 f = p.q_bf16 ? unpack2<true>(qf[kk][nt][u]) : unpack2<false>(qf[kk][nt][u]);
+                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // 2^e with amax 2^e in [2^14, 2^15); exponents kept where 2^-e and 2^e are normal
+                int e = 14 - (static_cast<int>((__float_as_uint(amax) >> 23) & 255u) - 127);
+                e = amax == 0.f || !(amax < INFINITY) ? 0 : (e > 120 ? 120 : (e < -120 ? -120 : e));
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+                for (int kk = 0; kk < DT; ++kk)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float2 f = p.q_bf16 ? unpack2<true>(qf[kk][nt][u]) : unpack2<false>(qf[kk][nt][u]);
+                        qf[kk][nt][u] = pack2<false>(f.x * up, f.y * up);
+                    }
+                const float mul = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.f) * down;
+                smul[nt][0] = __shfl_sync(0xffffffffu, mul, 8 * t4);
+                smul[nt][1] = __shfl_sync(0xffffffffu, mul, 8 * t4 + 4);
+            }
+        }
+        float o[DT][NT][4], mref[NT][2], lsum[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mref[nt][0] = mref[nt][1] = kNoMax;
+            lsum[nt][0] = lsum[nt][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < DT; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[j][nt][c] = 0.f;
+        }
+
+        for (unsigned tile = cons.begin + warp; tile < cons.end; tile += W) {
+            cp_async_wait_group<S::STAGES - 1>();
+            __syncwarp();
+            const uint32_t ks = ring + stage * 2 * S::TILE_BYTES, vs = ks + S::TILE_BYTES;
+            const unsigned okm = s_ok[warp][stage];
+            const int slot0 = (cons.rg.lo / TT + static_cast<int>(tile - cons.seg)) * TT;
+
+            // S^T = K Q^T
+            float s[MT][NT][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[m][nt][c] = 0.f;
+            if constexpr (!S::FP8) {
+                const int mrow = lane & 15, mpiece = lane >> 4;
+#pragma unroll
+                for (int kk = 0; kk < DT; ++kk)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        uint32_t a[4];
+                        ldsm4(a, ks + k_offset<S>(m * 16 + mrow, 2 * kk + mpiece));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816<S::BF16>(s[m][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+                    }
+            } else {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < D / 64; ++j) {
+                        const uint4 x = ld_shared_u4(ks + k_offset<S>(m * 16 + g, t4 + 4 * j));
+                        const uint4 y = ld_shared_u4(ks + k_offset<S>(m * 16 + g + 8, t4 + 4 * j));
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a[4] = {e4m3x2_f16x2(xs[i]), e4m3x2_f16x2(ys[i]), e4m3x2_hi_f16x2(xs[i]),
+                                                   e4m3x2_hi_f16x2(ys[i])};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<false>(s[m][nt], a, qf[4 * j + i][nt][0], qf[4 * j + i][nt][1]);
+                        }
+                    }
+            }
+
+            // log2-unit scores, masked; the vote on the reference
+            const bool whole = slot0 >= cons.rg.lo && slot0 + TT <= cons.rg.n && okm == (1u << MT) - 1u;
+            bool above = false;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float x = s[m][nt][c] * smul[nt][c & 1];
+                        if (!whole) {
+                            const int slot = slot0 + m * 16 + g + (c >> 1) * 8;
+                            if (slot < cons.rg.lo || slot >= cons.rg.n || !((okm >> m) & 1)) x = -INFINITY;
+                        }
+                        s[m][nt][c] = x;
+                        above |= x > mref[nt][c & 1] + 8.f;
+                    }
+            if (p.logits) {
+                float* to = p.logits + (size_t)tile * TT * HEADS;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            *reinterpret_cast<float2*>(to + (m * 16 + g + 8 * u) * HEADS + nt * 8 + 2 * t4) =
+                                make_float2(s[m][nt][2 * u], s[m][nt][2 * u + 1]);
+            }
+            if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float mx = mref[nt][u];
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) mx = fmaxf(mx, fmaxf(s[m][nt][u], s[m][nt][u + 2]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float f = fast_exp2(mref[nt][u] - mx);
+                        mref[nt][u] = mx;
+                        lsum[nt][u] *= f;
+#pragma unroll
+                        for (int j = 0; j < DT; ++j) {
+                            o[j][nt][u] *= f;
+                            o[j][nt][u + 2] *= f;
+                        }
+                    }
+            }
+
+            // P^T and O^T += V^T P^T
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float x = fast_exp2(s[m][nt][2 * u] - mref[nt][0]);
+                        const float y = fast_exp2(s[m][nt][2 * u + 1] - mref[nt][1]);
+                        lsum[nt][0] += x;
+                        lsum[nt][1] += y;
+                        const uint32_t w = pack2<S::BF16>(x, y);
+                        hi[nt][u] = transpose8x8(w);
+                        if constexpr (!S::FP8) {
+                            const float2 r = unpack2<S::BF16>(w);
+                            lo[nt][u] = transpose8x8(pack2<S::BF16>(x - r.x, y - r.y));
+                        }
+                    }
+                if constexpr (!S::FP8) {
+                    const int mrow = (lane & 7) + ((lane >> 4) << 3), mpiece = (lane >> 3) & 1;
+#pragma unroll
+                    for (int j = 0; j < DT; ++j) {
+                        uint32_t a[4];
+                        ldsm4_trans(a, vs + v_offset<S>(m * 16 + mrow, 2 * j + mpiece));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<S::BF16>(o[j][nt], a, hi[nt][0], hi[nt][1]);
+                            mma16816<S::BF16>(o[j][nt], a, lo[nt][0], lo[nt][1]);
+                        }
+                    }
+                } else {
+                    // slots 2t, 2t + 1, 2t + 8, 2t + 9; tile j's rows g and g + 8 are the two
+                    // neighbouring dims dim_of(j, g): words of four dims, slot pairs byte-interleaved
+                    constexpr int WORDS = D == 64 ? 2 : 4;       // 32-bit words per thread, slot and half
+#pragma unroll
+                    for (int hh = 0; hh < (D == 256 ? 2 : 1); ++hh) {
+                        uint32_t v[4][WORDS];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int row = m * 16 + 2 * t4 + (u & 1) + (u >> 1) * 8;
+                            if constexpr (D == 64) {
+                                const uint32_t at = vs + v_offset<S>(row, g >> 1) + (g & 1) * 8;
+                                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                             : "=r"(v[u][0]), "=r"(v[u][1])
+                                             : "r"(at)
+                                             : "memory");
+                            } else {
+                                const uint4 x = ld_shared_u4(vs + v_offset<S>(row, g + 8 * hh));
+                                v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+                            }
+                        }
+#pragma unroll
+                        for (int jj = 0; jj < 2 * WORDS; ++jj) {
+                            const uint32_t sel = jj & 1 ? 0x7362u : 0x5140u;
+                            const uint32_t x = __byte_perm(v[0][jj >> 1], v[1][jj >> 1], sel);
+                            const uint32_t y = __byte_perm(v[2][jj >> 1], v[3][jj >> 1], sel);
+                            const uint32_t a[4] = {e4m3x2_f16x2(x), e4m3x2_hi_f16x2(x), e4m3x2_f16x2(y),
+                                                   e4m3x2_hi_f16x2(y)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<false>(o[hh * 8 + jj][nt], a, hi[nt][0], hi[nt][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            issue(stage);
+            stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+        }
+
+        // ---- merge the warps: sums and references, then O in rounds of 8 heads ----
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float l = lsum[nt][u];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                if (g == 0) s_ml[warp][nt * 8 + 2 * t4 + u] = make_float2(mref[nt][u], l);
+            }
+        __syncthreads();
+        const bool split = cons.begin != cons.seg || cons.end != cons.seg + cons.rg.tiles;
+        const int slot = 2 * blockIdx.x + (cons.begin == cons.seg ? 1 : 0);
+        const float vmul = S::FP8 && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int c = nt * 8 + 2 * t4 + u;
+                float mx = kNoMax;
+#pragma unroll
+                for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_ml[w][c].x);
+                const float f = fast_exp2(mref[nt][u] - mx);
+                float* to = merge + (warp * 8 + 2 * t4 + u) * S::MERGE_STRIDE;
+#pragma unroll
+                for (int j = 0; j < DT; ++j) {
+                    if constexpr (!S::FP8) {
+                        to[16 * j + g] = o[j][nt][u] * f;
+                        to[16 * j + 8 + g] = o[j][nt][u + 2] * f;
+                    } else {
+                        const int d = D == 64 ? 8 * g + 2 * j : 16 * (g + 8 * (j >> 3)) + 2 * (j & 7);
+                        *reinterpret_cast<float2*>(to + d) = make_float2(o[j][nt][u] * f, o[j][nt][u + 2] * f);
+                    }
+                }
+            }
+            __syncthreads();
+            for (int e = tid; e < 8 * D / 4; e += W * 32) {
+                const int c = nt * 8 + e / (D / 4), d = (e % (D / 4)) * 4;
+                if (c >= nheads) continue;
+                float mx = kNoMax, l = 0.f;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_ml[w][c].x);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    l += s_ml[w][c].y * fast_exp2(s_ml[w][c].x - mx);
+                    const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + (c & 7)) * S::MERGE_STRIDE + d);
+                    a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+                }
+                if (split) {
+                    *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * HEADS + c) * D + d) = a;
+                    if (d == 0) p.part_ml[slot * HEADS + c] = make_float2(mx, l);
+                    continue;
+                }
+                const int head = head0 + c;
+                const float sk = p.sink ? __ldg(p.sink + head) * kLog2e : -INFINITY;
+                const float top = fmaxf(mx, sk);
+                const float f = fast_exp2(mx - top);
+                l = l * f + fast_exp2(sk - top);
+                const float inv = l > 0.f || l != l ? vmul * f / l : 0.f;
+                const size_t at = ((size_t)cons.b * p.heads + head) * D + d;
+                const uint2 w2 = p.q_bf16 ? make_uint2(pack2<true>(a.x * inv, a.y * inv), pack2<true>(a.z * inv, a.w * inv))
+                                          : make_uint2(pack2<false>(a.x * inv, a.y * inv), pack2<false>(a.z * inv, a.w * inv));
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w2;
+                if (d == 0) {
+                    const float l2 = l > 0.f || l != l ? top + log2f(l) : -INFINITY;
+                    if (p.lse) p.lse[(size_t)cons.b * p.heads + head] = l2 * kLn2;
+                    if (p.lse2) p.lse2[(size_t)cons.b * p.heads + head] = l2;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// The host side of one cache type.
+int launch_decode_bf16(const DecodeParams& p, int head_dim, int nt, void* stream);
+int launch_decode_f16(const DecodeParams& p, int head_dim, int nt, void* stream);
+int launch_decode_e4m3(const DecodeParams& p, int head_dim, int nt, void* stream);
+
+template <class S>
+inline int launch_decode_shape(const DecodeParams& p, void* stream) {
+    // shared memory beyond 48 KB is asked for once per device
+    static unsigned long long ready = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DSV4_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return DSV4_ERR_CUDA;
+    if (!(__atomic_load_n(&ready, __ATOMIC_ACQUIRE) >> dev & 1)) {
+        if (cudaFuncSetAttribute(dsv4_gqa_decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return DSV4_ERR_CUDA;
+        }
+        __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELEASE);
+    }
+    return launch(dsv4_gqa_decode_kernel<S>, dim3(p.ctas), S::W * 32, S::SMEM, stream, 1, p);
+}
+
+template <int KIND>
+inline int launch_decode_kind(const DecodeParams& p, int head_dim, int nt, void* stream) {
+    if (nt == 1) {
+        if (head_dim == 64) return launch_decode_shape<Shape<KIND, 64, 1>>(p, stream);
+        if (head_dim == 128) return launch_decode_shape<Shape<KIND, 128, 1>>(p, stream);
+        return launch_decode_shape<Shape<KIND, 256, 1>>(p, stream);
+    }
+    if (head_dim == 64) return launch_decode_shape<Shape<KIND, 64, 2>>(p, stream);
+    if (head_dim == 128) return launch_decode_shape<Shape<KIND, 128, 2>>(p, stream);
+    return launch_decode_shape<Shape<KIND, 256, 2>>(p, stream);
+}
+
+}  // namespace gqa
+}  // namespace dsv4
