@@ -11,22 +11,28 @@ namespace {
 constexpr int kJoinThreads = 256;
 constexpr int kWeightThreads = 256;
 constexpr int kWeightSlots = 4;            // slots per thread
+constexpr int kMinTiles = 2;               // per share: below, more warps would not shorten the chain of loads
 
-// Joins the pieces of split segments: block (segment, n-tile of 8 heads).
-// With M = max_i m_i, out = sum_i 2^(m_i - M) o_i / (sum_i 2^(m_i - M) l_i +
-// sink term).  Every block finds its segment's tiles from the lengths, as the
-// attention kernel did.  Requests without rows get their output here.
-template <int D, int TT, int HEADS>
+// Joins the pieces of cut segments.  With M = max_i m_i,
+//   out = sum_i 2^(m_i - M) o_i / (sum_i 2^(m_i - M) l_i + sink term).
+// Block (segment, 8 / PW heads): PW warps per head share its pieces, so that a
+// long segment's many pieces are read at once (PW = 8) and short segments do
+// not cost a block per head (PW = 1).  Every block finds its segment's tiles
+// from the lengths, as the attention kernel did; that part runs before the
+// wait for it (the attention kernel itself starts behind the call's inputs,
+// and only then lets this one go).  Requests without rows get their output
+// here.
+template <int D, int TT, int HEADS, int PW>
 __global__ void __launch_bounds__(kJoinThreads) dsv4_gqa_join_kernel(const __grid_constant__ DecodeParams p) {
+    constexpr int kHeads = 8 / PW;             // per block
+    constexpr int V = D / 32;                  // values per lane
     __shared__ unsigned s_sum[2][kJoinThreads / 32];
     __shared__ int s_near[2][kJoinThreads / 32];
-    __shared__ float s_w[kMaxCtas][8];
     __shared__ float2 s_ml[8];
+    __shared__ float s_o[PW > 1 ? 8 : 1][PW > 1 ? D : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hcs = p.c.kv_heads * p.chunks;
     const int b = blockIdx.x / hcs, hc = blockIdx.x % hcs;
-    grid_dependency_wait();
-    grid_dependents_go();
 
     unsigned err = 0, before = 0, total = 0;
     int next = 0x7fffffff, earlier = 0;
@@ -43,12 +49,11 @@ __global__ void __launch_bounds__(kJoinThreads) dsv4_gqa_join_kernel(const __gri
             if (e > b) next = min(next, e);
         }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-        next = min(next, __shfl_xor_sync(0xffffffffu, next, o));
-        earlier |= __shfl_xor_sync(0xffffffffu, earlier, o);
+    before = __reduce_add_sync(0xffffffffu, before);
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (link) {
+        next = __reduce_min_sync(0xffffffffu, next);
+        earlier = __reduce_or_sync(0xffffffffu, earlier);
     }
     if (lane == 0) {
         s_sum[0][warp] = before;
@@ -65,75 +70,116 @@ __global__ void __launch_bounds__(kJoinThreads) dsv4_gqa_join_kernel(const __gri
         next = min(next, s_near[0][w]);
         earlier |= s_near[1][w];
     }
+    grid_dependency_wait();
+    grid_dependents_go();
     if (link && tid == 0)
         p.info[b] = make_int4(static_cast<int>(before), next == 0x7fffffff ? -1 : next, !earlier, rq.n);
 
     const int h = hc / p.chunks, chunk = hc % p.chunks;
-    const int first = chunk * HEADS + blockIdx.y * 8;          // in the KV head's group
-    const int nheads = min(8, p.group - first);
-    if (nheads <= 0) return;
-    const int head0 = h * p.group + first;
-    uint16_t* out = static_cast<uint16_t*>(p.out) + ((size_t)b * p.heads + head0) * D;
+    const int head = blockIdx.y * kHeads + warp / PW;          // in the segment
+    const bool mine = chunk * HEADS + head < p.group;
+    const size_t at = (size_t)b * p.heads + h * p.group + chunk * HEADS + head;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + at * D + lane * V;
+    const float sk = p.sink && mine ? __ldg(p.sink + h * p.group + chunk * HEADS + head) * kLog2e : -INFINITY;
     if (rg.tiles == 0) {
-        for (int e = tid; e < nheads * D / 4; e += kJoinThreads) reinterpret_cast<uint2*>(out)[e] = make_uint2(0u, 0u);
-        if (tid < nheads) {
-            const float l2 = p.sink ? __ldg(p.sink + head0 + tid) * kLog2e : -INFINITY;
-            if (p.lse) p.lse[(size_t)b * p.heads + head0 + tid] = l2 * kLn2;
-            if (p.lse2) p.lse2[(size_t)b * p.heads + head0 + tid] = l2;
+        if (mine && warp % PW == 0) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) reinterpret_cast<uint32_t*>(out)[i] = 0u;
+            if (lane == 0) {
+                if (p.lse) p.lse[at] = sk * kLn2;
+                if (p.lse2) p.lse2[at] = sk;
+            }
         }
         return;
     }
-    const int ctas = share_count(p, total);
+    const int shares = share_count(p, total);
     const unsigned seg = before + hc * rg.tiles;
-    const int c0 = share_of(total, ctas, seg), c1 = share_of(total, ctas, seg + rg.tiles - 1);
+    const int c0 = share_of(total, shares, seg), c1 = share_of(total, shares, seg + rg.tiles - 1);
     if (c0 == c1) return;
     const int pieces = c1 - c0 + 1;
-    // warp w: head w
-    if (warp < nheads) {
-        const float2* ml = p.part_ml + blockIdx.y * 8 + warp;
-        float mx = kNoMax, l = 0.f;
-        for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, ml[(size_t)(2 * (c0 + i) + (i == 0)) * HEADS].x);
+    float a[V] = {}, mx = kNoMax, l = 0.f;
+    if (mine) {
+        // this warp's pieces, kBatch at a time; the reference moves between batches
+        constexpr int kBatch = 4;
+        for (int i0 = warp % PW; i0 < pieces; i0 += PW * kBatch) {
+            float2 ml[kBatch];
+            float x[kBatch][V];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        for (int i = lane; i < pieces; i += 32) {
-            const float2 x = ml[(size_t)(2 * (c0 + i) + (i == 0)) * HEADS];
-            const float f = fast_exp2(x.x - mx);
-            s_w[i][warp] = f;
-            l += f * x.y;
-        }
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * PW;
+                ml[k] = make_float2(kNoMax, 0.f);
+                if (i < pieces) {
+                    const size_t e = (size_t)piece_entry(c0 + i, i == 0) * HEADS + head;
+                    ml[k] = p.part_ml[e];
+                    const float* from = p.part_o + e * D + lane * V;
+                    if constexpr (V == 2) {
+                        const float2 y = *reinterpret_cast<const float2*>(from);
+                        x[k][0] = y.x; x[k][1] = y.y;
+                    } else {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (lane == 0) {
-            const float sk = p.sink ? __ldg(p.sink + head0 + warp) * kLog2e : -INFINITY;
-            const float top = fmaxf(mx, sk);
+                        for (int q = 0; q < V; q += 4) {
+                            const float4 y = *reinterpret_cast<const float4*>(from + q);
+                            x[k][q] = y.x; x[k][q + 1] = y.y; x[k][q + 2] = y.z; x[k][q + 3] = y.w;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < V; ++q) x[k][q] = 0.f;
+                }
+            }
+            float top = mx;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
             const float f = fast_exp2(mx - top);
-            l = l * f + fast_exp2(sk - top);
-            const float vmul = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
-            const bool any = l > 0.f || l != l;
-            s_ml[warp] = make_float2(any ? vmul * f / l : 0.f, 0.f);
-            const float l2 = any ? top + log2f(l) : -INFINITY;
-            if (p.lse) p.lse[(size_t)b * p.heads + head0 + warp] = l2 * kLn2;
-            if (p.lse2) p.lse2[(size_t)b * p.heads + head0 + warp] = l2;
+            mx = top;
+            l *= f;
+#pragma unroll
+            for (int q = 0; q < V; ++q) a[q] *= f;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float w = fast_exp2(ml[k].x - top);
+                l += w * ml[k].y;
+#pragma unroll
+                for (int q = 0; q < V; ++q) a[q] += w * x[k][q];
+            }
         }
     }
-    __syncthreads();
-    for (int e = tid; e < nheads * D / 4; e += kJoinThreads) {
-        const int c = e / (D / 4);
-        const float* at = p.part_o + (size_t)(2 * c0) * HEADS * D + (size_t)blockIdx.y * 8 * D + e * 4;
-        constexpr size_t kStep = 2 * (size_t)HEADS * D;
-        const float4 x0 = *reinterpret_cast<const float4*>(at + kStep / 2);
-        const float f0 = s_w[0][c];
-        float4 a = make_float4(x0.x * f0, x0.y * f0, x0.z * f0, x0.w * f0);
-#pragma unroll 8
-        for (int i = 1; i < pieces; ++i) {
-            const float4 x = *reinterpret_cast<const float4*>(at + i * kStep);
-            const float f = s_w[i][c];
-            a.x += x.x * f; a.y += x.y * f; a.z += x.z * f; a.w += x.w * f;
+    if constexpr (PW > 1) {
+        if (lane == 0) s_ml[warp] = make_float2(mx, l);
+#pragma unroll
+        for (int q = 0; q < V; ++q) s_o[warp][lane * V + q] = a[q];
+        __syncthreads();
+        if (warp % PW) return;
+        float top = kNoMax;
+#pragma unroll
+        for (int w = 0; w < PW; ++w) top = fmaxf(top, s_ml[warp + w].x);
+        l = 0.f;
+#pragma unroll
+        for (int q = 0; q < V; ++q) a[q] = 0.f;
+#pragma unroll
+        for (int w = 0; w < PW; ++w) {
+            const float f = fast_exp2(s_ml[warp + w].x - top);
+            l += f * s_ml[warp + w].y;
+#pragma unroll
+            for (int q = 0; q < V; ++q) a[q] += f * s_o[warp + w][lane * V + q];
         }
-        const float inv = s_ml[c].x;
-        reinterpret_cast<uint2*>(out)[e] =
-            p.q_bf16 ? make_uint2(pack2<true>(a.x * inv, a.y * inv), pack2<true>(a.z * inv, a.w * inv))
-                     : make_uint2(pack2<false>(a.x * inv, a.y * inv), pack2<false>(a.z * inv, a.w * inv));
+        mx = top;
+    }
+    if (!mine) return;
+    const float top = fmaxf(mx, sk);
+    const float f = fast_exp2(mx - top);
+    l = l * f + fast_exp2(sk - top);
+    const bool any = l > 0.f || l != l;
+    const float inv = any ? (p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f) * f / l : 0.f;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        const float x = a[2 * i] * inv, y = a[2 * i + 1] * inv;
+        reinterpret_cast<uint32_t*>(out)[i] = p.q_bf16 ? pack2<true>(x, y) : pack2<false>(x, y);
+    }
+    if (lane == 0) {
+        const float l2 = any ? top + log2f(l) : -INFINITY;
+        if (p.lse) p.lse[at] = l2 * kLn2;
+        if (p.lse2) p.lse2[at] = l2;
     }
 }
 
@@ -144,7 +190,7 @@ __global__ void __launch_bounds__(kJoinThreads) dsv4_gqa_join_kernel(const __gri
 // slot.
 template <int TT, int HEADS>
 __global__ void __launch_bounds__(kWeightThreads) dsv4_gqa_weight_kernel(const __grid_constant__ DecodeParams p) {
-    __shared__ float s_lse[64 + 16];
+    __shared__ __align__(16) float s_lse[64 + 16];
     const int tid = threadIdx.x;
     const int b = blockIdx.y / p.c.kv_heads, h = blockIdx.y % p.c.kv_heads;
     const int slot0 = blockIdx.x * kWeightThreads * kWeightSlots + tid;
@@ -154,7 +200,14 @@ __global__ void __launch_bounds__(kWeightThreads) dsv4_gqa_weight_kernel(const _
     if (!info.z || info.w == 0) return;
     unsigned err = 0;
     const int row = read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, err).row;
-    float acc[kWeightSlots] = {};
+    const size_t at = ((size_t)row * p.c.kv_heads + h) * p.width;
+    // each request's first slots of every chunk are on their way while the lse of its heads is fetched
+    float prior[kWeightSlots], acc[kWeightSlots] = {};
+#pragma unroll
+    for (int k = 0; k < kWeightSlots; ++k) {
+        const int slot = slot0 + k * kWeightThreads;
+        prior[k] = slot < p.max_len ? __ldcs(p.w_in + at + slot) : 0.f;
+    }
     int most = 0;
     for (int e = b;;) {
         const Range rg = key_range<TT>(p, info.w);
@@ -166,26 +219,27 @@ __global__ void __launch_bounds__(kWeightThreads) dsv4_gqa_weight_kernel(const _
                 const float l = tid < p.group ? p.lse2[(size_t)e * p.heads + h * p.group + tid] : INFINITY;
                 s_lse[tid] = l == -INFINITY ? INFINITY : l;
             }
-            __syncthreads();
             for (int ch = 0; ch < p.chunks; ++ch) {
                 const unsigned seg = static_cast<unsigned>(info.x) + (h * p.chunks + ch) * rg.tiles;
                 const float* base = p.logits + ((size_t)seg * TT - rg.lo / TT * TT) * HEADS;
+                float4 y[kWeightSlots][HEADS / 4];
 #pragma unroll
                 for (int k = 0; k < kWeightSlots; ++k) {
                     const int slot = slot0 + k * kWeightThreads;
-                    if (slot < rg.lo || slot >= rg.n) continue;
+                    const bool in = slot >= rg.lo && slot < rg.n;
                     const float4* x = reinterpret_cast<const float4*>(base + (size_t)slot * HEADS);
-                    float4 y[HEADS / 4];
 #pragma unroll
-                    for (int i = 0; i < HEADS / 4; ++i) y[i] = __ldcs(x + i);
+                    for (int i = 0; i < HEADS / 4; ++i)
+                        y[k][i] = in ? __ldcs(x + i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                }
+                if (ch == 0) __syncthreads();
 #pragma unroll
-                    for (int i = 0; i < HEADS / 4; ++i) {
-                        const float* l = s_lse + ch * HEADS + 4 * i;
-                        acc[k] += fast_exp2(y[i].x - l[0]);
-                        acc[k] += fast_exp2(y[i].y - l[1]);
-                        acc[k] += fast_exp2(y[i].z - l[2]);
-                        acc[k] += fast_exp2(y[i].w - l[3]);
-                    }
+                for (int i = 0; i < HEADS / 4; ++i) {
+                    const float4 l = *reinterpret_cast<const float4*>(s_lse + ch * HEADS + 4 * i);
+#pragma unroll
+                    for (int k = 0; k < kWeightSlots; ++k)
+                        acc[k] += (fast_exp2(y[k][i].x - l.x) + fast_exp2(y[k][i].y - l.y)) +
+                                  (fast_exp2(y[k][i].z - l.z) + fast_exp2(y[k][i].w - l.w));
                 }
             }
         }
@@ -193,11 +247,10 @@ __global__ void __launch_bounds__(kWeightThreads) dsv4_gqa_weight_kernel(const _
         e = info.y;
         info = p.info[e];
     }
-    const size_t at = ((size_t)row * p.c.kv_heads + h) * p.width;
 #pragma unroll
     for (int k = 0; k < kWeightSlots; ++k) {
         const int slot = slot0 + k * kWeightThreads;
-        if (slot < most) p.w_out[at + slot] = p.decay * p.w_in[at + slot] + acc[k];
+        if (slot < most) p.w_out[at + slot] = p.decay * prior[k] + acc[k];
     }
 }
 
@@ -211,6 +264,7 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 struct Plan {
     int group, nt, chunks, tt;
     long long tiles;                       // bound on the tile list
+    int ctas;                              // grid of the attention kernel
     size_t part_o, part_ml, lse2, info, logits, bytes;      // offsets, size
 };
 
@@ -227,32 +281,31 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
     const long long segments = (long long)batch * c->num_kv_heads * pl.chunks;
     pl.tiles = segments * ((max_len + pl.tt - 1) / pl.tt);
     if (pl.tiles >= 1LL << 31 || segments >= 1LL << 31) return DSV4_ERR_UNSUPPORTED;
+    // (512-byte rows: one CTA's ring fills an SM's shared memory)
+    const int most = c->head_dim * (c->format == DSV4_GQA_E4M3 ? 1 : 2) > 256 ? kMaxCtas / 2 : kMaxCtas;
+    const long long want = pl.tiles / kMinTiles;
+    pl.ctas = want < 1 ? 1 : (want < most ? static_cast<int>(want) : most);
+    const size_t entries = size_t(2) * pl.ctas * kWarps * 8 * pl.nt;
     pl.part_o = 0;
-    pl.part_ml = pl.part_o + up256(size_t(2) * kMaxCtas * 8 * pl.nt * c->head_dim * sizeof(float));
-    pl.lse2 = pl.part_ml + up256(size_t(2) * kMaxCtas * 8 * pl.nt * sizeof(float2));
+    pl.part_ml = pl.part_o + up256(entries * c->head_dim * sizeof(float));
+    pl.lse2 = pl.part_ml + up256(entries * sizeof(float2));
     pl.info = pl.lse2 + (weights ? up256(size_t(batch) * heads * sizeof(float)) : 0);
     pl.logits = pl.info + (weights ? up256(size_t(batch) * sizeof(int4)) : 0);
     pl.bytes = pl.logits + (weights ? size_t(pl.tiles) * pl.tt * 8 * pl.nt * sizeof(float) : 0);
     return DSV4_OK;
 }
 
-int sm_count() {
-    static int counts[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    int n = __atomic_load_n(&counts[dev], __ATOMIC_RELAXED);
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        __atomic_store_n(&counts[dev], n, __ATOMIC_RELAXED);
-    }
-    return n;
+template <int D, int TT, int HEADS>
+int launch_join_heads(const DecodeParams& p, void* stream) {
+    const unsigned segments = p.batch * p.c.kv_heads * p.chunks;
+    if (segments * HEADS < 2048)
+        return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 8>, dim3(segments, HEADS), kJoinThreads, 0, stream, 1, p);
+    return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 1>, dim3(segments, HEADS / 8), kJoinThreads, 0, stream, 1, p);
 }
 
 template <int D, int TT>
 int launch_join(const DecodeParams& p, int nt, void* stream) {
-    const unsigned segments = p.batch * p.c.kv_heads * p.chunks;
-    return nt == 1 ? launch(dsv4_gqa_join_kernel<D, TT, 8>, dim3(segments, 1), kJoinThreads, 0, stream, 1, p)
-                   : launch(dsv4_gqa_join_kernel<D, TT, 16>, dim3(segments, 2), kJoinThreads, 0, stream, 1, p);
+    return nt == 1 ? launch_join_heads<D, TT, 8>(p, stream) : launch_join_heads<D, TT, 16>(p, stream);
 }
 
 template <int TT>
@@ -294,8 +347,7 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     if (!workspace || workspace_bytes < pl.bytes) return DSV4_ERR_WORKSPACE;
     if (!aligned16(workspace)) return DSV4_ERR_INVALID;
     unsigned int* err = device_error_word();
-    const int sms = sm_count();
-    if (!err || !sms) return DSV4_ERR_CUDA;
+    if (!err) return DSV4_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     DecodeParams p;
     p.c = device_cache(cache);
@@ -323,10 +375,8 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     p.w_out = weights_out;
     p.width = width;
     p.decay = decay;
-    p.min_tiles = 4;
-    const long long most = pl.tiles / p.min_tiles;
-    const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-    p.ctas = most < 1 ? 1 : (most < grid ? static_cast<int>(most) : grid);
+    p.min_tiles = kMinTiles;
+    p.warps = pl.ctas * kWarps;
     p.err = err;
 
     const int d = cache->head_dim;

@@ -6,17 +6,16 @@
 //
 // Work: a segment is one (request, KV head, group of up to 8 NT query heads);
 // its key range is cut into tiles of TT slots.  All tiles of the batch form
-// one list, of which every CTA takes an equal contiguous share, so a ragged
-// batch is as balanced as a uniform one and a long request is split over as
-// many CTAs as it needs.  A segment that lies in one CTA's share is finished
-// there; of a cut one every CTA leaves (unnormalised output, maximum, sum) in
-// fp32 in the workspace, at most two pieces per CTA, which the join kernel
-// merges.
+// one list, of which every warp of the grid takes an equal contiguous share,
+// so a ragged batch is as balanced as a uniform one and a long request is
+// split over as many warps as it needs.  A segment that lies in one share is
+// finished there; of a cut one every warp leaves (unnormalised output,
+// reference, sum) in fp32 in the workspace, at most two pieces per warp, which
+// the join kernel merges.  Warps never wait for one another after the start.
 //
-// In a CTA, warp w takes tiles w, w + W, ... of a piece, each through its own
-// ring of cp.async stages (no block barrier in the loop; the ring runs ahead
-// over piece boundaries).  Scores are computed transposed, S^T = K Q^T, so
-// the 16 rows of an m16n8k16 MMA are slots and its 8 columns query heads: a
+// A warp streams its tiles through its own ring of cp.async stages, which runs
+// ahead over segment boundaries.  Scores are computed transposed, S^T = K Q^T,
+// so the 16 rows of an m16n8k16 MMA are slots and its 8 columns query heads: a
 // group of 8 heads wastes nothing.  The exponentials become the B operand of
 // O^T = V^T P^T by one 8x8 transposition in registers (movmatrix).  The
 // softmax is online with a lazy reference: a tile's scores are compared with
@@ -41,8 +40,8 @@ namespace gqa {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;           // reference of a head that has seen no score
-constexpr int kMaxCtas = 304;              // shares that the tile list is cut into, at most (two per SM)
-
+constexpr int kWarps = 4;                  // warps per CTA
+constexpr int kMaxCtas = 304;              // resident at once: two per SM
 struct DecodeParams {
     Cache c;
     const void* q;
@@ -57,8 +56,8 @@ struct DecodeParams {
     void* out;
     float* lse;
     // workspace
-    float* part_o;                         // [2 kMaxCtas][8 NT][D]
-    float2* part_ml;                       // [2 kMaxCtas][8 NT]
+    float* part_o;                         // [2 shares][8 NT][D]
+    float2* part_ml;                       // [2 shares][8 NT]
     float* lse2;                           // [batch][heads], log2 units (with weights)
     int4* info;                            // [batch] (with weights): first tile, next request of the same row or
                                            // -1, whether it is the row's first, rows
@@ -68,8 +67,8 @@ struct DecodeParams {
     float* w_out;
     long long width;
     float decay;
-    int min_tiles;                         // a CTA takes at least this many tiles
-    int ctas;                              // the decode grid
+    int min_tiles;                         // a share has at least this many tiles (where there are as many)
+    int warps;                             // of the grid: shares, at most
     unsigned int* err;
 };
 
@@ -87,21 +86,21 @@ __device__ __forceinline__ Range key_range(const DecodeParams& p, int n) {
     return r;
 }
 
-// How many CTAs share `total` tiles, and where share i begins.
+// How many warps share `total` tiles, and the list index that share i begins at.
 __device__ __forceinline__ int share_count(const DecodeParams& p, unsigned total) {
     const unsigned most = total / p.min_tiles;
-    return most < 1u ? 1 : (most > (unsigned)p.ctas ? p.ctas : (int)most);
+    return most < 1u ? 1 : (most > (unsigned)p.warps ? p.warps : (int)most);
 }
-__device__ __forceinline__ unsigned share_begin(unsigned total, int ctas, int i) {
-    return static_cast<unsigned>(static_cast<unsigned long long>(total) * i / ctas);
+__device__ __forceinline__ unsigned share_begin(unsigned total, int shares, int i) {
+    return static_cast<unsigned>(static_cast<unsigned long long>(total) * i / shares);
 }
-// The share that tile t lies in.
-__device__ __forceinline__ int share_of(unsigned total, int ctas, unsigned t) {
-    int i = static_cast<int>(static_cast<unsigned long long>(t) * ctas / total);
-    while (i + 1 < ctas && share_begin(total, ctas, i + 1) <= t) ++i;
-    while (i > 0 && share_begin(total, ctas, i) > t) --i;
-    return i;
+// The share that tile t lies in: the largest i with total i / shares < t + 1.
+__device__ __forceinline__ int share_of(unsigned total, int shares, unsigned t) {
+    return static_cast<int>((static_cast<unsigned long long>(t + 1) * shares - 1) / total);
 }
+// The workspace entry of share i's piece of a cut segment: one that begins
+// with its segment can only be the share's last, any other its first.
+__device__ __forceinline__ int piece_entry(int share, bool begins) { return 2 * share + (begins ? 1 : 0); }
 
 // ---------------------------------------------------------------- PTX
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -179,13 +178,12 @@ struct Shape {
     static constexpr int MT = TT / 16;                       // 16-slot MMA tiles
     static constexpr int DT = D / 16;                        // 16-dim tiles
     static constexpr int HEADS = 8 * NT;                     // query heads of a segment (padded)
-    static constexpr int W = 4;                              // warps per CTA
+    static constexpr int W = kWarps;
     static constexpr int TILE_BYTES = TT * ROWB;             // K or V of a stage
-    static constexpr int STAGES = TILE_BYTES > 4096 ? 1 : 3;
+    static constexpr int STAGES = 3;
+    static constexpr int CTAS = TILE_BYTES > 4096 ? 1 : 2;   // per SM (what shared memory holds)
     static constexpr int RING_BYTES = W * STAGES * 2 * TILE_BYTES;
-    static constexpr int MERGE_STRIDE = D + 4;               // floats per head of a merge row (bank spread)
-    static constexpr int MERGE_BYTES = W * 8 * MERGE_STRIDE * 4;
-    static constexpr int SMEM = RING_BYTES + MERGE_BYTES;
+    static constexpr int SMEM = RING_BYTES;
     static constexpr int PPR = ROWB / 16;                    // 16-byte pieces per row
     static constexpr int RPI = 32 / PPR;                     // rows per warp-wide copy
 };
@@ -210,7 +208,7 @@ __device__ __forceinline__ uint32_t v_offset(int row, int piece) {
 }
 
 // ---------------------------------------------------------------- the walk over tiles
-// A position in a CTA's share of the tile list.  Every warp has two: one that
+// A position in a warp's share of the tile list.  Every warp has two: one that
 // runs ahead issuing copies and one that follows computing.
 template <int TT>
 struct Cursor {
@@ -218,8 +216,8 @@ struct Cursor {
     Request rq;
     Range rg;
     unsigned seg;              // list index of the segment's first tile
-    unsigned end;              // end of the current piece
-    unsigned begin;            // begin of the current piece
+    unsigned end;              // end of the share's part of it
+    unsigned at;               // current tile
 
     __device__ __forceinline__ void load(const DecodeParams& p) {
         unsigned ignored = 0;
@@ -230,9 +228,9 @@ struct Cursor {
         end = seg + rg.tiles < t1 ? seg + rg.tiles : t1;
     }
     // to the next segment that has tiles; false at the end of the share
-    __device__ __forceinline__ bool next_piece(const DecodeParams& p, int hcs, unsigned t1) {
+    __device__ __forceinline__ bool next_segment(const DecodeParams& p, int hcs, unsigned t1) {
         if (end >= t1) return false;
-        seg = begin = end;
+        seg = at = end;
         if (++hc == hcs) {
             hc = 0;
             do {
@@ -246,13 +244,12 @@ struct Cursor {
 };
 
 template <class S>
-__global__ void __launch_bounds__(S::W * 32, 2) dsv4_gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int D = S::D, NT = S::NT, W = S::W, TT = S::TT, MT = S::MT, DT = S::DT, HEADS = S::HEADS;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float2 s_ml[W][HEADS];
-    __shared__ unsigned s_scan[W + 1];
-    __shared__ unsigned s_seg;                    // where the share begins: list index of the request's first tile
-    __shared__ int s_b;
+    __shared__ unsigned s_scan[W];
+    __shared__ unsigned s_seg[W];                 // where each share begins: list index of the request's first tile
+    __shared__ int s_b[W];                        // and the request
     __shared__ int s_ok[W][S::STAGES];            // a bit per 16-slot group: its page is in the pool
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -288,15 +285,23 @@ __global__ void __launch_bounds__(S::W * 32, 2) dsv4_gqa_decode_kernel(const __g
         __syncthreads();
     }
     if (err && blockIdx.x == 0) atomicOr(p.err, err);
-    const int ctas = share_count(p, total);
-    if ((int)blockIdx.x >= ctas || total == 0) return;
-    const unsigned t0 = share_begin(total, ctas, blockIdx.x), t1 = share_begin(total, ctas, blockIdx.x + 1);
-    if (t0 >= t1) return;
-    if (rounds == 1) {
-        if (t0 >= mine0 && t0 < mine0 + cnt0) {
-            s_b = tid;
-            s_seg = mine0;
+    if (total == 0) return;
+    const int shares = share_count(p, total);
+    // warps of one CTA take shares far apart, so that few shares spread over all SMs
+    auto share_id = [&](int w) { return w * gridDim.x + blockIdx.x; };
+    auto find = [&](unsigned base, unsigned cnt, int b) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if ((int)share_id(w) >= shares) continue;
+            const unsigned t = share_begin(total, shares, share_id(w));
+            if (t >= base && t < base + cnt) {
+                s_b[w] = b;
+                s_seg[w] = base;
+            }
         }
+    };
+    if (rounds == 1) {
+        find(mine0, cnt0, tid);
     } else {
         unsigned run = 0;
         for (int k = 0; k < rounds; ++k) {
@@ -318,22 +323,21 @@ __global__ void __launch_bounds__(S::W * 32, 2) dsv4_gqa_decode_kernel(const __g
                 if (w < warp) base += s_scan[w];
                 run += s_scan[w];
             }
-            if (t0 >= base + incl - cnt && t0 < base + incl) {
-                s_b = b;
-                s_seg = base + incl - cnt;
-            }
+            find(base + incl - cnt, cnt, b);
             __syncthreads();
-            if (run > t0) break;
         }
     }
     __syncthreads();
+    const int share = share_id(warp);
+    if (share >= shares) return;
+    const unsigned t0 = share_begin(total, shares, share), t1 = share_begin(total, shares, share + 1);
 
     Cursor<TT> cons;
-    cons.b = s_b;
+    cons.b = s_b[warp];
     cons.load(p);
-    cons.hc = static_cast<int>((t0 - s_seg) / cons.rg.tiles);
-    cons.seg = s_seg + cons.hc * cons.rg.tiles;
-    cons.begin = t0;
+    cons.at = t0;
+    cons.hc = static_cast<int>((cons.at - s_seg[warp]) / cons.rg.tiles);
+    cons.seg = s_seg[warp] + cons.hc * cons.rg.tiles;
     cons.bound(t1);
 
     // ---- the copying side ----
@@ -342,28 +346,24 @@ __global__ void __launch_bounds__(S::W * 32, 2) dsv4_gqa_decode_kernel(const __g
     const long long lane_off = lane_row * p.c.row_stride + lane_piece * 16;
     const int page_mask = (1 << p.c.page_shift) - 1;
     Cursor<TT> prod = cons;
-    unsigned ptile = prod.begin + warp;
     bool more = true;
     int page = -1;                                 // lane m < MT: page of 16-slot group m of the next tile
     bool wanted = false;                           // that group holds slots to attend
 
-    // to the warp's next tile; loads its page ids one tile ahead of their use
+    // page ids of the tile to be copied next, loaded one tile ahead of their use
     auto settle = [&]() {
-        while (more && ptile >= prod.end) {
-            more = prod.next_piece(p, hcs, t1);
-            ptile = prod.begin + warp;
-        }
+        if (more && prod.at >= prod.end) more = prod.next_segment(p, hcs, t1);
         page = -1;
         wanted = false;
         if (more && lane < MT) {
-            const int slot = (prod.rg.lo / TT + static_cast<int>(ptile - prod.seg)) * TT + lane * 16;
+            const int slot = (prod.rg.lo / TT + static_cast<int>(prod.at - prod.seg)) * TT + lane * 16;
             wanted = slot < prod.rg.n && slot + 16 > prod.rg.lo;
             if (wanted) page = __ldg(p.c.table + (long long)prod.rq.row * p.c.table_stride + (slot >> p.c.page_shift));
         }
     };
     auto issue = [&](int stage) {
         if (more) {
-            const int slot0 = (prod.rg.lo / TT + static_cast<int>(ptile - prod.seg)) * TT;
+            const int slot0 = (prod.rg.lo / TT + static_cast<int>(prod.at - prod.seg)) * TT;
             const bool ok = page >= 0 && page < p.c.num_pages;
             if (wanted && !ok) atomicOr(p.err, DSV4_DEV_ERR_GQA_PAGE);
             const unsigned okm = __ballot_sync(0xffffffffu, ok);
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(S::W * 32, 2) dsv4_gqa_decode_kernel(const __g
                     cp_async_16(vd + v_offset<S>(m * 16 + r, lane_piece), p.c.v + off, in ? 16u : 0u);
                 }
             }
-            ptile += W;
+            ++prod.at;
             settle();
         }
         cp_async_commit();
@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(S::W * 32, 2) dsv4_gqa_decode_kernel(const __g
 
     // ---- the computing side ----
     int stage = 0;
-    float* merge = reinterpret_cast<float*>(smem + S::RING_BYTES);
-    for (bool on = true; on; on = cons.next_piece(p, hcs, t1)) {
+    for (bool on = true; on; on = cons.next_segment(p, hcs, t1)) {
+        const bool begins = cons.at == cons.seg;
         const int h = cons.hc / p.chunks, chunk = cons.hc % p.chunks;
         const int head0 = h * p.group + chunk * HEADS;
         const int nheads = min(HEADS, p.group - chunk * HEADS);
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(S::W * 32, 2) dsv4_gqa_decode_kernel(const __g
                 for (int c = 0; c < 4; ++c) o[j][nt][c] = 0.f;
         }
 
-        for (unsigned tile = cons.begin + warp; tile < cons.end; tile += W) {
+        for (unsigned tile = cons.at; tile < cons.end; ++tile) {
             cp_async_wait_group<S::STAGES - 1>();
             __syncwarp();
             const uint32_t ks = ring + stage * 2 * S::TILE_BYTES, vs = ks + S::TILE_BYTES;
@@ -627,78 +627,88 @@ __global__ void __launch_bounds__(S::W * 32, 2) dsv4_gqa_decode_kernel(const __g
             stage = stage + 1 == S::STAGES ? 0 : stage + 1;
         }
 
-        // ---- merge the warps: sums and references, then O in rounds of 8 heads ----
+        // ---- the piece's sums, and its output ----
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                float l = lsum[nt][u];
-                l += __shfl_xor_sync(0xffffffffu, l, 4);
-                l += __shfl_xor_sync(0xffffffffu, l, 8);
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                if (g == 0) s_ml[warp][nt * 8 + 2 * t4 + u] = make_float2(mref[nt][u], l);
+                lsum[nt][u] += __shfl_xor_sync(0xffffffffu, lsum[nt][u], 4);
+                lsum[nt][u] += __shfl_xor_sync(0xffffffffu, lsum[nt][u], 8);
+                lsum[nt][u] += __shfl_xor_sync(0xffffffffu, lsum[nt][u], 16);
             }
-        __syncthreads();
-        const bool split = cons.begin != cons.seg || cons.end != cons.seg + cons.rg.tiles;
-        const int slot = 2 * blockIdx.x + (cons.begin == cons.seg ? 1 : 0);
+        if (!begins || cons.end != cons.seg + cons.rg.tiles) {
+            const int entry = piece_entry(share, begins);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int c = nt * 8 + 2 * t4 + u;
+                    if (c >= nheads) continue;
+                    float* to = p.part_o + ((size_t)entry * HEADS + c) * D;
+#pragma unroll
+                    for (int j = 0; j < DT; ++j) {
+                        if constexpr (!S::FP8) {
+                            to[16 * j + g] = o[j][nt][u];
+                            to[16 * j + 8 + g] = o[j][nt][u + 2];
+                        } else {
+                            const int d = D == 64 ? 8 * g + 2 * j : 16 * (g + 8 * (j >> 3)) + 2 * (j & 7);
+                            *reinterpret_cast<float2*>(to + d) = make_float2(o[j][nt][u], o[j][nt][u + 2]);
+                        }
+                    }
+                    if (g == 0) p.part_ml[entry * HEADS + c] = make_float2(mref[nt][u], lsum[nt][u]);
+                }
+            continue;
+        }
         const float vmul = S::FP8 && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
+        const size_t row = (size_t)cons.b * p.heads + head0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            float inv[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int c = nt * 8 + 2 * t4 + u;
-                float mx = kNoMax;
+                const float sk = p.sink && c < nheads ? __ldg(p.sink + head0 + c) * kLog2e : -INFINITY;
+                const float top = fmaxf(mref[nt][u], sk);
+                const float f = fast_exp2(mref[nt][u] - top);
+                const float l = lsum[nt][u] * f + fast_exp2(sk - top);
+                const bool any = l > 0.f || l != l;
+                inv[u] = any ? vmul * f / l : 0.f;
+                if (g == 0 && c < nheads) {
+                    const float l2 = any ? top + log2f(l) : -INFINITY;
+                    if (p.lse) p.lse[row + c] = l2 * kLn2;
+                    if (p.lse2) p.lse2[row + c] = l2;
+                }
+            }
+            uint16_t* out = static_cast<uint16_t*>(p.out);
+            if constexpr (!S::FP8) {
+                // pairs of heads to pairs of dims: this thread then holds head g, dims 2t and 2t + 1 of an 8-dim block
 #pragma unroll
-                for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_ml[w][c].x);
-                const float f = fast_exp2(mref[nt][u] - mx);
-                float* to = merge + (warp * 8 + 2 * t4 + u) * S::MERGE_STRIDE;
+                for (int j = 0; j < DT; ++j)
 #pragma unroll
-                for (int j = 0; j < DT; ++j) {
-                    if constexpr (!S::FP8) {
-                        to[16 * j + g] = o[j][nt][u] * f;
-                        to[16 * j + 8 + g] = o[j][nt][u + 2] * f;
-                    } else {
-                        const int d = D == 64 ? 8 * g + 2 * j : 16 * (g + 8 * (j >> 3)) + 2 * (j & 7);
-                        *reinterpret_cast<float2*>(to + d) = make_float2(o[j][nt][u] * f, o[j][nt][u + 2] * f);
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t w = transpose8x8(
+                            pack2<S::BF16>(o[j][nt][2 * u] * inv[0], o[j][nt][2 * u + 1] * inv[1]));
+                        if (nt * 8 + g < nheads)
+                            *reinterpret_cast<uint32_t*>(out + (row + nt * 8 + g) * D + 16 * j + 8 * u + 2 * t4) = w;
+                    }
+            } else {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int c = nt * 8 + 2 * t4 + u;
+                    if (c >= nheads) continue;
+#pragma unroll
+                    for (int j = 0; j < DT; j += 4) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float x = o[j + i][nt][u] * inv[u], y = o[j + i][nt][u + 2] * inv[u];
+                            w[i] = p.q_bf16 ? pack2<true>(x, y) : pack2<false>(x, y);
+                        }
+                        const int d = D == 64 ? 8 * g : 16 * (g + 8 * (j >> 3)) + 2 * (j & 7);
+                        *reinterpret_cast<uint4*>(out + (row + c) * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }
-            __syncthreads();
-            for (int e = tid; e < 8 * D / 4; e += W * 32) {
-                const int c = nt * 8 + e / (D / 4), d = (e % (D / 4)) * 4;
-                if (c >= nheads) continue;
-                float mx = kNoMax, l = 0.f;
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_ml[w][c].x);
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    l += s_ml[w][c].y * fast_exp2(s_ml[w][c].x - mx);
-                    const float4 x = *reinterpret_cast<const float4*>(merge + (w * 8 + (c & 7)) * S::MERGE_STRIDE + d);
-                    a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-                }
-                if (split) {
-                    *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * HEADS + c) * D + d) = a;
-                    if (d == 0) p.part_ml[slot * HEADS + c] = make_float2(mx, l);
-                    continue;
-                }
-                const int head = head0 + c;
-                const float sk = p.sink ? __ldg(p.sink + head) * kLog2e : -INFINITY;
-                const float top = fmaxf(mx, sk);
-                const float f = fast_exp2(mx - top);
-                l = l * f + fast_exp2(sk - top);
-                const float inv = l > 0.f || l != l ? vmul * f / l : 0.f;
-                const size_t at = ((size_t)cons.b * p.heads + head) * D + d;
-                const uint2 w2 = p.q_bf16 ? make_uint2(pack2<true>(a.x * inv, a.y * inv), pack2<true>(a.z * inv, a.w * inv))
-                                          : make_uint2(pack2<false>(a.x * inv, a.y * inv), pack2<false>(a.z * inv, a.w * inv));
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w2;
-                if (d == 0) {
-                    const float l2 = l > 0.f || l != l ? top + log2f(l) : -INFINITY;
-                    if (p.lse) p.lse[(size_t)cons.b * p.heads + head] = l2 * kLn2;
-                    if (p.lse2) p.lse2[(size_t)cons.b * p.heads + head] = l2;
-                }
-            }
-            __syncthreads();
         }
     }
 }
@@ -723,7 +733,7 @@ inline int launch_decode_shape(const DecodeParams& p, void* stream) {
         }
         __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELEASE);
     }
-    return launch(dsv4_gqa_decode_kernel<S>, dim3(p.ctas), S::W * 32, S::SMEM, stream, 1, p);
+    return launch(dsv4_gqa_decode_kernel<S>, dim3(p.warps / S::W), S::W * 32, S::SMEM, stream, 1, p);
 }
 
 template <int KIND>

@@ -2,29 +2,33 @@
 // weight (include/dsv4gqa.h states what is computed).
 //
 // Two kernels.  The select kernel gives every (request, KV head) to one
-// cluster of 1 to 8 CTAs: weights become order-preserving 32-bit keys (held
-// in shared memory where they fit), a radix select of 11 + 11 + 10 bits finds
-// the key of the last row kept and how many rows of that very key stay, and
-// one ordered pass lists the freed slots below `keep` and the kept rows
-// behind it.  Histograms and counts are combined over the cluster through
-// distributed shared memory; every count is exact and every order is that of
-// the slots, so the result does not depend on timing.  The move kernel copies
-// the listed rows: only rows that change their slot are read and written,
-// each once.  It is bound by HBM (4 head_dim bytes x element size per moved
-// row and direction); the select kernel by its passes over shared memory.
+// cluster of 1 to 8 CTAs.  Weights become order-preserving 32-bit keys, which
+// stay in registers: a warp holds a run of consecutive slots, lane l of its
+// i-th register slot 32 i + l of the run.  A radix select of four 8-bit digits
+// finds the key of the last row kept and how many rows of that very key stay;
+// its histograms have eight copies, so that the few hot bins of a digit
+// (weights lie in a few binades) cost few conflicts.  Then lane i holds the
+// kept rows of chunk i as a bit mask, so counting and ranking the freed slots
+// below `keep` and the kept rows behind it is one scan over lanes, and only
+// chunks that have any are visited again.  Histograms and
+// counts are combined over the cluster through distributed shared memory;
+// every count is exact and every order is that of the slots, so the result
+// does not depend on timing.  The move kernel copies the listed rows: only
+// rows that change their slot are read and written, each once.  It is bound by
+// HBM (4 head_dim bytes x element size per moved row and direction).
 #include "dsv4_gqa.cuh"
 
 namespace dsv4 {
 namespace gqa {
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 32;              // rows per block of the move kernel
+constexpr int kBins = 256;
+constexpr int kCopies = 8;
+constexpr int kMoveThreads = 128;
+// rows that a warp of the move kernel copies, by the 16-byte pieces of a K and a V row
+__host__ __device__ constexpr int warp_rows(int pieces) { return pieces >= 32 ? 16 : 32; }
 constexpr int kMaxCluster = 8;
-constexpr int kKeysPerCta = 48 * 1024;     // keys that a CTA holds in shared memory, at most
+constexpr int kHeldKeys = 32 * 1024;       // keys that the largest CTA holds in registers
 
 struct EvictParams {
     Cache c;
@@ -43,7 +47,6 @@ struct EvictParams {
     int* holes;                            // [batch][KV heads][most] their new slots
     int* movers;                           // [batch][KV heads][most] their slots
     int most;
-    int cached;                            // keys per CTA that shared memory holds
     int row_pieces;                        // 16-byte pieces of a row
     unsigned int* err;
 };
@@ -62,11 +65,13 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     return v;
 }
 
+template <int WARPS>
 struct SelectShared {
-    uint32_t hist[2][kBins];               // a CTA's histogram; the second for the next digit
-    uint32_t warp_sum[kSelWarps];
-    uint32_t count[2][4];                  // this CTA's ties / holes / movers, for the cluster
-    uint32_t pick[2];                      // chosen bin, rows wanted in it
+    uint32_t hist[kBins][kCopies];         // lane l counts in copy l mod kCopies
+    uint32_t bins[2][kBins];               // this CTA's sums, for the cluster (by digit parity)
+    uint32_t warp_sum[WARPS];
+    uint32_t count[2][2];                  // this CTA's ties; holes and movers, for the cluster
+    uint32_t pick[3];                      // chosen bin, rows wanted in it, rows in it
     int skip;
 };
 
@@ -78,45 +83,45 @@ __device__ __forceinline__ void lane_sync() {
         __syncthreads();
 }
 
-// Exclusive prefix of v over the block's threads, and the block's total.
-__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_sum, uint32_t& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-    }
+// Exclusive prefix of v over the block's warps (v uniform in a warp), and the
+// block's total.
+template <int WARPS>
+__device__ __forceinline__ uint32_t warps_exclusive(uint32_t v, uint32_t* warp_sum, uint32_t& total) {
+    const int warp = threadIdx.x >> 5;
     __syncthreads();
-    if (lane == 31) warp_sum[warp] = incl;
+    if ((threadIdx.x & 31) == 0) warp_sum[warp] = v;
     __syncthreads();
     uint32_t base = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
         if (w < warp) base += warp_sum[w];
         total += warp_sum[w];
     }
-    return base + incl - v;
+    return base;
 }
 
-template <int CLUSTER>
-__global__ void __launch_bounds__(kSelThreads) dsv4_gqa_select_kernel(const __grid_constant__ EvictParams p) {
-    extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ SelectShared sh;
+// THREADS x KEYS slots per CTA; KEYS = 0: any number, keys made anew in every
+// pass (rows beyond 8 x 32768 slots).
+template <int THREADS, int KEYS, int CLUSTER>
+__global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_gqa_select_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int WARPS = THREADS / 32;
+    __shared__ SelectShared<WARPS> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int id = blockIdx.x / CLUSTER, rank = blockIdx.x % CLUSTER;
     const int b = id / p.c.kv_heads, h = id % p.c.kv_heads;
+    for (int i = tid; i < kBins * kCopies / 4; i += THREADS)
+        reinterpret_cast<uint4*>(&sh.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) sh.skip = 0;
     grid_dependency_wait();
     grid_dependents_go();
 
     unsigned err = 0;
     const Request rq = read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, err);
     const int seen = p.seen ? __ldg(p.seen + b) : rq.n;
-    if (tid == 0) sh.skip = 0;
-    __syncthreads();
     if (p.req && rq.n > 0) {                 // a row that an earlier request of the call names too
-        for (int e = tid; e < b; e += kSelThreads) {
+        __syncthreads();
+        for (int e = tid; e < b; e += THREADS) {
             unsigned ignored = 0;
             const Request x = read_request(p.lens, p.req, p.c.table_rows, p.max_len, e, ignored);
             if (x.n > 0 && x.row == rq.row) sh.skip = 1;
@@ -132,103 +137,133 @@ __global__ void __launch_bounds__(kSelThreads) dsv4_gqa_select_kernel(const __gr
     const int* p_in = p.p_in ? p.p_in + at : nullptr;
     int* p_out = p.p_out ? p.p_out + at : nullptr;
     const bool copy_w = w_in != w_out, copy_p = p_in != p_out;
-    if (rq.n <= p.keep || sh.skip) {         // (uniform over the cluster)
+    const bool skip = err & DSV4_DEV_ERR_REQ_ROW;
+    if (rq.n <= p.keep || skip) {            // (uniform over the cluster)
         if (rank == 0 && tid == 0) p.counts[id] = 0;
-        if ((copy_w || copy_p) && !sh.skip)
-            for (int s = rank * kSelThreads + tid; s < rq.n; s += CLUSTER * kSelThreads) {
+        if ((copy_w || copy_p) && !skip)
+            for (int s = rank * THREADS + tid; s < rq.n; s += CLUSTER * THREADS) {
                 if (copy_w) w_out[s] = w_in[s];
                 if (copy_p) p_out[s] = p_in[s];
             }
         return;
     }
 
-    // this CTA's slots, a multiple of 32 each
+    // this warp's run of slots: equal shares of the CTAs, then of their warps, in chunks of 32
     const int n = rq.n;
-    const int per = ((n + CLUSTER - 1) / CLUSTER + 31) & ~31;
-    const int s0 = min(n, rank * per), s1 = min(n, s0 + per);
-    const bool cached = s1 - s0 <= p.cached;
-    auto make_key = [&](int s) -> uint32_t {
-        const int pos = p_in ? __ldg(p_in + s) : s;
-        if (pos < p.first || pos >= seen - p.recent) return 0xffffffffu;
-        return weight_key(__ldg(w_in + s));
+    const int per = ((n + CLUSTER * WARPS - 1) / (CLUSTER * WARPS) + 31) & ~31;
+    const int r0 = min(n, (rank * WARPS + warp) * per), r1 = min(n, r0 + per);
+    const int chunks = (r1 - r0 + 31) >> 5;
+    auto make_key = [&](float w, int pos) -> uint32_t {
+        return pos < p.first || pos >= seen - p.recent ? 0xffffffffu : weight_key(w);
     };
-    auto key = [&](int s) -> uint32_t { return cached ? keys[s - s0] : make_key(s); };
-    for (int i = tid; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
-    if (cached)
-        for (int s = s0 + tid; s < s1; s += kSelThreads) keys[s - s0] = make_key(s);
+    uint32_t held[KEYS ? KEYS : 1];
+    if constexpr (KEYS > 0) {
+        // a batch's loads before their uses: 4 KB (with positions) per warp in flight
+        constexpr int kBatch = 16;
+#pragma unroll
+        for (int i0 = 0; i0 < KEYS; i0 += kBatch) {
+            float w[kBatch];
+            int pos[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int s = r0 + 32 * (i0 + i) + lane;
+                w[i] = 0.f;
+                pos[i] = s;
+                if (s < r1) {
+                    w[i] = __ldg(w_in + s);
+                    if (p_in) pos[i] = __ldg(p_in + s);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) held[i0 + i] = make_key(w[i], pos[i]);
+        }
+    }
+    // visit(chunk, key, inside) for chunks from .. from + COUNT - 1 of the warp, in order
+    auto each = [&](int from, int count, auto&& visit) {
+        if constexpr (KEYS > 0) {
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i)
+                if (i >= from && i < from + count && i < chunks) visit(i, held[i], r0 + 32 * i + lane < r1);
+        } else {
+            for (int i = from; i < min(from + count, chunks); ++i) {
+                const int s = r0 + 32 * i + lane;
+                const bool in = s < r1;
+                visit(i, in ? make_key(__ldg(w_in + s), p_in ? __ldg(p_in + s) : s) : 0u, in);
+            }
+        }
+    };
     __syncthreads();
 
-    // ---- the key of the last row kept: `want` rows of key `prefix` stay ----
-    uint32_t prefix = 0, want = p.keep, equal = 0;
-#pragma unroll
-    for (int digit = 0; digit < 3; ++digit) {
-        const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
-        const int bits = digit == 2 ? 10 : 11;
-        uint32_t* hist = sh.hist[digit & 1];
-        for (int s = s0 + tid; s < s1; s += kSelThreads) {
-            const uint32_t k = key(s);
-            if (digit == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits)))
-                atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+    // ---- the key of the last row kept: `want` of the `equal` rows of key `prefix` stay ----
+    uint32_t prefix = 0, mask = 0, want = p.keep, equal = 0;
+    for (int digit = 0; digit < 4; ++digit) {
+        const int shift = 24 - 8 * digit;
+        each(0, chunks, [&](int, uint32_t k, bool in) {
+            if (in && (k & mask) == prefix) atomicAdd(&sh.hist[(k >> shift) & 255u][lane % kCopies], 1u);
+        });
+        __syncthreads();
+        // bin sums (a bin's copies are two neighbouring uint4); the copies are cleared for the next digit
+        uint32_t* bins = sh.bins[digit & 1];
+        for (int i = tid; i < kBins * kCopies / 4; i += THREADS) {
+            uint4* c = reinterpret_cast<uint4*>(&sh.hist[0][0]) + i;
+            const uint4 x = *c;
+            *c = make_uint4(0, 0, 0, 0);
+            uint32_t v = x.x + x.y + x.z + x.w;
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            if ((i & 1) == 0) bins[i >> 1] = v;
         }
         lane_sync<CLUSTER>();
-        // thread t: bins from the top, kBins / kSelThreads of them
-        constexpr int kPer = kBins / kSelThreads;
-        uint32_t mine[kPer], sum = 0;
-        const int top = (1 << bits) - 1 - tid * kPer;
+        // one warp looks for the bin: lane l holds bins 255 - 8 l .. 248 - 8 l
+        if (warp == 0) {
+            uint32_t mine[8], sum = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            mine[i] = 0;
-            if (top - i >= 0) {
-                const uint32_t a = smem_u32(&hist[top - i]);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t* bin = &bins[255 - 8 * lane - i];
                 if constexpr (CLUSTER == 1) {
-                    mine[i] = hist[top - i];
+                    mine[i] = *bin;
                 } else {
+                    const uint32_t a = smem_u32(bin);
+                    mine[i] = 0;
 #pragma unroll
                     for (int r = 0; r < CLUSTER; ++r) mine[i] += ld_cluster_u32(mapa(a, r));
                 }
+                sum += mine[i];
             }
-            sum += mine[i];
-        }
-        uint32_t total;
-        uint32_t above = block_exclusive(sum, sh.warp_sum, total);
-        if (above < want && above + sum >= want) {
+            uint32_t above = sum;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                if (above < want && above + mine[i] >= want) {
-                    sh.pick[0] = static_cast<uint32_t>(top - i);
-                    sh.pick[1] = want - above;
-                    sh.count[0][3] = mine[i];
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, above, o);
+                if (lane >= o) above += x;
+            }
+            above -= sum;
+            if (above < want && above + sum >= want) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (above < want && above + mine[i] >= want) {
+                        sh.pick[0] = 255 - 8 * lane - i;
+                        sh.pick[1] = want - above;
+                        sh.pick[2] = mine[i];
+                    }
+                    above += mine[i];
                 }
-                above += mine[i];
             }
         }
         __syncthreads();
         prefix |= sh.pick[0] << shift;
+        mask |= 255u << shift;
         want = sh.pick[1];
-        equal = sh.count[0][3];
-        // the other histogram is ready for the next digit; this one is cleared once every
-        // CTA of the cluster has read it (the next digit's barrier)
-        if (digit == 1) {
-            uint32_t* old = sh.hist[0];
-            for (int i = tid; i < kBins; i += kSelThreads) old[i] = 0;
-        }
-        __syncthreads();
+        equal = sh.pick[2];
+        if (equal == want) break;            // all rows of this prefix stay (uniform over the cluster)
     }
+    // kept: keys above the prefix, and of those at it all (equal == want) or the first `want`
+    const bool every = equal == want;
 
-    // ---- warp w of a CTA: a contiguous run of its slots, 32 at a time ----
-    const int run = (((s1 - s0) + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int r0 = min(s1, s0 + warp * run), r1 = min(s1, r0 + run);
-    const uint32_t below = (1u << lane) - 1u;
-    // ranks of this warp's first element among the lane's ties
-    uint32_t tie = 0;
-    const bool every = equal == want;        // all rows of the last key stay
+    uint32_t tie = 0;                        // rows at the prefix before this warp's
     if (!every) {
         uint32_t c = 0;
-        for (int s = r0 + lane; s - lane < r1; s += 32)
-            c += __popc(__ballot_sync(0xffffffffu, s < r1 && key(s) == prefix));
+        each(0, chunks, [&](int, uint32_t k, bool in) { c += __popc(__ballot_sync(0xffffffffu, in && k == prefix)); });
         uint32_t total;
-        const uint32_t ex = block_exclusive(lane == 0 ? c : 0, sh.warp_sum, total);
-        tie = __shfl_sync(0xffffffffu, ex, 0);
+        tie = warps_exclusive<WARPS>(c, sh.warp_sum, total);
         if (tid == 0) sh.count[0][0] = total;
         lane_sync<CLUSTER>();
         if constexpr (CLUSTER > 1) {
@@ -236,105 +271,181 @@ __global__ void __launch_bounds__(kSelThreads) dsv4_gqa_select_kernel(const __gr
             for (int r = 0; r < rank; ++r) tie += ld_cluster_u32(mapa(a, r));
         }
     }
-    auto walk = [&](auto&& visit) {          // visit(slot, kept, inside) for the warp's slots, ties resolved
-        uint32_t t = tie;
-        for (int s = r0 + lane; s - lane < r1; s += 32) {
-            const bool in = s < r1;
-            const uint32_t k = in ? key(s) : 0u;
-            const bool same = in && k == prefix;
-            bool kept = in && k > prefix;
-            if (every) {
-                kept |= same;
-            } else {
+    const uint32_t below = (1u << lane) - 1u;
+    // bits 0 .. count - 1
+    auto low_bits = [](int count) { return count >= 32 ? ~0u : count <= 0 ? 0u : (1u << count) - 1u; };
+    // lane i: the kept rows of chunk from + i; t: rows at the prefix so far
+    auto kept_rows = [&](int from, uint32_t& t) {
+        uint32_t own = 0;
+        each(from, 32, [&](int i, uint32_t k, bool in) {
+            const uint32_t top = k & mask;
+            bool kept = in && (top > prefix || (every && top == prefix));
+            if (!every) {
+                const bool same = in && k == prefix;
                 const unsigned m = __ballot_sync(0xffffffffu, same);
                 kept |= same && t + __popc(m & below) < want;
                 t += __popc(m);
             }
-            visit(s, kept, in);
-        }
+            const unsigned m = __ballot_sync(0xffffffffu, kept);
+            if (lane == i - from) own = m;
+        });
+        return own;
     };
-    uint32_t nh = 0, nm = 0;
-    walk([&](int s, bool kept, bool in) {
-        nh += __popc(__ballot_sync(0xffffffffu, in && !kept && s < p.keep));
-        nm += __popc(__ballot_sync(0xffffffffu, kept && s >= p.keep));
-    });
-    uint32_t hole_total, move_total;
-    uint32_t hole = block_exclusive(lane == 0 ? nh : 0, sh.warp_sum, hole_total);
-    uint32_t move = block_exclusive(lane == 0 ? nm : 0, sh.warp_sum, move_total);
-    hole = __shfl_sync(0xffffffffu, hole, 0);
-    move = __shfl_sync(0xffffffffu, move, 0);
-    if (tid == 0) {
-        sh.count[1][0] = hole_total;
-        sh.count[1][1] = move_total;
+    // lane i's chunk: evicted slots below `keep`, kept ones behind it
+    auto hole_bits = [&](int from, uint32_t own) {
+        const int s = r0 + 32 * (from + lane);
+        return ~own & low_bits(r1 - s) & low_bits(p.keep - s);
+    };
+    auto move_bits = [&](int from, uint32_t own) { return own & ~low_bits(p.keep - (r0 + 32 * (from + lane))); };
+
+    constexpr int kGroups = KEYS ? (KEYS + 31) / 32 : 1;     // groups of 32 chunks whose masks stay in registers
+    uint32_t own[kGroups], nh = 0, nm = 0;
+    {
+        uint32_t t = tie;
+        if constexpr (KEYS > 0) {
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                own[i] = kept_rows(32 * i, t);
+                nh += __popc(hole_bits(32 * i, own[i]));
+                nm += __popc(move_bits(32 * i, own[i]));
+            }
+        } else {
+            for (int from = 0; from < chunks; from += 32) {
+                own[0] = kept_rows(from, t);
+                nh += __popc(hole_bits(from, own[0]));
+                nm += __popc(move_bits(from, own[0]));
+            }
+        }
     }
-    lane_sync<CLUSTER>();
+    nh = __reduce_add_sync(0xffffffffu, nh);
+    nm = __reduce_add_sync(0xffffffffu, nm);
+    uint32_t hole_total, move_total;
+    uint32_t hole = warps_exclusive<WARPS>(nh, sh.warp_sum, hole_total);
+    uint32_t move = warps_exclusive<WARPS>(nm, sh.warp_sum, move_total);
     if constexpr (CLUSTER > 1) {
+        if (tid == 0) {
+            sh.count[1][0] = hole_total;
+            sh.count[1][1] = move_total;
+        }
+        cluster_sync();
         const uint32_t a = smem_u32(&sh.count[1][0]);
         for (int r = 0; r < rank; ++r) {
             hole += ld_cluster_u32(mapa(a, r));
             move += ld_cluster_u32(mapa(a + 4, r));
         }
     }
-    if (rank == CLUSTER - 1 && tid == 0) p.counts[id] = move + move_total;   // (warp 0's prefix is the ranks before)
+    if (rank == CLUSTER - 1 && tid == 0) p.counts[id] = move + move_total;   // (warp 0's prefix: the CTAs before)
     int* holes = p.holes + (size_t)id * p.most;
     int* movers = p.movers + (size_t)id * p.most;
-    walk([&](int s, bool kept, bool in) {
-        const bool is_hole = in && !kept && s < p.keep, is_move = kept && s >= p.keep;
-        const unsigned mh = __ballot_sync(0xffffffffu, is_hole), mm = __ballot_sync(0xffffffffu, is_move);
-        if (is_hole) holes[hole + __popc(mh & below)] = s;
-        if (is_move) movers[move + __popc(mm & below)] = s;
-        hole += __popc(mh);
-        move += __popc(mm);
-        if (kept && s < p.keep) {
-            if (copy_w) w_out[s] = w_in[s];
-            if (copy_p) p_out[s] = p_in[s];
+    auto list = [&](int from, uint32_t kept) {
+        const uint32_t hb = hole_bits(from, kept), mb = move_bits(from, kept);
+        // both counts of a chunk in one word: at most 1024 of each in 32 chunks
+        const uint32_t both = __popc(hb) | __popc(mb) << 16;
+        uint32_t incl = both;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
         }
-    });
+        const uint32_t ex = incl - both, sum = __shfl_sync(0xffffffffu, incl, 31);
+        for (unsigned todo = __ballot_sync(0xffffffffu, both != 0); todo; todo &= todo - 1) {
+            const int i = __ffs(todo) - 1;
+            const uint32_t hm = __shfl_sync(0xffffffffu, hb, i), mm = __shfl_sync(0xffffffffu, mb, i);
+            const uint32_t at = __shfl_sync(0xffffffffu, ex, i);
+            const int s = r0 + 32 * (from + i) + lane;
+            if (hm >> lane & 1) holes[hole + (at & 0xffffu) + __popc(hm & below)] = s;
+            if (mm >> lane & 1) movers[move + (at >> 16) + __popc(mm & below)] = s;
+        }
+        hole += sum & 0xffffu;
+        move += sum >> 16;
+        const int firsts = min(min(32, chunks - from), (p.keep - r0 - 32 * from + 31) / 32);   // chunks below `keep`
+        if (copy_w || copy_p)
+#pragma unroll 4
+            for (int i = 0; i < firsts; ++i) {
+                const int s = r0 + 32 * (from + i) + lane;
+                if ((__shfl_sync(0xffffffffu, kept, i) >> lane & 1) && s < p.keep) {
+                    if (copy_w) w_out[s] = __ldg(w_in + s);
+                    if (copy_p) p_out[s] = __ldg(p_in + s);
+                }
+            }
+    };
+    if constexpr (KEYS > 0) {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) list(32 * i, own[i]);
+    } else {
+        uint32_t t = tie;
+        for (int from = 0; from < chunks; from += 32) list(from, kept_rows(from, t));
+    }
     // no CTA of the cluster may end while another still reads its counts
     if constexpr (CLUSTER > 1) cluster_sync();
 }
 
-// Rows holes[j] <- movers[j]: block (32 rows, request and KV head).  A warp
-// takes whole rows; K and V pieces of a row go to its lanes.
-__global__ void __launch_bounds__(kMoveThreads) dsv4_gqa_move_kernel(const __grid_constant__ EvictParams p) {
-    const int tid = threadIdx.x;
+// Rows holes[j] <- movers[j]: a warp copies 16 or 32 of them.  Lane j first
+// finds the places of row j (slot lists and page table, one round trip each
+// for all rows), then the warp copies row after row, PIECES = 16-byte pieces
+// of the K and V rows together, all loads of eight warp-wide copies before
+// their stores.
+template <int PIECES>
+__global__ void __launch_bounds__(kMoveThreads, 8) dsv4_gqa_move_kernel(const __grid_constant__ EvictParams p) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int id = blockIdx.y, b = id / p.c.kv_heads, h = id % p.c.kv_heads;
     grid_dependency_wait();
     grid_dependents_go();
+    const int row = p.req ? __ldg(p.req + b) : b;
+    const bool placed = row >= 0 && row < p.c.table_rows;
     if (blockIdx.x == 0 && h == 0 && tid == 0) {
         int n = __ldg(p.lens + b);
-        n = n < 0 ? 0 : n > p.max_len ? p.max_len : n;
-        const int row = p.req ? __ldg(p.req + b) : b;
-        if (row < 0 || row >= p.c.table_rows) n = 0;
+        n = n < 0 || !placed ? 0 : n > p.max_len ? p.max_len : n;
         p.lens_out[b] = n < p.keep ? n : p.keep;
     }
     const int count = p.counts[id];
-    const int j0 = blockIdx.x * kMoveRows, j1 = min(count, j0 + kMoveRows);
-    if (j0 >= j1) return;
-    const int row = p.req ? __ldg(p.req + b) : b;
-    const int* table = p.c.table + (long long)row * p.c.table_stride;
+    constexpr int kWarpRows = warp_rows(PIECES);
+    const int j0 = (blockIdx.x * (kMoveThreads / 32) + warp) * kWarpRows;
+    if (j0 >= count) return;
+    const int rows = min(kWarpRows, count - j0);
     const int mask = (1 << p.c.page_shift) - 1;
-    const int* holes = p.holes + (size_t)id * p.most;
-    const int* movers = p.movers + (size_t)id * p.most;
-    const size_t at = ((size_t)row * p.c.kv_heads + h) * p.width;
-    const int pieces = 2 * p.row_pieces;                 // K, then V
-    for (int e = tid; e < (j1 - j0) * pieces; e += kMoveThreads) {
-        const int j = j0 + e / pieces, piece = e % pieces;
-        const int dst = holes[j], src = movers[j];
-        const int to = __ldg(table + (dst >> p.c.page_shift)), of = __ldg(table + (src >> p.c.page_shift));
-        if (piece == 0) {
-            if (p.w_out) p.w_out[at + dst] = p.w_in[at + src];
-            if (p.p_out) p.p_out[at + dst] = p.p_in[at + src];
+    long long to = -1, of = -1;              // byte offsets of row j0 + lane
+    if (lane < rows) {
+        const int dst = p.holes[(size_t)id * p.most + j0 + lane], src = p.movers[(size_t)id * p.most + j0 + lane];
+        const int* table = p.c.table + (long long)row * p.c.table_stride;
+        const int tp = __ldg(table + (dst >> p.c.page_shift)), fp = __ldg(table + (src >> p.c.page_shift));
+        const size_t at = ((size_t)row * p.c.kv_heads + h) * p.width;
+        p.w_out[at + dst] = p.w_in[at + src];
+        if (p.p_out) p.p_out[at + dst] = p.p_in[at + src];
+        if (tp < 0 || tp >= p.c.num_pages || fp < 0 || fp >= p.c.num_pages) {
+            atomicOr(p.err, DSV4_DEV_ERR_GQA_PAGE);
+        } else {
+            to = tp * p.c.page_stride + (dst & mask) * p.c.row_stride + h * p.c.head_stride;
+            of = fp * p.c.page_stride + (src & mask) * p.c.row_stride + h * p.c.head_stride;
         }
-        if (to < 0 || to >= p.c.num_pages || of < 0 || of >= p.c.num_pages) {
-            if (piece == 0) atomicOr(p.err, DSV4_DEV_ERR_GQA_PAGE);
-            continue;
+    }
+    // a warp-wide copy moves 32 / PIECES rows, or a part of one
+    constexpr int kRows = PIECES < 32 ? 32 / PIECES : 1, kParts = PIECES < 32 ? 1 : PIECES / 32;
+    constexpr int kBatch = 8 / kParts;
+    const int piece = lane % PIECES, sub = lane / PIECES;
+#pragma unroll 1
+    for (int r = 0; r < rows; r += kRows * kBatch) {
+        uint4 x[kBatch][kParts];
+        auto pool_of = [&](int q) {
+            const int at = piece + 32 * q;
+            return at >= PIECES / 2 ? p.c.v + (at - PIECES / 2) * 16 : p.c.k + at * 16;
+        };
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = r + i * kRows + sub;
+            const long long f = __shfl_sync(0xffffffffu, of, j & 31);
+            if (j < rows && f >= 0)
+#pragma unroll
+                for (int q = 0; q < kParts; ++q) x[i][q] = __ldcs(reinterpret_cast<const uint4*>(pool_of(q) + f));
         }
-        uint8_t* pool = piece < p.row_pieces ? p.c.k : p.c.v;
-        const int x = piece < p.row_pieces ? piece : piece - p.row_pieces;
-        const long long head = h * p.c.head_stride + x * 16;
-        *reinterpret_cast<uint4*>(pool + to * p.c.page_stride + (dst & mask) * p.c.row_stride + head) =
-            __ldcs(reinterpret_cast<const uint4*>(pool + of * p.c.page_stride + (src & mask) * p.c.row_stride + head));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = r + i * kRows + sub;
+            const long long t = __shfl_sync(0xffffffffu, to, j & 31);
+            if (j < rows && t >= 0)
+#pragma unroll
+                for (int q = 0; q < kParts; ++q) *reinterpret_cast<uint4*>(pool_of(q) + t) = x[i][q];
+        }
     }
 }
 
@@ -362,21 +473,42 @@ int layout(const dsv4_gqa_cache* c, int batch, int max_len, int keep, Layout& l)
     return DSV4_OK;
 }
 
+template <int THREADS, int KEYS, int CLUSTER>
+int launch_select_one(const EvictParams& p, void* stream) {
+    return launch(dsv4_gqa_select_kernel<THREADS, KEYS, CLUSTER>, dim3(p.batch * p.c.kv_heads * CLUSTER), THREADS, 0,
+                  stream, CLUSTER, p);
+}
+
+template <int PIECES>
+int launch_move(const EvictParams& p, void* stream) {
+    constexpr int kRows = kMoveThreads / 32 * warp_rows(PIECES);
+    return launch(dsv4_gqa_move_kernel<PIECES>, dim3((p.most + kRows - 1) / kRows, p.batch * p.c.kv_heads),
+                  kMoveThreads, 0, stream, 1, p);
+}
+
 template <int CLUSTER>
-int launch_select(const EvictParams& p, size_t smem, void* stream) {
-    static unsigned long long ready = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSV4_ERR_CUDA;
-    if (!(__atomic_load_n(&ready, __ATOMIC_ACQUIRE) >> dev & 1)) {
-        if (cudaFuncSetAttribute(dsv4_gqa_select_kernel<CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kKeysPerCta * 4) != cudaSuccess) {
-            cudaGetLastError();
-            return DSV4_ERR_CUDA;
-        }
-        __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELEASE);
+int launch_select_cluster(const EvictParams& p, int per, void* stream) {
+    return per <= 8192    ? launch_select_one<512, 16, CLUSTER>(p, stream)
+           : per <= 16384 ? launch_select_one<512, 32, CLUSTER>(p, stream)
+                          : launch_select_one<512, 64, CLUSTER>(p, stream);
+}
+
+// The smallest CTA that holds a row's keys, or a cluster of them: where there
+// are few rows, several CTAs share one, as long as each has 2048 slots or more.
+int launch_select(const EvictParams& p, void* stream) {
+    const int ids = p.batch * p.c.kv_heads;
+    int cluster = 1;
+    while (cluster < kMaxCluster &&
+           (p.max_len > cluster * kHeldKeys || (ids * cluster < 152 && p.max_len > 4096 * cluster)))
+        cluster *= 2;
+    const int per = (p.max_len + cluster - 1) / cluster;
+    if (per > kHeldKeys) return launch_select_one<512, 0, 8>(p, stream);
+    switch (cluster) {
+        case 1: return per <= 4096 ? launch_select_one<256, 16, 1>(p, stream) : launch_select_cluster<1>(p, per, stream);
+        case 2: return launch_select_cluster<2>(p, per, stream);
+        case 4: return launch_select_cluster<4>(p, per, stream);
+        default: return launch_select_cluster<8>(p, per, stream);
     }
-    return launch(dsv4_gqa_select_kernel<CLUSTER>, dim3(p.batch * p.c.kv_heads * CLUSTER), kSelThreads, smem, stream,
-                  CLUSTER, p);
 }
 
 }  // namespace
@@ -429,20 +561,14 @@ int dsv4_gqa_evict(int32_t batch, const int32_t* lens, const int32_t* seq_lens, 
     p.row_pieces = cache->head_dim * (cache->format == DSV4_GQA_E4M3 ? 1 : 2) / 16;
     p.err = err;
 
-    // a cluster per (request, KV head): more CTAs where there are few and long ones
-    const int ids = batch * cache->num_kv_heads;
-    int cluster = 1;
-    while (cluster < kMaxCluster && (max_len > cluster * kKeysPerCta || (ids * cluster < 152 && max_len > 4096 * cluster)))
-        cluster *= 2;
-    const int per = ((max_len + cluster - 1) / cluster + 31) & ~31;
-    p.cached = per <= kKeysPerCta ? per : 0;
-    const size_t smem = (size_t)p.cached * 4;
-    int r = cluster == 1   ? launch_select<1>(p, smem, stream)
-            : cluster == 2 ? launch_select<2>(p, smem, stream)
-            : cluster == 4 ? launch_select<4>(p, smem, stream)
-                           : launch_select<8>(p, smem, stream);
+    const int r = launch_select(p, stream);
     if (r) return r;
-    return launch(dsv4_gqa_move_kernel, dim3((p.most + kMoveRows - 1) / kMoveRows, ids), kMoveThreads, 0, stream, 1, p);
+    switch (p.row_pieces) {
+        case 4: return launch_move<8>(p, stream);
+        case 8: return launch_move<16>(p, stream);
+        case 16: return launch_move<32>(p, stream);
+        default: return launch_move<64>(p, stream);
+    }
 }
 
 }  // extern "C"

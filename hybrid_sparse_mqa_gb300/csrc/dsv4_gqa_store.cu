@@ -1,12 +1,13 @@
 // dsv4_gqa_store.cu - the write of new K and V rows into a grouped-query
 // cache (include/dsv4gqa.h states what is computed).
 //
-// How: the work is n x KV heads x 2 (K and V) rows of head_dim values.  A
-// thread moves 16 values (two 16-byte loads; 32 bytes stored, or 16 e4m3
-// codes), consecutive threads on consecutive pieces of a row, then heads,
-// then tokens, so loads and stores are full lines.  Bound by HBM: 2 bytes
-// read and 2 (or 1) written per value; the indices and the page-table entry
-// are read through L1 by the threads of a token.
+// How: a block stores one head of K or of V for a run of tokens, so that rows
+// of consecutive slots are written as one contiguous stretch; blocks that run
+// together cover all heads of the same tokens, whose rows lie side by side in
+// the input.  A thread moves 16 values of each of kItems tokens (two 16-byte
+// loads; 32 bytes stored, or 16 e4m3 codes), all loads and then all page-table
+// loads before the first store: three round trips per thread, over kItems
+// times the bytes.  Bound by HBM: 2 bytes read and 2 (or 1) written per value.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -17,7 +18,8 @@ namespace dsv4 {
 namespace gqa {
 namespace {
 
-constexpr int kStoreThreads = 256;
+constexpr int kStoreThreads = 128;
+constexpr int kItems = 2;                  // tokens per thread
 
 struct StoreParams {
     Cache c;
@@ -42,66 +44,165 @@ __device__ __forceinline__ float2 widen(uint32_t w) {
         return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// e4m3 codes of two values: the fp32 quotient, nearest code, ties to even,
-// saturating (one rounding to fp32, one to e4m3, as the header states).
-template <int TYPE>
-__device__ __forceinline__ uint32_t codes2(uint32_t w, float scale) {
-    const float2 x = widen<TYPE>(w);
-    return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale)), __NV_SATFINITE,
-                                    __NV_E4M3);
+// Two fp32 values in one 64-bit register (each lane of a packed operation
+// rounds as the scalar one does).
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t e4m3x2(float2 q) {
+    return __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
 }
 
-// One (tensor, token, head, 16-value piece) per thread.
+// The pair w clamped to +-lim (lim: the type's bits, twice), NaN kept.
+template <int TYPE>
+__device__ __forceinline__ uint32_t clamp2(uint32_t w, uint32_t lim) {
+    const uint32_t neg = lim ^ 0x80008000u;
+    if constexpr (TYPE == DSV4_GQA_BF16) {
+        __nv_bfloat162 x = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&lim));
+        x = __hmax2_nan(x, *reinterpret_cast<const __nv_bfloat162*>(&neg));
+        return *reinterpret_cast<uint32_t*>(&x);
+    } else {
+        __half2 x = __hmin2_nan(*reinterpret_cast<__half2*>(&w), *reinterpret_cast<const __half2*>(&lim));
+        x = __hmax2_nan(x, *reinterpret_cast<const __half2*>(&neg));
+        return *reinterpret_cast<uint32_t*>(&x);
+    }
+}
+
+// What the codes of one head need: its scale, and whether the quotients can
+// be had without dividing.
+template <int TYPE>
+struct Packer {
+    float scale;
+    bool fast;
+    uint32_t lim;                          // 512 scale, as a pair of the input's type
+    uint64_t ny2, s2;                      // -RN(1 / scale) and scale, twice
+
+    __device__ __forceinline__ explicit Packer(float s) : scale(s) {
+        fast = TYPE == DSV4_GQA_BF16 ? s >= 0x1p-60f && s <= 0x1p60f : s >= 0x1p-23f && s <= 127.f;
+        const float y = -__frcp_rn(s), l = 512.f * s;
+        if constexpr (TYPE == DSV4_GQA_BF16) {
+            lim = pack_bf16x2(l, l);
+        } else {
+            const __half2 v = __floats2half2_rn(l, l);
+            lim = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        ny2 = f32x2(y, y);
+        s2 = f32x2(s, s);
+    }
+
+    // The e4m3 codes of 16 values: of the correctly rounded fp32 quotients
+    // x / scale, nearest code, ties to even, saturating.  Fast path: values
+    // are first clamped to 512 scale (beyond 448 scale every code saturates),
+    // so nothing overflows, then one Markstein correction of q0 = x y with
+    // y = RN(1 / scale) gives the correctly rounded quotient (residuals are
+    // exact where a code depends on them: quotients below 2^-11 have code 0
+    // either way).  Worked on n = -x: q0 = n (-y), r = q0 scale + n,
+    // q = r (-y) + q0, whose zeros have the sign of x.  Dividing instead took
+    // 19 instructions a value and 114 us for 64 x 1024 tokens of 8 heads; this
+    // takes about 5, and the kernel is bound by memory.
+    __device__ __forceinline__ uint4 codes16(uint4 a, uint4 b) const {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t c[8];
+        if (fast) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 n = widen<TYPE>(clamp2<TYPE>(w[j], lim) ^ 0x80008000u);
+                const uint64_t n2 = f32x2(n.x, n.y);
+                const uint64_t q0 = mul_f32x2(n2, ny2);
+                const uint64_t q = fma_f32x2(fma_f32x2(q0, s2, n2), ny2, q0);
+                float2 v;
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(q));
+                c[j] = e4m3x2(v);
+            }
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                const float2 x = widen<TYPE>(w[j]);
+                c[j] = e4m3x2(make_float2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale)));
+            }
+        }
+        return make_uint4(c[0] | c[1] << 16, c[2] | c[3] << 16, c[4] | c[5] << 16, c[6] | c[7] << 16);
+    }
+};
+
 template <int TYPE, bool PACK, int PIECES>
 __global__ void __launch_bounds__(kStoreThreads) dsv4_gqa_store_kernel(const __grid_constant__ StoreParams p) {
+    constexpr int kTokens = kStoreThreads / PIECES;          // of one item
     grid_dependency_wait();
     grid_dependents_go();
-    const long long id = (long long)blockIdx.x * kStoreThreads + threadIdx.x;
-    const int piece = static_cast<int>(id % PIECES);
-    const long long rest = id / PIECES;
-    const int h = static_cast<int>(rest % p.c.kv_heads);
-    const long long both = rest / p.c.kv_heads;
-    const int which = static_cast<int>(both & 1);
-    const long long i = both >> 1;
-    if (i >= p.n) return;
-    const uint4* src = reinterpret_cast<const uint4*>(p.src[which] + i * p.token_stride[which] +
-                                                      h * p.head_stride[which]) + 2 * piece;
-    const uint4 a = __ldcs(src), b = __ldcs(src + 1);
-    const int r = __ldg(p.req_rows + i), s = __ldg(p.slots + i);
-    const int lp = s >> p.c.page_shift;
-    int page = -1;
-    if (r >= 0 && r < p.c.table_rows && s >= 0 && lp < p.table_width && s < p.width)
-        page = __ldg(p.c.table + (long long)r * p.c.table_stride + lp);
-    if (page < 0 || page >= p.c.num_pages) {
-        if (piece == 0) atomicOr(p.err, DSV4_DEV_ERR_STORE_ROW);
-        return;
+    const int heads2 = 2 * p.c.kv_heads;
+    const int hw = blockIdx.x % heads2, which = hw & 1, h = hw >> 1;
+    const int piece = threadIdx.x % PIECES;
+    const int i0 = blockIdx.x / heads2 * (kTokens * kItems) + threadIdx.x / PIECES;
+    uint4 a[kItems], b[kItems];
+    int r[kItems], s[kItems], page[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int i = i0 + k * kTokens;
+        r[k] = s[k] = -1;
+        if (i < p.n) {
+            const uint4* src = reinterpret_cast<const uint4*>(p.src[which] + i * p.token_stride[which] +
+                                                              h * p.head_stride[which]) + 2 * piece;
+            r[k] = __ldg(p.req_rows + i);
+            s[k] = __ldg(p.slots + i);
+            a[k] = __ldcs(src);
+            b[k] = __ldcs(src + 1);
+        }
     }
-    const long long at = page * p.c.page_stride + h * p.c.head_stride +
-                         (s & ((1 << p.c.page_shift) - 1)) * p.c.row_stride;
-    uint4* dst = reinterpret_cast<uint4*>((which ? p.c.v : p.c.k) + at);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        page[k] = -1;
+        const int lp = s[k] >> p.c.page_shift;
+        if (r[k] >= 0 && r[k] < p.c.table_rows && s[k] >= 0 && lp < p.table_width && s[k] < p.width)
+            page[k] = __ldg(p.c.table + (long long)r[k] * p.c.table_stride + lp);
+    }
+    float scale = 1.f;
     if constexpr (PACK) {
         const float* scales = which ? p.c.v_scale : p.c.k_scale;
-        const float scale = scales ? __ldg(scales + h) : 1.f;
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint32_t c[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = codes2<TYPE>(w[2 * j], scale) | (codes2<TYPE>(w[2 * j + 1], scale) << 16);
-        dst[piece] = make_uint4(c[0], c[1], c[2], c[3]);
-    } else {
-        dst[2 * piece] = a;
-        dst[2 * piece + 1] = b;
+        if (scales) scale = __ldg(scales + h);
     }
-    if (piece == 0 && which == 0) {
-        const long long t = ((long long)r * p.c.kv_heads + h) * p.width + s;
-        if (p.weights) p.weights[t] = 0.f;
-        if (p.positions) p.positions[t] = __ldg(p.token_positions + i);
+    const Packer<TYPE> pack(scale);
+    uint8_t* pool = (which ? p.c.v : p.c.k) + h * p.c.head_stride;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int i = i0 + k * kTokens;
+        if (i >= p.n) break;
+        if (page[k] < 0 || page[k] >= p.c.num_pages) {
+            if (piece == 0) atomicOr(p.err, DSV4_DEV_ERR_STORE_ROW);
+            continue;
+        }
+        uint4* dst = reinterpret_cast<uint4*>(pool + page[k] * p.c.page_stride +
+                                              (s[k] & ((1 << p.c.page_shift) - 1)) * p.c.row_stride);
+        if constexpr (PACK) {
+            dst[piece] = pack.codes16(a[k], b[k]);
+        } else {
+            dst[2 * piece] = a[k];
+            dst[2 * piece + 1] = b[k];
+        }
+        if (piece == 0 && which == 0) {
+            const long long t = ((long long)r[k] * p.c.kv_heads + h) * p.width + s[k];
+            if (p.weights) p.weights[t] = 0.f;
+            if (p.positions) p.positions[t] = __ldg(p.token_positions + i);
+        }
     }
 }
 
 template <int TYPE, bool PACK>
 int launch_store(const StoreParams& p, int head_dim, void* stream) {
-    const long long threads = (long long)p.n * 2 * p.c.kv_heads * (head_dim / 16);
-    const long long blocks = (threads + kStoreThreads - 1) / kStoreThreads;
+    const int tokens = kStoreThreads / (head_dim / 16) * kItems;
+    const long long blocks = ((long long)p.n + tokens - 1) / tokens * 2 * p.c.kv_heads;
     if (blocks > 0x7fffffffLL) return DSV4_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(blocks));
     if (head_dim == 64) return launch(dsv4_gqa_store_kernel<TYPE, PACK, 4>, grid, kStoreThreads, 0, stream, 1, p);

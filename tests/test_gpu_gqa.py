@@ -398,21 +398,26 @@ def test_store_matches(A, kv, q, dim, token_major):
     assert torch.equal(w_d.cpu(), w) and torch.equal(pos_d.cpu(), pos)
 
 
-def test_store_rounds_every_value_as_the_quotient_does(A):
-    # all finite bf16 values, against scales that are not powers of two
-    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF)
-    x = bits[torch.isfinite(bits.float())]
-    x = torch.cat([x, torch.zeros(-len(x) % 128, dtype=BF)]).view(-1, 1, 128)
+@pytest.mark.parametrize("q", [BF, HF])
+def test_store_rounds_every_value_as_the_quotient_does(A, q):
+    # every value of the input's type, against scales that are not powers of two,
+    # among them the first ones that are divided by instead of multiplied
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(q)
+    x = torch.cat([bits, torch.zeros(-len(bits) % 128, dtype=q)]).view(-1, 1, 128)
     n = x.shape[0]
-    for scale in (1.0, 0.02173, 3.7e-3, 1.4142135, 977.3):
-        c = Case(kv=F8, hkv=1, dim=128, rows=1, slots=n, page=256)
+    edges = (2.0 ** -60, 1.3 * 2.0 ** 60, 1e-30) if q == BF else (2.0 ** -23, 127.0, 127.1, 1e-8)
+    for scale in (1.0, 0.02173, 3.7e-3, 1.4142135, 97.3, 1023.7) + edges:
+        c = Case(kv=F8, q=q, hkv=1, dim=128, rows=1, slots=n, page=256)
         c.ks = torch.tensor([scale])
         c.vs = torch.tensor([scale * 1.09])
         cache = c.handle(A)
         A.dsv4_gqa_store(x.cuda(), x.cuda(), torch.zeros(n, dtype=torch.int32).cuda(),
                          torch.arange(n, dtype=torch.int32).cuda(), cache)
         want, _ = _store_reference(c, x, x, [0] * n, list(range(n)))
-        assert np.array_equal(_bits(c.k_d), want[0]) and np.array_equal(_bits(c.v_d), want[1])
+        for got, ref in ((c.k_d, want[0]), (c.v_d, want[1])):
+            g = _bits(got)
+            nan = (ref & 0x7F) == 0x7F                 # (a NaN's sign is not a value)
+            assert np.array_equal((g & 0x7F) == 0x7F, nan) and np.array_equal(g[~nan], ref[~nan]), scale
 
 
 def test_store_of_values_without_a_code(A):
