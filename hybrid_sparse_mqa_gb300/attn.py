@@ -381,38 +381,41 @@ def make_gqa_cache(k_pages, v_pages, page_table, *, k_scale=None, v_scale=None):
     c.v_scale = None if v_scale is None else v_scale.data_ptr()
     c._keep = keep
     c._ref = ctypes.addressof(c)
+    lib()                       # (a descriptor is only good for the library's calls)
     c._index = k_pages.get_device()
-    c._dtype = k_pages.dtype
-    c._tracked = (c.page_table_rows, heads)
+    c._tracked = torch.Size((c.page_table_rows, heads))
     c._slots = page_table.shape[1] * page_size
     c._scale = 1.0 / math.sqrt(dim)
     return c
 
 
-def _raw(x):
-    return None if x is None else x.data_ptr()
+# The checks below are one expression per call where nothing is wrong; which
+# of them failed is worked out only then (a decode step's calls are bound by
+# the host).
+def _is(x, dtype, n, index):
+    return x.dtype is dtype and x.numel() == n and x.is_contiguous() and x.get_device() == index
 
 
-def _i32(name, x, n, index):
-    if x.dtype != torch.int32 or x.numel() != n or not x.is_contiguous() or x.get_device() != index:
-        raise Dsv4Error(f"{name} must be a contiguous int32 tensor of {n} entries on the cache's device")
-    return x.data_ptr()
+def _need(x, name, dtype, n, index):
+    """x is a contiguous `dtype` tensor of n entries on the cache's device."""
+    if not _is(x, dtype, n, index):
+        raise Dsv4Error(f"{name} must be a contiguous {dtype} tensor of {n} entries on the cache's device")
 
 
-def _tracked(name, x, dtype, cache):
-    """[request rows, KV heads, width] contiguous: its pointer."""
-    if x.dtype != dtype or x.dim() != 3 or tuple(x.shape[:2]) != cache._tracked or not x.is_contiguous() \
-            or x.get_device() != cache._index:
+def _width(name, x, dtype, cache):
+    """The width of a [request rows, KV heads, width] contiguous tensor."""
+    if x.dtype is not dtype or x.dim() != 3 or not x.is_contiguous() or x.get_device() != cache._index \
+            or x.shape[:2] != cache._tracked:
         raise Dsv4Error(f"{name} must be a contiguous {dtype} [{cache._tracked[0]}, {cache._tracked[1]}, width] tensor "
                         "on the cache's device")
-    return x.data_ptr()
+    return x.size(2)
 
 
 def _raw_stream(stream, index):
     """The stream's handle; the cache's device has to be the current one, as for every launch."""
     if index < 0 or index != torch.cuda.current_device():
         raise Dsv4Error("the cache must be on the current CUDA device")
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _scratch(workspace, need, cache, stream):
@@ -425,41 +428,50 @@ def _scratch(workspace, need, cache, stream):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _gqa_type(x, cache):
+    """The type code of q, k or v for this cache."""
+    t = _GQA_TYPES.get(x.dtype, DSV4_GQA_E4M3)
+    if t == DSV4_GQA_E4M3 or (cache.format != t and cache.format != DSV4_GQA_E4M3):
+        raise Dsv4Error("rows must be bf16 or f16, and have the cache's type unless that is float8_e4m3fn")
+    return t
+
+
 def dsv4_gqa_store(k, v, req_rows, slots, cache, *, weights=None, positions=None, token_positions=None, stream=None):
     """Write new rows k, v ([n, KV heads, head_dim], bf16 or f16, rows
     contiguous) to slot slots[i] of page-table row req_rows[i] (int32 [n]
     each), packed for an e4m3 cache.  weights (fp32 [request rows, KV heads,
     width]) starts at 0 there, positions (int32, same shape) at
     token_positions[i]."""
-    n = k.shape[0]
-    shape = (n, cache.num_kv_heads, cache.head_dim)
     index = cache._index
-    if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype:
-        raise Dsv4Error("k and v must be bf16 or f16, both alike")
-    if cache._dtype not in (k.dtype, torch.float8_e4m3fn):
-        raise Dsv4Error("k and v must have the cache's type")
-    if tuple(k.shape) != shape or tuple(v.shape) != shape or k.stride(2) != 1 or v.stride(2) != 1 \
-            or k.get_device() != index or v.get_device() != index:
-        raise Dsv4Error(f"k and v must be {list(shape)} tensors with contiguous rows on the cache's device")
-    rp, sp = _i32("req_rows", req_rows, n, index), _i32("slots", slots, n, index)
-    if (positions is None) != (token_positions is None):
-        raise Dsv4Error("positions and token_positions go together")
+    n = k.size(0)
+    kt, kh, k1 = k.stride()
+    vt, vh, v1 = v.stride()
+    type_ = _gqa_type(k, cache)
+    if k.shape != (n, cache.num_kv_heads, cache.head_dim) or v.shape != k.shape or v.dtype is not k.dtype \
+            or k1 != 1 or v1 != 1 or k.get_device() != index or v.get_device() != index:
+        raise Dsv4Error(f"k and v must be {[n, cache.num_kv_heads, cache.head_dim]} tensors of one type with contiguous "
+                        "rows on the cache's device")
+    if n <= 1 or cache.num_kv_heads == 1:         # a dimension of one entry may have any stride
+        kt, vt = (0, 0) if n <= 1 else (kt, vt)
+        kh, vh = (0, 0) if cache.num_kv_heads == 1 else (kh, vh)
+    _need(req_rows, "req_rows", torch.int32, n, index)
+    _need(slots, "slots", torch.int32, n, index)
     wp = pp = tp = None
     width = 0
     if weights is not None:
-        wp, width = _tracked("weights", weights, torch.float32, cache), weights.shape[2]
-    if positions is not None:
-        pp, tp = _tracked("positions", positions, torch.int32, cache), _i32("token_positions", token_positions, n, index)
-        if weights is not None and positions.shape[2] != width:
+        width = _width("weights", weights, torch.float32, cache)
+        wp = weights.data_ptr()
+    if positions is not None and token_positions is not None:
+        w2 = _width("positions", positions, torch.int32, cache)
+        if wp is not None and w2 != width:
             raise Dsv4Error("weights and positions must have one width")
-        width = positions.shape[2]
-    kt, kh, _ = k.stride()
-    vt, vh, _ = v.stride()
-    if n <= 1 or shape[1] == 1:         # a dimension of one entry may have any stride
-        kt, vt = (0, 0) if n <= 1 else (kt, vt)
-        kh, vh = (0, 0) if shape[1] == 1 else (kh, vh)
-    rc = lib().dsv4_gqa_store(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _GQA_TYPES[k.dtype], n, rp, sp, cache._ref,
-                              wp, pp, width, tp, _raw_stream(stream, index))
+        width = w2
+        _need(token_positions, "token_positions", torch.int32, n, index)
+        pp, tp = positions.data_ptr(), token_positions.data_ptr()
+    elif positions is not None or token_positions is not None:
+        raise Dsv4Error("positions and token_positions go together")
+    rc = _lib.dsv4_gqa_store(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, type_, n, req_rows.data_ptr(),
+                             slots.data_ptr(), cache._ref, wp, pp, width, tp, _raw_stream(stream, index))
     if rc:
         _check(rc)
 
@@ -476,53 +488,60 @@ def dsv4_gqa_decode(q, lens, cache, *, sink=None, scale=None, window=0, max_len=
     fine), lens int32 [batch].  Returns (out, lse).  With weights (fp32
     [request rows, KV heads, width]) every cached row's weight is accumulated
     into weights_out, by default in place."""
-    if q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16) or q.get_device() != cache._index:
-        raise Dsv4Error("q must be a bf16 or f16 [batch, heads, head_dim] tensor on the cache's device")
-    batch, heads, dim = q.shape
-    if cache._dtype not in (q.dtype, torch.float8_e4m3fn):
-        raise Dsv4Error("q must have the cache's type")
-    if dim != cache.head_dim or q.stride(2) != 1 or (heads > 1 and q.stride(1) != dim):
-        raise Dsv4Error(f"q's rows must be heads of {cache.head_dim} contiguous values, one behind the other")
     index = cache._index
-    lp = _i32("lens", lens, batch, index)
-    rp = None if req_pool_indices is None else _i32("req_pool_indices", req_pool_indices, batch, index)
-    if rp is None and batch > cache.page_table_rows:
+    type_ = _gqa_type(q, cache)
+    if q.dim() != 3 or q.get_device() != index:
+        raise Dsv4Error("q must be a [batch, heads, head_dim] tensor on the cache's device")
+    batch, heads, dim = q.shape
+    qs, q2, q1 = q.stride()
+    if dim != cache.head_dim or q1 != 1 or (q2 != dim and heads > 1):
+        raise Dsv4Error(f"q's rows must be heads of {cache.head_dim} contiguous values, one behind the other")
+    _need(lens, "lens", torch.int32, batch, index)
+    rp = None
+    if req_pool_indices is not None:
+        _need(req_pool_indices, "req_pool_indices", torch.int32, batch, index)
+        rp = req_pool_indices.data_ptr()
+    elif batch > cache.page_table_rows:
         raise Dsv4Error("without req_pool_indices the page table needs a row for every request")
-    if sink is not None and (sink.dtype != torch.float32 or sink.numel() != heads or not sink.is_contiguous()
-                             or sink.get_device() != index):
-        raise Dsv4Error(f"sink must be a contiguous fp32 tensor of {heads} entries on the cache's device")
+    sp = None
+    if sink is not None:
+        _need(sink, "sink", torch.float32, heads, index)
+        sp = sink.data_ptr()
     if max_len is None:
         max_len = cache._slots
     wp = op = None
     width = 0
     if weights is not None:
-        wp, width = _tracked("weights", weights, torch.float32, cache), weights.shape[2]
-        op = wp
+        width = _width("weights", weights, torch.float32, cache)
+        wp = op = weights.data_ptr()
         if weights_out is not None:
-            op = _tracked("weights_out", weights_out, torch.float32, cache)
-            if weights_out.shape[2] != width:
+            if _width("weights_out", weights_out, torch.float32, cache) != width:
                 raise Dsv4Error("weights and weights_out must have one width")
+            op = weights_out.data_ptr()
         if max_len > width:
             raise Dsv4Error("weights must be at least max_len wide")
     elif weights_out is not None:
         raise Dsv4Error("weights_out goes with weights")
     if out is None:
         out = torch.empty(batch, heads, dim, dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.get_device() != index:
+        if stream is not None:
+            out.record_stream(stream)
+    elif out.shape != q.shape or not _is(out, q.dtype, batch * heads * dim, index):
         raise Dsv4Error("out must be a contiguous tensor like q")
     if lse is None:
         lse = torch.empty(batch, heads, dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or lse.numel() != batch * heads or not lse.is_contiguous() \
-            or lse.get_device() != index:
-        raise Dsv4Error("lse must be a contiguous fp32 [batch, heads] tensor on the cache's device")
+        if stream is not None:
+            lse.record_stream(stream)
+    else:
+        _need(lse, "lse", torch.float32, batch * heads, index)
     if batch == 0:
         return out, lse
     need = 0 if workspace is not None else dsv4_gqa_decode_workspace_size(cache, batch, heads, max_len, wp is not None)
     workspace, have = _scratch(workspace, need, cache, stream)
-    rc = lib().dsv4_gqa_decode(q.data_ptr(), q.stride(0) if batch > 1 else heads * dim, _GQA_TYPES[q.dtype], batch,
-                               heads, lp, rp, cache._ref, window, max_len, _raw(sink),
-                               cache._scale if scale is None else scale, wp, op, width, decay, out.data_ptr(),
-                               lse.data_ptr(), workspace.data_ptr(), have, _raw_stream(stream, index))
+    rc = _lib.dsv4_gqa_decode(q.data_ptr(), qs if batch > 1 else heads * dim, type_, batch, heads, lens.data_ptr(), rp,
+                              cache._ref, window, max_len, sp, cache._scale if scale is None else scale, wp, op, width,
+                              decay, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), have,
+                              _raw_stream(stream, index))
     if rc:
         _check(rc)
     return out, lse
@@ -541,25 +560,34 @@ def dsv4_gqa_evict(lens, cache, weights, keep, *, seq_lens=None, positions=None,
     that stay but stand behind the bound move into the freed slots, with their
     weights and positions (in place unless weights_out / positions_out are
     given).  Returns lens_out (a new tensor unless given; may be lens)."""
-    batch = lens.numel()
     index = cache._index
-    lp = _i32("lens", lens, batch, index)
-    np_ = None if seq_lens is None else _i32("seq_lens", seq_lens, batch, index)
-    rp = None if req_pool_indices is None else _i32("req_pool_indices", req_pool_indices, batch, index)
-    if rp is None and batch > cache.page_table_rows:
+    batch = lens.numel()
+    _need(lens, "lens", torch.int32, batch, index)
+    np_ = rp = None
+    if seq_lens is not None:
+        _need(seq_lens, "seq_lens", torch.int32, batch, index)
+        np_ = seq_lens.data_ptr()
+    if req_pool_indices is not None:
+        _need(req_pool_indices, "req_pool_indices", torch.int32, batch, index)
+        rp = req_pool_indices.data_ptr()
+    elif batch > cache.page_table_rows:
         raise Dsv4Error("without req_pool_indices the page table needs a row for every request")
-    wp, width = _tracked("weights", weights, torch.float32, cache), weights.shape[2]
-    op = wp
+    width = _width("weights", weights, torch.float32, cache)
+    wp = op = weights.data_ptr()
+    same = True
     if weights_out is not None:
-        op = _tracked("weights_out", weights_out, torch.float32, cache)
+        same = _width("weights_out", weights_out, torch.float32, cache) == width
+        op = weights_out.data_ptr()
     pp = qp = None
     if positions is not None:
-        pp = qp = _tracked("positions", positions, torch.int32, cache)
+        same = same and _width("positions", positions, torch.int32, cache) == width
+        pp = qp = positions.data_ptr()
         if positions_out is not None:
-            qp = _tracked("positions_out", positions_out, torch.int32, cache)
+            same = same and _width("positions_out", positions_out, torch.int32, cache) == width
+            qp = positions_out.data_ptr()
     elif positions_out is not None:
         raise Dsv4Error("positions_out goes with positions")
-    if any(x is not None and x.shape[2] != width for x in (weights_out, positions, positions_out)):
+    if not same:
         raise Dsv4Error("weights and positions must have one width")
     if max_len is None:
         max_len = min(cache._slots, width)
@@ -567,13 +595,16 @@ def dsv4_gqa_evict(lens, cache, weights, keep, *, seq_lens=None, positions=None,
         raise Dsv4Error("weights must be at least max_len wide")
     if lens_out is None:
         lens_out = torch.empty_like(lens)
-    ep = _i32("lens_out", lens_out, batch, index)
+        if stream is not None:
+            lens_out.record_stream(stream)
+    else:
+        _need(lens_out, "lens_out", torch.int32, batch, index)
     if batch == 0:
         return lens_out
     need = 0 if workspace is not None else dsv4_gqa_evict_workspace_size(cache, batch, max_len, keep)
     workspace, have = _scratch(workspace, need, cache, stream)
-    rc = lib().dsv4_gqa_evict(batch, lp, np_, rp, cache._ref, max_len, keep, first, recent, wp, op, pp, qp, width, ep,
-                              workspace.data_ptr(), have, _raw_stream(stream, index))
+    rc = _lib.dsv4_gqa_evict(batch, lens.data_ptr(), np_, rp, cache._ref, max_len, keep, first, recent, wp, op, pp, qp,
+                             width, lens_out.data_ptr(), workspace.data_ptr(), have, _raw_stream(stream, index))
     if rc:
         _check(rc)
     return lens_out

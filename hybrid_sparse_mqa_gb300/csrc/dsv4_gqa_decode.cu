@@ -8,28 +8,28 @@ namespace dsv4 {
 namespace gqa {
 namespace {
 
-constexpr int kJoinThreads = 256;
 constexpr int kWeightThreads = 256;
 constexpr int kWeightSlots = 4;            // slots per thread
 constexpr int kMinTiles = 2;               // per share: below, more warps would not shorten the chain of loads
 
 // Joins the pieces of cut segments.  With M = max_i m_i,
 //   out = sum_i 2^(m_i - M) o_i / (sum_i 2^(m_i - M) l_i + sink term).
-// Block (segment, 8 / PW heads): PW warps per head share its pieces, so that a
-// long segment's many pieces are read at once (PW = 8) and short segments do
-// not cost a block per head (PW = 1).  Every block finds its segment's tiles
+// Block (segment, 8 / PW heads or one): PW warps per head share its pieces, so
+// that a long segment's many pieces are read at once (PW = 8, or 16) and short
+// segments do not cost a block per head (PW = 1).  Every block finds its segment's tiles
 // from the lengths, as the attention kernel did; that part runs before the
 // wait for it (the attention kernel itself starts behind the call's inputs,
 // and only then lets this one go).  Requests without rows get their output
 // here.
 template <int D, int TT, int HEADS, int PW>
-__global__ void __launch_bounds__(kJoinThreads) dsv4_gqa_join_kernel(const __grid_constant__ DecodeParams p) {
-    constexpr int kHeads = 8 / PW;             // per block
+__global__ void __launch_bounds__(PW > 8 ? PW * 32 : 256) dsv4_gqa_join_kernel(const __grid_constant__ DecodeParams p) {
+    constexpr int kHeads = PW < 8 ? 8 / PW : 1;              // per block
+    constexpr int kThreads = PW * kHeads * 32;
     constexpr int V = D / 32;                  // values per lane
-    __shared__ unsigned s_sum[2][kJoinThreads / 32];
-    __shared__ int s_near[2][kJoinThreads / 32];
-    __shared__ float2 s_ml[8];
-    __shared__ float s_o[PW > 1 ? 8 : 1][PW > 1 ? D : 1];
+    __shared__ unsigned s_sum[2][kThreads / 32];
+    __shared__ int s_near[2][kThreads / 32];
+    __shared__ float2 s_ml[PW * kHeads];
+    __shared__ float s_o[PW > 1 ? PW : 1][PW > 1 ? D : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hcs = p.c.kv_heads * p.chunks;
     const int b = blockIdx.x / hcs, hc = blockIdx.x % hcs;
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kJoinThreads) dsv4_gqa_join_kernel(const __gri
     const Request rq = read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, err);
     const Range rg = key_range<TT>(p, rq.n);
     const bool link = p.info && hc == 0 && blockIdx.y == 0;
-    for (int e = tid; e < p.batch; e += kJoinThreads) {
+    for (int e = tid; e < p.batch; e += kThreads) {
         const Request x = read_request(p.lens, p.req, p.c.table_rows, p.max_len, e, err);
         const unsigned cnt = key_range<TT>(p, x.n).tiles * hcs;
         total += cnt;
@@ -64,11 +64,18 @@ __global__ void __launch_bounds__(kJoinThreads) dsv4_gqa_join_kernel(const __gri
     __syncthreads();
     before = total = 0;
 #pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         before += s_sum[0][w];
         total += s_sum[1][w];
         next = min(next, s_near[0][w]);
         earlier |= s_near[1][w];
+    }
+    int c0 = 0, c1 = 0;
+    if (rg.tiles > 0) {
+        const Shares shares = make_shares(p, total);
+        const unsigned seg = before + hc * rg.tiles;
+        c0 = share_of(shares, seg);
+        c1 = share_of(shares, seg + rg.tiles - 1);
     }
     grid_dependency_wait();
     grid_dependents_go();
@@ -92,15 +99,12 @@ __global__ void __launch_bounds__(kJoinThreads) dsv4_gqa_join_kernel(const __gri
         }
         return;
     }
-    const int shares = share_count(p, total);
-    const unsigned seg = before + hc * rg.tiles;
-    const int c0 = share_of(total, shares, seg), c1 = share_of(total, shares, seg + rg.tiles - 1);
     if (c0 == c1) return;
     const int pieces = c1 - c0 + 1;
     float a[V] = {}, mx = kNoMax, l = 0.f;
     if (mine) {
         // this warp's pieces, kBatch at a time; the reference moves between batches
-        constexpr int kBatch = 4;
+        constexpr int kBatch = V > 4 ? 4 : 8;
         for (int i0 = warp % PW; i0 < pieces; i0 += PW * kBatch) {
             float2 ml[kBatch];
             float x[kBatch][V];
@@ -145,25 +149,36 @@ __global__ void __launch_bounds__(kJoinThreads) dsv4_gqa_join_kernel(const __gri
         }
     }
     if constexpr (PW > 1) {
+        // dims over the block's first D threads, each adding up its dim of all warps
         if (lane == 0) s_ml[warp] = make_float2(mx, l);
 #pragma unroll
         for (int q = 0; q < V; ++q) s_o[warp][lane * V + q] = a[q];
         __syncthreads();
-        if (warp % PW) return;
-        float top = kNoMax;
+        if (tid >= D || !mine) return;
+        mx = kNoMax;
 #pragma unroll
-        for (int w = 0; w < PW; ++w) top = fmaxf(top, s_ml[warp + w].x);
+        for (int w = 0; w < PW; ++w) mx = fmaxf(mx, s_ml[w].x);
         l = 0.f;
-#pragma unroll
-        for (int q = 0; q < V; ++q) a[q] = 0.f;
+        float x = 0.f;
 #pragma unroll
         for (int w = 0; w < PW; ++w) {
-            const float f = fast_exp2(s_ml[warp + w].x - top);
-            l += f * s_ml[warp + w].y;
-#pragma unroll
-            for (int q = 0; q < V; ++q) a[q] += f * s_o[warp + w][lane * V + q];
+            const float f = fast_exp2(s_ml[w].x - mx);
+            l += f * s_ml[w].y;
+            x += f * s_o[w][tid];
         }
-        mx = top;
+        const float top = fmaxf(mx, sk);
+        const float f = fast_exp2(mx - top);
+        l = l * f + fast_exp2(sk - top);
+        const bool any = l > 0.f || l != l;
+        x *= any ? (p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f) * f / l : 0.f;
+        const uint32_t w2 = p.q_bf16 ? pack2<true>(x, 0.f) : pack2<false>(x, 0.f);
+        static_cast<uint16_t*>(p.out)[at * D + tid] = static_cast<uint16_t>(w2);
+        if (tid == 0) {
+            const float l2 = any ? top + log2f(l) : -INFINITY;
+            if (p.lse) p.lse[at] = l2 * kLn2;
+            if (p.lse2) p.lse2[at] = l2;
+        }
+        return;
     }
     if (!mine) return;
     const float top = fmaxf(mx, sk);
@@ -264,7 +279,7 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 struct Plan {
     int group, nt, chunks, tt;
     long long tiles;                       // bound on the tile list
-    int ctas;                              // grid of the attention kernel
+    int ctas, claims;                      // resident CTAs of the attention kernel, and claimable ones
     size_t part_o, part_ml, lse2, info, logits, bytes;      // offsets, size
 };
 
@@ -285,7 +300,8 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
     const int most = c->head_dim * (c->format == DSV4_GQA_E4M3 ? 1 : 2) > 256 ? kMaxCtas / 2 : kMaxCtas;
     const long long want = pl.tiles / kMinTiles;
     pl.ctas = want < 1 ? 1 : (want < most ? static_cast<int>(want) : most);
-    const size_t entries = size_t(2) * pl.ctas * kWarps * 8 * pl.nt;
+    pl.claims = pl.ctas == most && pl.tiles >= (long long)most * kWarps * kClaimTiles ? 3 * most : 0;
+    const size_t entries = size_t(2) * (pl.ctas + pl.claims) * kWarps * 8 * pl.nt;
     pl.part_o = 0;
     pl.part_ml = pl.part_o + up256(entries * c->head_dim * sizeof(float));
     pl.lse2 = pl.part_ml + up256(entries * sizeof(float2));
@@ -298,9 +314,13 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
 template <int D, int TT, int HEADS>
 int launch_join_heads(const DecodeParams& p, void* stream) {
     const unsigned segments = p.batch * p.c.kv_heads * p.chunks;
-    if (segments * HEADS < 2048)
-        return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 8>, dim3(segments, HEADS), kJoinThreads, 0, stream, 1, p);
-    return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 1>, dim3(segments, HEADS / 8), kJoinThreads, 0, stream, 1, p);
+    // pieces of a segment, if all are about as long
+    const unsigned pieces = (p.warps + p.claims * kWarps) / segments + 1;
+    if (pieces > 96)
+        return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 16>, dim3(segments, HEADS), 512, 0, stream, 1, p);
+    if (pieces > 32)
+        return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 8>, dim3(segments, HEADS), 256, 0, stream, 1, p);
+    return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 1>, dim3(segments, HEADS / 8), 256, 0, stream, 1, p);
 }
 
 template <int D, int TT>
@@ -377,6 +397,7 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     p.decay = decay;
     p.min_tiles = kMinTiles;
     p.warps = pl.ctas * kWarps;
+    p.claims = pl.claims;
     p.err = err;
 
     const int d = cache->head_dim;

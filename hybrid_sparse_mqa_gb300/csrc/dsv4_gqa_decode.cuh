@@ -42,6 +42,16 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;           // reference of a head that has seen no score
 constexpr int kWarps = 4;                  // warps per CTA
 constexpr int kMaxCtas = 304;              // resident at once: two per SM
+// What the three rounds take of a warp's part of a long list, in 32nds.  Taking
+// a share costs a piece to write and join and some stalled loads: 32 x
+// 2048..32768 rows (230 tiles per warp) go from 352 to 336 us, 2 x 131072 rows
+// (108) from 171 to 170, while 64 x 1024..16384 e4m3 rows (34) would go from 99
+// to 111.
+constexpr int kPart1 = 4, kPart2 = 1, kPart3 = 1;
+constexpr int kClaimTiles = 64;            // a list is long from so many tiles per resident warp
+constexpr int kClaimAhead = 6;             // tiles before the end of a share at which the next is asked for
+constexpr int kClaimRing = 16;             // claims that a warp may be behind another of its CTA
+constexpr int kWaitLimit = 1 << 20;        // polls before a claim is given up
 struct DecodeParams {
     Cache c;
     const void* q;
@@ -68,7 +78,8 @@ struct DecodeParams {
     long long width;
     float decay;
     int min_tiles;                         // a share has at least this many tiles (where there are as many)
-    int warps;                             // of the grid: shares, at most
+    int warps;                             // of the resident CTAs
+    int claims;                            // CTAs of the grid behind those, to be claimed (0: none)
     unsigned int* err;
 };
 
@@ -86,17 +97,43 @@ __device__ __forceinline__ Range key_range(const DecodeParams& p, int n) {
     return r;
 }
 
-// How many warps share `total` tiles, and the list index that share i begins at.
-__device__ __forceinline__ int share_count(const DecodeParams& p, unsigned total) {
+// How the list's `total` tiles are shared out: n parts of q tiles each (the
+// first r one more), each a share; or, where u > 0, each part four shares, of
+// which the last three hold kPart1 u, kPart2 u and kPart3 u tiles.  Shares are
+// numbered in the order of the list.
+struct Shares {
+    int count, n;
+    unsigned q, r, u;
+};
+__device__ __forceinline__ Shares make_shares(const DecodeParams& p, unsigned total) {
+    Shares s;
+    const bool cut = p.claims && total >= (unsigned)p.warps * kClaimTiles;
     const unsigned most = total / p.min_tiles;
-    return most < 1u ? 1 : (most > (unsigned)p.warps ? p.warps : (int)most);
+    s.n = cut ? p.warps : most < 1u ? 1 : (most > (unsigned)p.warps ? p.warps : (int)most);
+    s.q = total / s.n;
+    s.r = total - s.q * s.n;
+    s.u = cut ? s.q / 32 : 0u;
+    s.count = cut ? 4 * s.n : s.n;
+    return s;
 }
-__device__ __forceinline__ unsigned share_begin(unsigned total, int shares, int i) {
-    return static_cast<unsigned>(static_cast<unsigned long long>(total) * i / shares);
+// The list index that share i begins at.
+__device__ __forceinline__ unsigned share_begin(const Shares& s, int i) {
+    const unsigned part = s.u ? i >> 2 : i, level = s.u ? i & 3 : 0;
+    if (level == 0) return part * s.q + min(part, s.r);
+    const unsigned behind = level == 1 ? kPart1 + kPart2 + kPart3 : level == 2 ? kPart2 + kPart3 : kPart3;
+    return (part + 1) * s.q + min(part + 1, s.r) - behind * s.u;
 }
-// The share that tile t lies in: the largest i with total i / shares < t + 1.
-__device__ __forceinline__ int share_of(unsigned total, int shares, unsigned t) {
-    return static_cast<int>((static_cast<unsigned long long>(t + 1) * shares - 1) / total);
+// The share that tile t lies in.
+__device__ __forceinline__ int share_of(const Shares& s, unsigned t) {
+    const unsigned longer = s.r * (s.q + 1);
+    const unsigned part = t < longer ? t / (s.q + 1) : s.r + (t - longer) / s.q;
+    if (!s.u) return static_cast<int>(part);
+    const unsigned left = (part + 1) * s.q + min(part + 1, s.r) - t;         // tiles to the end of the part
+    const int level = left > (kPart1 + kPart2 + kPart3) * s.u ? 0
+                      : left > (kPart2 + kPart3) * s.u        ? 1
+                      : left > kPart3 * s.u                   ? 2
+                                                              : 3;
+    return static_cast<int>(4 * part) + level;
 }
 // The workspace entry of share i's piece of a cut segment: one that begins
 // with its segment can only be the share's last, any other its first.
@@ -166,6 +203,29 @@ __device__ __forceinline__ void cp_async_wait_group() {
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
+// Asks for a CTA of the grid that has not been launched; the answer's 16 bytes
+// land at `result` and complete on `bar`.
+__device__ __forceinline__ void claim_submit(uint32_t result, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     result),
+                 "r"(bar)
+                 : "memory");
+}
+// The index of the CTA that was taken over, or -1 if none was left.
+__device__ __forceinline__ int claim_result(uint32_t result) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b128 r;\n"
+        " ld.shared.b128 r, [%2];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+        " selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+        : "=r"(ok), "=r"(x)
+        : "r"(result)
+        : "memory");
+    return ok ? static_cast<int>(x) : -1;
+}
+
 // ---------------------------------------------------------------- shape
 // KIND: DSV4_GQA_BF16 / F16 / E4M3.  A warp's stage is TT rows of K and of V.
 template <int KIND_, int D_, int NT_>
@@ -183,7 +243,10 @@ struct Shape {
     static constexpr int STAGES = 3;
     static constexpr int CTAS = TILE_BYTES > 4096 ? 1 : 2;   // per SM (what shared memory holds)
     static constexpr int RING_BYTES = W * STAGES * 2 * TILE_BYTES;
-    static constexpr int SMEM = RING_BYTES;
+    // queries of a segment, a row per head (16 bytes of padding spread the rows over the banks where there is room)
+    static constexpr int QROW = D * 2 + (NT == 1 ? 16 : 0);
+    static constexpr int Q_BYTES = HEADS * QROW;
+    static constexpr int SMEM = RING_BYTES + W * Q_BYTES;
     static constexpr int PPR = ROWB / 16;                    // 16-byte pieces per row
     static constexpr int RPI = 32 / PPR;                     // rows per warp-wide copy
 };
@@ -227,6 +290,34 @@ struct Cursor {
     __device__ __forceinline__ void bound(unsigned t1) {
         end = seg + rg.tiles < t1 ? seg + rg.tiles : t1;
     }
+    // finds the segment of list index `at`; the whole warp (lane's requests: early, later(32 + lane), ...)
+    template <class F>
+    __device__ __forceinline__ void locate(const DecodeParams& p, int hcs, int lane, const Request& early, F&& later) {
+        unsigned run = 0;
+        for (int from = 0;; from += 32) {
+            const Request mine = from ? later(from + lane) : early;
+            const unsigned cnt = key_range<TT>(p, mine.n).tiles * hcs;
+            unsigned incl = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const unsigned here = __ballot_sync(0xffffffffu, at < run + incl);
+            if (here || from + 32 >= p.batch) {
+                const int i = here ? __ffs(here) - 1 : 0;
+                b = from + i;
+                seg = run + __shfl_sync(0xffffffffu, incl - cnt, i);
+                rq.row = __shfl_sync(0xffffffffu, mine.row, i);
+                rq.n = __shfl_sync(0xffffffffu, mine.n, i);
+                break;
+            }
+            run += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        rg = key_range<TT>(p, rq.n);
+        hc = rg.tiles > 0 ? static_cast<int>((at - seg) / rg.tiles) : 0;
+        seg += hc * rg.tiles;
+    }
     // to the next segment that has tiles; false at the end of the share
     __device__ __forceinline__ bool next_segment(const DecodeParams& p, int hcs, unsigned t1) {
         if (end >= t1) return false;
@@ -247,112 +338,153 @@ template <class S>
 __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int D = S::D, NT = S::NT, W = S::W, TT = S::TT, MT = S::MT, DT = S::DT, HEADS = S::HEADS;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ unsigned s_scan[W];
-    __shared__ unsigned s_seg[W];                 // where each share begins: list index of the request's first tile
-    __shared__ int s_b[W];                        // and the request
     __shared__ int s_ok[W][S::STAGES];            // a bit per 16-slot group: its page is in the pool
+    // CTAs whose shares this one has taken, in order (-1: there are no more), how many entries are there, and which
+    // each warp computes; one request is on its way at a time, its sender holds the lock
+    __shared__ int s_cta[kClaimRing], s_known, s_done[W], s_lock, s_phase;
+    __shared__ __align__(16) uint8_t s_answer[16];
+    __shared__ __align__(8) uint64_t s_bar;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     const int hcs = p.c.kv_heads * p.chunks;
+    const uint32_t bar = smem_u32(&s_bar);
+    if (tid == 0) {
+        s_cta[0] = blockIdx.x;
+        s_known = 1;
+        s_lock = s_phase = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) s_done[w] = 0;
+        mbar_init(bar, 1);
+        fence_mbar_init_cluster();
+    }
+    __syncthreads();
     grid_dependency_wait();
     grid_dependents_go();
 
-    // ---- total tiles, and the request that this share begins in ----
-    unsigned err = 0, total = 0, mine0 = 0, cnt0 = 0;
-    const int rounds = (p.batch + W * 32 - 1) / (W * 32);
-    for (int k = 0; k < rounds; ++k) {
-        const int b = k * W * 32 + tid;
-        unsigned cnt = 0;
-        if (b < p.batch)
-            cnt = key_range<TT>(p, read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, err).n).tiles * hcs;
-        unsigned incl = cnt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) s_scan[warp] = incl;
-        __syncthreads();
-        unsigned base = total;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            if (w < warp) base += s_scan[w];
-            total += s_scan[w];
-        }
-        mine0 = base + incl - cnt;
-        cnt0 = cnt;
-        __syncthreads();
-    }
-    if (err && blockIdx.x == 0) atomicOr(p.err, err);
-    if (total == 0) return;
-    const int shares = share_count(p, total);
-    // warps of one CTA take shares far apart, so that few shares spread over all SMs
-    auto share_id = [&](int w) { return w * gridDim.x + blockIdx.x; };
-    auto find = [&](unsigned base, unsigned cnt, int b) {
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            if ((int)share_id(w) >= shares) continue;
-            const unsigned t = share_begin(total, shares, share_id(w));
-            if (t >= base && t < base + cnt) {
-                s_b[w] = b;
-                s_seg[w] = base;
-            }
-        }
+    // one request per lane; the first 32 stay in registers
+    unsigned err = 0;
+    auto request_of = [&](int b) {
+        Request r{0, 0};
+        return b < p.batch ? read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, err) : r;
     };
-    if (rounds == 1) {
-        find(mine0, cnt0, tid);
-    } else {
-        unsigned run = 0;
-        for (int k = 0; k < rounds; ++k) {
-            const int b = k * W * 32 + tid;
-            unsigned cnt = 0;
-            if (b < p.batch)
-                cnt = key_range<TT>(p, read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, err).n).tiles * hcs;
-            unsigned incl = cnt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (lane == 31) s_scan[warp] = incl;
-            __syncthreads();
-            unsigned base = run;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                if (w < warp) base += s_scan[w];
-                run += s_scan[w];
-            }
-            find(base + incl - cnt, cnt, b);
-            __syncthreads();
-        }
+    const Request early = request_of(lane);
+    unsigned total = key_range<TT>(p, early.n).tiles;
+    for (int b = lane + 32; b < p.batch; b += 32) total += key_range<TT>(p, request_of(b).n).tiles;
+    total = __reduce_add_sync(0xffffffffu, total) * hcs;
+    if (err && blockIdx.x == 0 && warp == 0) atomicOr(p.err, err);
+    if (total == 0) return;
+    const Shares shares = make_shares(p, total);
+    // warps of one resident CTA take shares far apart, so that few shares spread over all SMs
+    const int ctas = p.warps / W;
+    auto share_id = [&](int cta) {
+        if (cta < ctas) return (warp * ctas + cta) * (shares.u ? 4 : 1);
+        const int j = (cta - ctas) * W + warp;
+        return shares.u ? j % p.warps * 4 + 1 + j / p.warps : shares.count;      // (short list: nothing)
+    };
+    const int first = share_id(blockIdx.x);
+    if (first >= shares.count) {
+        if (lane == 0) *(volatile int*)&s_done[warp] = 0x3fffffff;
+        return;
     }
-    __syncthreads();
-    const int share = share_id(warp);
-    if (share >= shares) return;
-    const unsigned t0 = share_begin(total, shares, share), t1 = share_begin(total, shares, share + 1);
+
+    // Entry k of s_cta for this warp, -2 while it is not known.  The first warp to ask for it sends the request; no
+    // call waits.  (The whole warp calls.)
+    bool sent = false;                            // by this warp's lane 0, answer outstanding
+    auto taken = [&](int k) {
+        int got = -2;
+        if (lane == 0) {
+            volatile int *known = &s_known, *phase = &s_phase, *done = s_done;
+            if (!sent && *known <= k && atomicCAS(&s_lock, 0, 1) == 0) {
+                __threadfence_block();
+                bool room = *known == k;          // (not answered meanwhile, and no warp a ring behind)
+#pragma unroll
+                for (int w = 0; w < W; ++w) room &= done[w] + kClaimRing > k;
+                if (room) {
+                    fence_proxy_async();
+                    mbar_arrive_expect_tx(bar, 16);
+                    claim_submit(smem_u32(s_answer), bar);
+                    sent = true;
+                } else {
+                    atomicExch(&s_lock, 0);
+                }
+            }
+            if (sent && mbar_test(bar, *phase)) {
+                *(volatile int*)&s_cta[k % kClaimRing] = claim_result(smem_u32(s_answer));
+                *phase ^= 1;
+                __threadfence_block();
+                *known = k + 1;
+                __threadfence_block();
+                atomicExch(&s_lock, 0);
+                sent = false;
+            }
+            if (*known > k) {
+                __threadfence_block();
+                got = *(volatile int*)&s_cta[k % kClaimRing];
+            }
+        }
+        return __shfl_sync(0xffffffffu, got, 0);
+    };
 
     Cursor<TT> cons;
-    cons.b = s_b[warp];
-    cons.load(p);
-    cons.at = t0;
-    cons.hc = static_cast<int>((cons.at - s_seg[warp]) / cons.rg.tiles);
-    cons.seg = s_seg[warp] + cons.hc * cons.rg.tiles;
-    cons.bound(t1);
+    unsigned c1 = share_begin(shares, first + 1);
+    {
+        cons.at = share_begin(shares, first);
+        cons.locate(p, hcs, lane, early, request_of);
+        cons.bound(c1);
+    }
 
     // ---- the copying side ----
     const uint32_t ring = smem_u32(smem) + warp * (S::STAGES * 2 * S::TILE_BYTES);
     const int lane_row = lane / S::PPR, lane_piece = lane % S::PPR;
     const long long lane_off = lane_row * p.c.row_stride + lane_piece * 16;
     const int page_mask = (1 << p.c.page_shift) - 1;
+    // the K scale of cons's KV head, loaded as soon as cons comes to it: ahead of the copies
+    auto load_kscale = [&]() { return S::FP8 && p.c.k_scale ? __ldg(p.c.k_scale + cons.hc / p.chunks) : 1.f; };
+    float kscale = load_kscale();
     Cursor<TT> prod = cons;
+    unsigned p1 = c1;
+    int entry_p = 0, next_p = -2;                  // prod's entry of s_cta; the one behind it, once it is known
+    bool asking = false;
     bool more = true;
     int page = -1;                                 // lane m < MT: page of 16-slot group m of the next tile
     bool wanted = false;                           // that group holds slots to attend
+    const uint32_t qbuf = smem_u32(smem) + S::RING_BYTES + warp * S::Q_BYTES;
+    int pieces = 0, piece = 0;                     // pieces (a share's part of a segment) that prod has come to; cons's
+    int q_piece = -1;                              // piece whose queries the buffer holds or is getting
+    bool q_free = true, fresh = true;              // they have been read; prod has just come to its piece
 
-    // page ids of the tile to be copied next, loaded one tile ahead of their use
+    // prod to the tile that is copied next; its page ids are loaded one tile ahead of their use
     auto settle = [&]() {
-        if (more && prod.at >= prod.end) more = prod.next_segment(p, hcs, t1);
+        if (shares.u && more) {
+            // the next share is asked for a little before this one ends
+            asking |= prod.at + kClaimAhead >= p1;
+            if (asking && next_p == -2) next_p = taken(entry_p + 1);
+        }
+        if (more && prod.at >= prod.end) {
+            fresh = true;
+            ++pieces;
+            if (!prod.next_segment(p, hcs, p1)) {
+                for (int tries = 0; shares.u && next_p == -2; ++tries) {
+                    next_p = taken(entry_p + 1);
+                    if (tries >= kWaitLimit) {
+                        if (lane == 0) atomicOr(p.err, DSV4_DEV_ERR_TIMEOUT);
+                        next_p = -1;
+                    }
+                }
+                more = next_p >= 0;
+                if (more) {
+                    ++entry_p;
+                    const int id = share_id(next_p);
+                    next_p = -2;
+                    asking = false;
+                    p1 = share_begin(shares, id + 1);
+                    prod.at = share_begin(shares, id);
+                    prod.locate(p, hcs, lane, early, request_of);
+                    prod.bound(p1);
+                }
+            }
+        }
         page = -1;
         wanted = false;
         if (more && lane < MT) {
@@ -362,6 +494,20 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         }
     };
     auto issue = [&](int stage) {
+        if (more && fresh && q_free) {
+            // the piece's queries, with its first tile
+            const int chunk = prod.hc % p.chunks, head0 = prod.hc / p.chunks * p.group + chunk * HEADS;
+            const int nheads = min(HEADS, p.group - chunk * HEADS);
+            const uint8_t* from = static_cast<const uint8_t*>(p.q) + (prod.b * p.q_stride + (long long)head0 * D) * 2;
+            for (int i = lane; i < HEADS * D / 8; i += 32) {
+                const int c = i / (D / 8), piece = i % (D / 8);
+                const bool have = c < nheads;
+                cp_async_16(qbuf + c * S::QROW + piece * 16, from + (have ? i * 16 : 0), have ? 16u : 0u);
+            }
+            q_piece = pieces;
+            q_free = false;
+        }
+        fresh = false;
         if (more) {
             const int slot0 = (prod.rg.lo / TT + static_cast<int>(prod.at - prod.seg)) * TT;
             const bool ok = page >= 0 && page < p.c.num_pages;
@@ -398,24 +544,32 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
 
     // ---- the computing side ----
     int stage = 0;
-    for (bool on = true; on; on = cons.next_segment(p, hcs, t1)) {
+    int share = first, entry_c = 0;                // cons's share and entry of s_cta
+    for (bool on = true; on;) {
         const bool begins = cons.at == cons.seg;
         const int h = cons.hc / p.chunks, chunk = cons.hc % p.chunks;
         const int head0 = h * p.group + chunk * HEADS;
         const int nheads = min(HEADS, p.group - chunk * HEADS);
-        // q as the B operand; head g of n-tile nt
+        // q as the B operand; head g of n-tile nt.  From the buffer, if the copying side found it free when it came
+        // to this piece (very short pieces: from global memory).
+        cp_async_wait_group<S::STAGES - 1>();
+        __syncwarp();
+        const bool in_buffer = q_piece == piece;
+        const uint8_t* qbase = in_buffer ? smem + S::RING_BYTES + warp * S::Q_BYTES
+                                         : static_cast<const uint8_t*>(p.q) +
+                                               (cons.b * p.q_stride + (long long)head0 * D) * 2;
+        const int qrow = in_buffer ? S::QROW : D * 2;
         uint32_t qf[DT][NT][2];
         float smul[NT][2];                         // score factor of the two heads whose columns this thread holds
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const bool have = nt * 8 + g < nheads;
-            const uint32_t* qr = reinterpret_cast<const uint32_t*>(
-                static_cast<const uint16_t*>(p.q) + cons.b * p.q_stride + (long long)(head0 + nt * 8 + g) * D);
+            const uint32_t* qr = reinterpret_cast<const uint32_t*>(qbase + (nt * 8 + g) * qrow);
             if constexpr (!S::FP8) {
 #pragma unroll
                 for (int kk = 0; kk < DT; ++kk) {
-                    qf[kk][nt][0] = have ? __ldg(qr + kk * 8 + t4) : 0u;
-                    qf[kk][nt][1] = have ? __ldg(qr + kk * 8 + t4 + 4) : 0u;
+                    qf[kk][nt][0] = have ? qr[kk * 8 + t4] : 0u;
+                    qf[kk][nt][1] = have ? qr[kk * 8 + t4 + 4] : 0u;
                 }
                 smul[nt][0] = smul[nt][1] = p.scale_log2;
             } else {
@@ -426,7 +580,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                     const int d2 = (16 * (t4 + 4 * (kk >> 2)) + 4 * (kk & 3)) / 2;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        qf[kk][nt][u] = have ? __ldg(qr + d2 + u) : 0u;
+                        qf[kk][nt][u] = have ? qr[d2 + u] : 0u;
                         const float2 f = p.q_bf16 ? unpack2<true>(qf[kk][nt][u]) : unpack2<false>(qf[kk][nt][u]);
                         amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
@@ -445,11 +599,16 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                         const float2 f = p.q_bf16 ? unpack2<true>(qf[kk][nt][u]) : unpack2<false>(qf[kk][nt][u]);
                         qf[kk][nt][u] = pack2<false>(f.x * up, f.y * up);
                     }
-                const float mul = p.scale_log2 * (p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.f) * down;
+                const float mul = p.scale_log2 * kscale * down;
                 smul[nt][0] = __shfl_sync(0xffffffffu, mul, 8 * t4);
                 smul[nt][1] = __shfl_sync(0xffffffffu, mul, 8 * t4 + 4);
             }
         }
+        if (in_buffer) {
+            __syncwarp();
+            q_free = true;
+        }
+        ++piece;
         float o[DT][NT][4], mref[NT][2], lsum[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -636,8 +795,23 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 lsum[nt][u] += __shfl_xor_sync(0xffffffffu, lsum[nt][u], 8);
                 lsum[nt][u] += __shfl_xor_sync(0xffffffffu, lsum[nt][u], 16);
             }
-        if (!begins || cons.end != cons.seg + cons.rg.tiles) {
-            const int entry = piece_entry(share, begins);
+        // the next piece, if there is one
+        const bool cut = !begins || cons.end != cons.seg + cons.rg.tiles;
+        const int here_b = cons.b, here = share;
+        on = cons.next_segment(p, hcs, c1);
+        if (!on && entry_c < entry_p) {
+            ++entry_c;
+            share = share_id(*(volatile int*)&s_cta[entry_c % kClaimRing]);
+            if (lane == 0) *(volatile int*)&s_done[warp] = entry_c;
+            c1 = share_begin(shares, share + 1);
+            cons.at = share_begin(shares, share);
+            cons.locate(p, hcs, lane, early, request_of);
+            cons.bound(c1);
+            on = true;
+        }
+        if (on) kscale = load_kscale();
+        if (cut) {
+            const int entry = piece_entry(here, begins);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -660,7 +834,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
             continue;
         }
         const float vmul = S::FP8 && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
-        const size_t row = (size_t)cons.b * p.heads + head0;
+        const size_t row = (size_t)here_b * p.heads + head0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float inv[2];
@@ -733,7 +907,7 @@ inline int launch_decode_shape(const DecodeParams& p, void* stream) {
         }
         __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELEASE);
     }
-    return launch(dsv4_gqa_decode_kernel<S>, dim3(p.warps / S::W), S::W * 32, S::SMEM, stream, 1, p);
+    return launch(dsv4_gqa_decode_kernel<S>, dim3(p.warps / S::W + p.claims), S::W * 32, S::SMEM, stream, 1, p);
 }
 
 template <int KIND>

@@ -341,6 +341,53 @@ def test_decode_offsets_beyond_32_bits(A):
     assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
+@pytest.mark.parametrize("lens", [[90000, 1, 88001], [60000, 0, 120001], [3, 5, 40]])
+def test_decode_of_long_lists(A, lens):
+    # enough tiles that most shares are claimed while the kernel runs; and short lists in the same room.
+    # Definition in 64 bits on the GPU; nothing may depend on who claims what.
+    rows, hkv, heads, dim, page = 3, 8, 16, 64, 256
+    width = -(-120001 // page)
+    gen = torch.Generator(device="cuda").manual_seed(77)
+    shape = (rows * width, hkv, page, dim)
+    k, v = (torch.randn(shape, generator=gen, device="cuda", dtype=BF) for _ in range(2))
+    table = torch.randperm(rows * width, generator=gen, device="cuda").view(rows, width).to(torch.int32)
+    cache = A.make_gqa_cache(k, v, table)
+    q = torch.randn(rows, heads, dim, generator=gen, device="cuda", dtype=BF)
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    w = torch.zeros(rows, hkv, width * page, device="cuda")
+    got = []
+    for _ in range(3):
+        wo = torch.full_like(w, -1.0)
+        out, lse = A.dsv4_gqa_decode(q, n, cache, weights=w, weights_out=wo)
+        plain = A.dsv4_gqa_decode(q, n, cache)
+        assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
+        got.append((out, lse, wo))
+    assert A.dsv4_attn_get_device_error() == 0
+    for x in got[1:]:
+        assert all(torch.equal(p, r) for p, r in zip(x, got[0]))
+    out, lse, wo = got[0]
+    for b, m in enumerate(lens):
+        assert bool((wo[b, :, m:] == -1.0).all())
+        if m == 0:
+            assert bool((out[b] == 0).all()) and bool(torch.isinf(lse[b]).all())
+            continue
+        for h in range(hkv):
+            kk, vv = (x[table[b].long(), h].reshape(-1, dim)[:m].double() for x in (k, v))
+            qq = q[b, 2 * h: 2 * h + 2].double()
+            s = qq @ kk.T / 8.0
+            ref_lse = torch.logsumexp(s, dim=1)
+            p = torch.exp(s - ref_lse[:, None])
+            ref = p @ vv
+            mag = float((qq.abs() @ kk.abs().T).max()) / 8.0
+            ds, sums = (dim + 8) * 2.0 ** -23 * mag, (m / 16 + 64) * 2.0 ** -23
+            # (sums: as above; they grow with the rows of one share, not with m, but the bound need not be tight)
+            tol = (2 * ds + 2.0 ** -20 + 2.0 ** -16 + sums) * (p @ vv.abs()) + (2.0 ** -8 + 2.0 ** -22) * ref.abs()
+            assert bool(((out[b, 2 * h: 2 * h + 2].double() - ref).abs() <= tol).all())
+            assert float((lse[b, 2 * h: 2 * h + 2].double() - ref_lse).abs().max()) <= ds + sums + 2.0 ** -18
+            tw = p.sum(0) * (2 * ds + 2.0 ** -19 + sums)
+            assert bool(((wo[b, h, :m].double() - p.sum(0)).abs() <= tw + 1e-12).all())
+
+
 # ---------------------------------------------------------------- store
 def _bits(x):
     x = x.detach().cpu()
