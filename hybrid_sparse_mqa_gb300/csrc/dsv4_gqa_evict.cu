@@ -28,6 +28,7 @@ constexpr int kMoveThreads = 128;
 // rows that a warp of the move kernel copies, by the 16-byte pieces of a K and a V row
 __host__ __device__ constexpr int warp_rows(int pieces) { return pieces >= 32 ? 16 : 32; }
 constexpr int kMaxCluster = 8;
+constexpr int kFew = 4;                    // rows over the bound that are looked for one by one
 constexpr int kHeldKeys = 32 * 1024;       // keys that the largest CTA holds in registers
 
 struct EvictParams {
@@ -65,11 +66,20 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 template <int WARPS>
 struct SelectShared {
-    uint32_t hist[kBins][kCopies];         // lane l counts in copy l mod kCopies
-    uint32_t bins[2][kBins];               // this CTA's sums, for the cluster (by digit parity)
-    uint32_t warp_sum[WARPS];
+    uint4 hist[kBins][kCopies / 4];        // lane l counts in copy l mod kCopies
+    uint4 bins[2][kBins / 4];              // this CTA's sums, for the cluster (by digit parity)
+    uint32_t warp_sum[2][WARPS];
     uint32_t count[2][2];                  // this CTA's ties; holes and movers, for the cluster
     uint32_t pick[3];                      // chosen bin, rows wanted in it, rows in it
     int skip;
@@ -83,22 +93,23 @@ __device__ __forceinline__ void lane_sync() {
         __syncthreads();
 }
 
-// Exclusive prefix of v over the block's warps (v uniform in a warp), and the
-// block's total.
+// Exclusive prefixes of v and w (uniform in a warp) over the block's warps, and
+// the block's totals.
 template <int WARPS>
-__device__ __forceinline__ uint32_t warps_exclusive(uint32_t v, uint32_t* warp_sum, uint32_t& total) {
-    const int warp = threadIdx.x >> 5;
+__device__ __forceinline__ void warps_exclusive(uint32_t& v, uint32_t& w, uint32_t (*sums)[WARPS], uint32_t& total_v,
+                                                uint32_t& total_w) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) warp_sum[warp] = v;
-    __syncthreads();
-    uint32_t base = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) base += warp_sum[w];
-        total += warp_sum[w];
+    if (lane == 0) {
+        sums[0][warp] = v;
+        sums[1][warp] = w;
     }
-    return base;
+    __syncthreads();
+    const uint32_t a = lane < WARPS ? sums[0][lane] : 0u, c = lane < WARPS ? sums[1][lane] : 0u;
+    total_v = __reduce_add_sync(0xffffffffu, a);
+    total_w = __reduce_add_sync(0xffffffffu, c);
+    v = __reduce_add_sync(0xffffffffu, lane < warp ? a : 0u);
+    w = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0u);
 }
 
 // THREADS x KEYS slots per CTA; KEYS = 0: any number, keys made anew in every
@@ -110,8 +121,7 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int id = blockIdx.x / CLUSTER, rank = blockIdx.x % CLUSTER;
     const int b = id / p.c.kv_heads, h = id % p.c.kv_heads;
-    for (int i = tid; i < kBins * kCopies / 4; i += THREADS)
-        reinterpret_cast<uint4*>(&sh.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < kBins * kCopies / 4; i += THREADS) (&sh.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0) sh.skip = 0;
     grid_dependency_wait();
     grid_dependents_go();
@@ -175,7 +185,20 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) held[i0 + i] = make_key(w[i], pos[i]);
+            for (int i = 0; i < kBatch; ++i) {
+                const int s = r0 + 32 * (i0 + i) + lane;
+                held[i0 + i] = make_key(w[i], pos[i]);
+                // slots below `keep` in case their rows stay; the move kernel writes the others' again
+                if (s < r1 && s < p.keep) {
+                    if (copy_w) w_out[s] = w[i];
+                    if (copy_p) p_out[s] = pos[i];
+                }
+            }
+        }
+    } else if (copy_w || copy_p) {
+        for (int s = r0 + lane; s < min(r1, p.keep); s += 32) {
+            if (copy_w) w_out[s] = __ldg(w_in + s);
+            if (copy_p) p_out[s] = __ldg(p_in + s);
         }
     }
     // visit(chunk, key, inside) for chunks from .. from + COUNT - 1 of the warp, in order
@@ -194,41 +217,108 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
     };
     __syncthreads();
 
+    int* holes = p.holes + (size_t)id * p.most;
+    int* movers = p.movers + (size_t)id * p.most;
+    if constexpr (CLUSTER == 1 && KEYS > 0) {
+        // A cache just over its bound, as after every step of a decode loop: the few rows to go are looked for one by
+        // one, smallest key first, of equal ones the highest slot.  (One of 2049 rows, 512 rows of weights: 17 us
+        // together with the move kernel by the radix select, NEW_STEP us so.)
+        if (n - p.keep <= kFew) {
+            int gone[kFew];
+            for (int e = 0; e < n - p.keep; ++e) {
+                uint32_t low = 0xffffffffu;
+                int at = -1;
+                each(0, chunks, [&](int i, uint32_t k, bool in) {
+                    const int s = r0 + 32 * i + lane;
+                    bool was = false;
+#pragma unroll
+                    for (int x = 0; x < kFew; ++x) was |= x < e && gone[x] == s;
+                    if (in && !was && k <= low) {
+                        low = k;
+                        at = s;
+                    }
+                });
+                const uint32_t wlow = __reduce_min_sync(0xffffffffu, low);
+                const int wat = __reduce_max_sync(0xffffffffu, low == wlow ? at : -1);
+                if (lane == 0) {
+                    sh.warp_sum[0][warp] = wlow;
+                    sh.warp_sum[1][warp] = static_cast<uint32_t>(wat);
+                }
+                __syncthreads();
+                const uint32_t x = lane < WARPS ? sh.warp_sum[0][lane] : 0xffffffffu;
+                const int y = lane < WARPS ? static_cast<int>(sh.warp_sum[1][lane]) : -1;
+                const uint32_t least = __reduce_min_sync(0xffffffffu, x);
+                const int slot = __reduce_max_sync(0xffffffffu, x == least ? y : -1);
+#pragma unroll
+                for (int q = 0; q < kFew; ++q)
+                    if (q == e) gone[q] = slot;
+                __syncthreads();
+            }
+            if (tid == 0) {
+                // freed slots below `keep` in ascending order, and the rows behind it that stay
+                int count = 0;
+                for (int last = -1;; ++count) {
+                    int next = p.keep;
+#pragma unroll
+                    for (int q = 0; q < kFew; ++q)
+                        if (q < n - p.keep && gone[q] > last) next = min(next, gone[q]);
+                    if (next >= p.keep) break;
+                    holes[count] = last = next;
+                }
+                p.counts[id] = count;
+                int to = 0;
+                for (int s = p.keep; s < n; ++s) {
+                    bool stays = true;
+#pragma unroll
+                    for (int q = 0; q < kFew; ++q) stays &= !(q < n - p.keep && gone[q] == s);
+                    if (stays) movers[to++] = s;
+                }
+            }
+            return;
+        }
+    }
+
     // ---- the key of the last row kept: `want` of the `equal` rows of key `prefix` stay ----
     uint32_t prefix = 0, mask = 0, want = p.keep, equal = 0;
     for (int digit = 0; digit < 4; ++digit) {
         const int shift = 24 - 8 * digit;
         each(0, chunks, [&](int, uint32_t k, bool in) {
-            if (in && (k & mask) == prefix) atomicAdd(&sh.hist[(k >> shift) & 255u][lane % kCopies], 1u);
+            if (in && (k & mask) == prefix) atomicAdd(reinterpret_cast<uint32_t*>(sh.hist[(k >> shift) & 255u]) + lane % kCopies, 1u);
         });
         __syncthreads();
         // bin sums (a bin's copies are two neighbouring uint4); the copies are cleared for the next digit
-        uint32_t* bins = sh.bins[digit & 1];
+        uint4* bins = sh.bins[digit & 1];
         for (int i = tid; i < kBins * kCopies / 4; i += THREADS) {
-            uint4* c = reinterpret_cast<uint4*>(&sh.hist[0][0]) + i;
+            uint4* c = &sh.hist[0][0] + i;
             const uint4 x = *c;
             *c = make_uint4(0, 0, 0, 0);
             uint32_t v = x.x + x.y + x.z + x.w;
             v += __shfl_xor_sync(0xffffffffu, v, 1);
-            if ((i & 1) == 0) bins[i >> 1] = v;
+            if ((i & 1) == 0) reinterpret_cast<uint32_t*>(bins)[i >> 1] = v;
         }
         lane_sync<CLUSTER>();
         // one warp looks for the bin: lane l holds bins 255 - 8 l .. 248 - 8 l
         if (warp == 0) {
             uint32_t mine[8], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t* bin = &bins[255 - 8 * lane - i];
-                if constexpr (CLUSTER == 1) {
-                    mine[i] = *bin;
-                } else {
-                    const uint32_t a = smem_u32(bin);
-                    mine[i] = 0;
+            for (int i = 0; i < 8; ++i) mine[i] = 0;
 #pragma unroll
-                    for (int r = 0; r < CLUSTER; ++r) mine[i] += ld_cluster_u32(mapa(a, r));
+            for (int r = 0; r < CLUSTER; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4* at = &bins[63 - 2 * lane - i];
+                    uint4 x;
+                    if constexpr (CLUSTER == 1)
+                        x = *at;
+                    else
+                        x = ld_cluster_u4(mapa(smem_u32(at), r));
+                    mine[4 * i] += x.w;
+                    mine[4 * i + 1] += x.z;
+                    mine[4 * i + 2] += x.y;
+                    mine[4 * i + 3] += x.x;
                 }
-                sum += mine[i];
-            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += mine[i];
             uint32_t above = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -262,8 +352,9 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
     if (!every) {
         uint32_t c = 0;
         each(0, chunks, [&](int, uint32_t k, bool in) { c += __popc(__ballot_sync(0xffffffffu, in && k == prefix)); });
-        uint32_t total;
-        tie = warps_exclusive<WARPS>(c, sh.warp_sum, total);
+        uint32_t none = 0, total, zero;
+        warps_exclusive<WARPS>(c, none, sh.warp_sum, total, zero);
+        tie = c;
         if (tid == 0) sh.count[0][0] = total;
         lane_sync<CLUSTER>();
         if constexpr (CLUSTER > 1) {
@@ -319,9 +410,8 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
     }
     nh = __reduce_add_sync(0xffffffffu, nh);
     nm = __reduce_add_sync(0xffffffffu, nm);
-    uint32_t hole_total, move_total;
-    uint32_t hole = warps_exclusive<WARPS>(nh, sh.warp_sum, hole_total);
-    uint32_t move = warps_exclusive<WARPS>(nm, sh.warp_sum, move_total);
+    uint32_t hole = nh, move = nm, hole_total, move_total;
+    warps_exclusive<WARPS>(hole, move, sh.warp_sum, hole_total, move_total);
     if constexpr (CLUSTER > 1) {
         if (tid == 0) {
             sh.count[1][0] = hole_total;
@@ -335,8 +425,6 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
         }
     }
     if (rank == CLUSTER - 1 && tid == 0) p.counts[id] = move + move_total;   // (warp 0's prefix: the CTAs before)
-    int* holes = p.holes + (size_t)id * p.most;
-    int* movers = p.movers + (size_t)id * p.most;
     auto list = [&](int from, uint32_t kept) {
         const uint32_t hb = hole_bits(from, kept), mb = move_bits(from, kept);
         // both counts of a chunk in one word: at most 1024 of each in 32 chunks
@@ -358,16 +446,6 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
         }
         hole += sum & 0xffffu;
         move += sum >> 16;
-        const int firsts = min(min(32, chunks - from), (p.keep - r0 - 32 * from + 31) / 32);   // chunks below `keep`
-        if (copy_w || copy_p)
-#pragma unroll 4
-            for (int i = 0; i < firsts; ++i) {
-                const int s = r0 + 32 * (from + i) + lane;
-                if ((__shfl_sync(0xffffffffu, kept, i) >> lane & 1) && s < p.keep) {
-                    if (copy_w) w_out[s] = __ldg(w_in + s);
-                    if (copy_p) p_out[s] = __ldg(p_in + s);
-                }
-            }
     };
     if constexpr (KEYS > 0) {
 #pragma unroll

@@ -589,6 +589,8 @@ def test_evict_equal_and_special_weights(A):
         if kind == 3:
             w = -torch.rand(w.shape, generator=c.gen)
         check_evict(A, c, [300, 299, 120, 150], 128, w=w, recent=20)
+        check_evict(A, c, [300, 299, 297, 296], 296, w=w, recent=20)       # one to four rows too many
+        check_evict(A, c, [300, 298, 120, 150], 296, w=w, recent=296, inplace=True)
 
 
 def test_evict_rows_named_in_any_order_twice_or_not_at_all(A):
