@@ -300,7 +300,7 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
     const int most = c->head_dim * (c->format == DSV4_GQA_E4M3 ? 1 : 2) > 256 ? kMaxCtas / 2 : kMaxCtas;
     const long long want = pl.tiles / kMinTiles;
     pl.ctas = want < 1 ? 1 : (want < most ? static_cast<int>(want) : most);
-    pl.claims = pl.ctas == most && pl.tiles >= (long long)most * kWarps * kClaimTiles ? 3 * most : 0;
+    pl.claims = pl.ctas == most && pl.tiles >= (long long)most * kWarps * kClaimTiles ? most : 0;
     const size_t entries = size_t(2) * (pl.ctas + pl.claims) * kWarps * 8 * pl.nt;
     pl.part_o = 0;
     pl.part_ml = pl.part_o + up256(entries * c->head_dim * sizeof(float));

@@ -6,15 +6,26 @@
 //
 // Work: a segment is one (request, KV head, group of up to 8 NT query heads);
 // its key range is cut into tiles of TT slots.  All tiles of the batch form
-// one list, of which every warp of the grid takes an equal contiguous share,
-// so a ragged batch is as balanced as a uniform one and a long request is
-// split over as many warps as it needs.  A segment that lies in one share is
-// finished there; of a cut one every warp leaves (unnormalised output,
-// reference, sum) in fp32 in the workspace, at most two pieces per warp, which
-// the join kernel merges.  Warps never wait for one another after the start.
+// one list, of which every warp of the grid takes a contiguous share, so a
+// ragged batch is as balanced as a uniform one and a long request is split
+// over as many warps as it needs.  A segment that lies in one share is finished
+// there; of a cut one every share leaves (unnormalised output, reference, sum)
+// in fp32 in the workspace, at most two pieces each, which the join kernel
+// merges.  (A CTA per share with a merge of its warps in shared memory took
+// 56 us where a share per warp takes 35: 48 requests of up to 2000 rows, 16
+// heads of 64.)
+//
+// SMs do not get equal bandwidth (equal shares ended between 117 and 165 us
+// for 2 x 131072 rows), so of a long list the last eighth of every warp's part
+// is given out to whoever is free.  A share for each warp of a CTA makes up one
+// more CTA of the grid, which a resident CTA that runs out of tiles takes over
+// before it is launched (clusterlaunchcontrol.try_cancel): the hardware's own
+// queue, with no counter in memory.  What a share holds does not depend on who
+// takes it, so results do not either.
 //
 // A warp streams its tiles through its own ring of cp.async stages, which runs
-// ahead over segment boundaries.  Scores are computed transposed, S^T = K Q^T,
+// ahead over segment and share boundaries, and the queries of the next segment
+// with them.  Scores are computed transposed, S^T = K Q^T,
 // so the 16 rows of an m16n8k16 MMA are slots and its 8 columns query heads: a
 // group of 8 heads wastes nothing.  The exponentials become the B operand of
 // O^T = V^T P^T by one 8x8 transposition in registers (movmatrix).  The
@@ -42,16 +53,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;           // reference of a head that has seen no score
 constexpr int kWarps = 4;                  // warps per CTA
 constexpr int kMaxCtas = 304;              // resident at once: two per SM
-// What the three rounds take of a warp's part of a long list, in 32nds.  Taking
-// a share costs a piece to write and join and some stalled loads: 32 x
+// What is kept back of a warp's part of a long list, in 32nds.  Taking another
+// share costs a piece to write and join and some stalled loads: 32 x
 // 2048..32768 rows (230 tiles per warp) go from 352 to 336 us, 2 x 131072 rows
-// (108) from 171 to 170, while 64 x 1024..16384 e4m3 rows (34) would go from 99
-// to 111.
-constexpr int kPart1 = 4, kPart2 = 1, kPart3 = 1;
+// (108) from 171 to 165, while 64 x 1024..16384 e4m3 rows (34) would go from 99
+// to 102.  Two or three rounds of smaller shares gained no more.
+constexpr int kTail = 4;
 constexpr int kClaimTiles = 64;            // a list is long from so many tiles per resident warp
 constexpr int kClaimAhead = 6;             // tiles before the end of a share at which the next is asked for
 constexpr int kClaimRing = 16;             // claims that a warp may be behind another of its CTA
 constexpr int kWaitLimit = 1 << 20;        // polls before a claim is given up
+
 struct DecodeParams {
     Cache c;
     const void* q;
@@ -98,12 +110,12 @@ __device__ __forceinline__ Range key_range(const DecodeParams& p, int n) {
 }
 
 // How the list's `total` tiles are shared out: n parts of q tiles each (the
-// first r one more), each a share; or, where u > 0, each part four shares, of
-// which the last three hold kPart1 u, kPart2 u and kPart3 u tiles.  Shares are
-// numbered in the order of the list.
+// first r one more), each a share; or, where tail > 0, each part two shares, of
+// which the second holds `tail` tiles.  Shares are numbered in the order of the
+// list.
 struct Shares {
     int count, n;
-    unsigned q, r, u;
+    unsigned q, r, tail;
 };
 __device__ __forceinline__ Shares make_shares(const DecodeParams& p, unsigned total) {
     Shares s;
@@ -112,28 +124,23 @@ __device__ __forceinline__ Shares make_shares(const DecodeParams& p, unsigned to
     s.n = cut ? p.warps : most < 1u ? 1 : (most > (unsigned)p.warps ? p.warps : (int)most);
     s.q = total / s.n;
     s.r = total - s.q * s.n;
-    s.u = cut ? s.q / 32 : 0u;
-    s.count = cut ? 4 * s.n : s.n;
+    s.tail = cut ? s.q * kTail / 32 : 0u;
+    s.count = cut ? 2 * s.n : s.n;
     return s;
 }
 // The list index that share i begins at.
 __device__ __forceinline__ unsigned share_begin(const Shares& s, int i) {
-    const unsigned part = s.u ? i >> 2 : i, level = s.u ? i & 3 : 0;
-    if (level == 0) return part * s.q + min(part, s.r);
-    const unsigned behind = level == 1 ? kPart1 + kPart2 + kPart3 : level == 2 ? kPart2 + kPart3 : kPart3;
-    return (part + 1) * s.q + min(part + 1, s.r) - behind * s.u;
+    const unsigned part = s.tail ? (i + 1) >> 1 : i;       // it begins, or the one before it ends
+    const unsigned at = part * s.q + min(part, s.r);
+    return s.tail && i & 1 ? at - s.tail : at;
 }
 // The share that tile t lies in.
 __device__ __forceinline__ int share_of(const Shares& s, unsigned t) {
     const unsigned longer = s.r * (s.q + 1);
     const unsigned part = t < longer ? t / (s.q + 1) : s.r + (t - longer) / s.q;
-    if (!s.u) return static_cast<int>(part);
+    if (!s.tail) return static_cast<int>(part);
     const unsigned left = (part + 1) * s.q + min(part + 1, s.r) - t;         // tiles to the end of the part
-    const int level = left > (kPart1 + kPart2 + kPart3) * s.u ? 0
-                      : left > (kPart2 + kPart3) * s.u        ? 1
-                      : left > kPart3 * s.u                   ? 2
-                                                              : 3;
-    return static_cast<int>(4 * part) + level;
+    return static_cast<int>(2 * part) + (left <= s.tail ? 1 : 0);
 }
 // The workspace entry of share i's piece of a cut segment: one that begins
 // with its segment can only be the share's last, any other its first.
@@ -378,9 +385,9 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     // warps of one resident CTA take shares far apart, so that few shares spread over all SMs
     const int ctas = p.warps / W;
     auto share_id = [&](int cta) {
-        if (cta < ctas) return (warp * ctas + cta) * (shares.u ? 4 : 1);
+        if (cta < ctas) return (warp * ctas + cta) * (shares.tail ? 2 : 1);
         const int j = (cta - ctas) * W + warp;
-        return shares.u ? j % p.warps * 4 + 1 + j / p.warps : shares.count;      // (short list: nothing)
+        return shares.tail ? 2 * j + 1 : shares.count;       // (short list: nothing)
     };
     const int first = share_id(blockIdx.x);
     if (first >= shares.count) {
@@ -456,7 +463,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
 
     // prod to the tile that is copied next; its page ids are loaded one tile ahead of their use
     auto settle = [&]() {
-        if (shares.u && more) {
+        if (shares.tail && more) {
             // the next share is asked for a little before this one ends
             asking |= prod.at + kClaimAhead >= p1;
             if (asking && next_p == -2) next_p = taken(entry_p + 1);
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
             fresh = true;
             ++pieces;
             if (!prod.next_segment(p, hcs, p1)) {
-                for (int tries = 0; shares.u && next_p == -2; ++tries) {
+                for (int tries = 0; shares.tail && next_p == -2; ++tries) {
                     next_p = taken(entry_p + 1);
                     if (tries >= kWaitLimit) {
                         if (lane == 0) atomicOr(p.err, DSV4_DEV_ERR_TIMEOUT);
