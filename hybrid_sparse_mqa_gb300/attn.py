@@ -383,7 +383,7 @@ def make_gqa_cache(k_pages, v_pages, page_table, *, k_scale=None, v_scale=None):
     c._ref = ctypes.addressof(c)
     lib()                       # (a descriptor is only good for the library's calls)
     c._index = k_pages.get_device()
-    c._tracked = torch.Size((c.page_table_rows, heads))
+    c._rows = torch.Size((heads, dim))
     c._slots = page_table.shape[1] * page_size
     c._scale = 1.0 / math.sqrt(dim)
     return c
@@ -404,16 +404,18 @@ def _need(x, name, dtype, n, index):
 
 def _width(name, x, dtype, cache):
     """The width of a [request rows, KV heads, width] contiguous tensor."""
-    if x.dtype is not dtype or x.dim() != 3 or not x.is_contiguous() or x.get_device() != cache._index \
-            or x.shape[:2] != cache._tracked:
-        raise Dsv4Error(f"{name} must be a contiguous {dtype} [{cache._tracked[0]}, {cache._tracked[1]}, width] tensor "
-                        "on the cache's device")
-    return x.size(2)
+    if x.dim() == 3:
+        rows, heads, width = x.shape
+        if x.dtype is dtype and rows == cache.page_table_rows and heads == cache.num_kv_heads and x.is_contiguous() \
+                and x.get_device() == cache._index:
+            return width
+    raise Dsv4Error(f"{name} must be a contiguous {dtype} [{cache.page_table_rows}, {cache.num_kv_heads}, width] tensor "
+                    "on the cache's device")
 
 
 def _raw_stream(stream, index):
     """The stream's handle; the cache's device has to be the current one, as for every launch."""
-    if index < 0 or index != torch.cuda.current_device():
+    if index < 0 or index != torch._C._cuda_getDevice():
         raise Dsv4Error("the cache must be on the current CUDA device")
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
@@ -443,12 +445,15 @@ def dsv4_gqa_store(k, v, req_rows, slots, cache, *, weights=None, positions=None
     width]) starts at 0 there, positions (int32, same shape) at
     token_positions[i]."""
     index = cache._index
-    n = k.size(0)
+    if k.dim() != 3 or v.dim() != 3:
+        raise Dsv4Error("k and v must be [n, KV heads, head_dim] tensors")
+    shape = k.shape
+    n = shape[0]
     kt, kh, k1 = k.stride()
     vt, vh, v1 = v.stride()
     type_ = _gqa_type(k, cache)
-    if k.shape != (n, cache.num_kv_heads, cache.head_dim) or v.shape != k.shape or v.dtype is not k.dtype \
-            or k1 != 1 or v1 != 1 or k.get_device() != index or v.get_device() != index:
+    if shape[1:] != cache._rows or v.shape != shape or v.dtype is not k.dtype or k1 != 1 or v1 != 1 \
+            or k.get_device() != index or v.get_device() != index:
         raise Dsv4Error(f"k and v must be {[n, cache.num_kv_heads, cache.head_dim]} tensors of one type with contiguous "
                         "rows on the cache's device")
     if n <= 1 or cache.num_kv_heads == 1:         # a dimension of one entry may have any stride

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(PW > 8 ? PW * 32 : 256) dsv4_gqa_join_kernel(c
             l += f * s_ml[w].y;
             x += f * s_o[w][tid];
         }
-        const float top = fmaxf(mx, sk);
+        const float top = fminf(fmaxf(mx, sk), 3e38f);
         const float f = fast_exp2(mx - top);
         l = l * f + fast_exp2(sk - top);
         const bool any = l > 0.f || l != l;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(PW > 8 ? PW * 32 : 256) dsv4_gqa_join_kernel(c
         return;
     }
     if (!mine) return;
-    const float top = fmaxf(mx, sk);
+    const float top = fminf(fmaxf(mx, sk), 3e38f);
     const float f = fast_exp2(mx - top);
     l = l * f + fast_exp2(sk - top);
     const bool any = l > 0.f || l != l;

@@ -208,6 +208,19 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// 16-byte global -> shared copy through L2 lines that are the first to go (a
+// cache row is read once per call; what is written for the kernels behind
+// stays); src_bytes = 0 writes zeros and reads nothing.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void cp_async_16_hint(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(src_bytes),
+                 "l"(policy)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // Asks for a CTA of the grid that has not been launched; the answer's 16 bytes
@@ -446,6 +459,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     const int lane_row = lane / S::PPR, lane_piece = lane % S::PPR;
     const long long lane_off = lane_row * p.c.row_stride + lane_piece * 16;
     const int page_mask = (1 << p.c.page_shift) - 1;
+    const uint64_t policy = evict_first_policy();
     // the K scale of cons's KV head, loaded as soon as cons comes to it: ahead of the copies
     auto load_kscale = [&]() { return S::FP8 && p.c.k_scale ? __ldg(p.c.k_scale + cons.hc / p.chunks) : 1.f; };
     float kscale = load_kscale();
@@ -535,8 +549,8 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                     const int r = i * S::RPI + lane_row;        // row in the group
                     const bool in = have && s + r < prod.rg.n && s + r >= prod.rg.lo;
                     const long long off = in ? base + i * S::RPI * p.c.row_stride : 0;
-                    cp_async_16(kd + k_offset<S>(m * 16 + r, lane_piece), p.c.k + off, in ? 16u : 0u);
-                    cp_async_16(vd + v_offset<S>(m * 16 + r, lane_piece), p.c.v + off, in ? 16u : 0u);
+                    cp_async_16_hint(kd + k_offset<S>(m * 16 + r, lane_piece), p.c.k + off, in ? 16u : 0u, policy);
+                    cp_async_16_hint(vd + v_offset<S>(m * 16 + r, lane_piece), p.c.v + off, in ? 16u : 0u, policy);
                 }
             }
             ++prod.at;
@@ -849,7 +863,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
             for (int u = 0; u < 2; ++u) {
                 const int c = nt * 8 + 2 * t4 + u;
                 const float sk = p.sink && c < nheads ? __ldg(p.sink + head0 + c) * kLog2e : -INFINITY;
-                const float top = fmaxf(mref[nt][u], sk);
+                const float top = fminf(fmaxf(mref[nt][u], sk), 3e38f);     // (a sink of +inf: out = 0)
                 const float f = fast_exp2(mref[nt][u] - top);
                 const float l = lsum[nt][u] * f + fast_exp2(sk - top);
                 const bool any = l > 0.f || l != l;

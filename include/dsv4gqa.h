@@ -72,6 +72,9 @@
  *   a padded batch may hold any row there), rows on a page id outside the
  *   pool are skipped (DSV4_DEV_ERR_GQA_PAGE), a stored row that has no place
  *   is skipped (DSV4_DEV_ERR_STORE_ROW).
+ *   Every kernel can be captured into a graph; make the first call of a
+ *   function on a device before any capture (its kernels are loaded then).
+ *   A captured call reads lens, tables and rows anew at every replay.
  *   lens, seq_lens, req_pool_indices: int32 [batch]; req_pool_indices NULL =
  *   request b is row b.
  *   weights (fp32) and positions (int32): [page_table_rows, num_kv_heads,

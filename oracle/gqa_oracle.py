@@ -66,6 +66,9 @@ def gqa_decode(q, lens, cache, *, max_len, scale, window=0, sink=None, req=None,
             top = every.max()
             if top == -np.inf:
                 continue
+            if sk == np.inf:
+                lse[b, i] = np.inf
+                continue
             total = np.exp(every - top).sum()
             p = np.exp(s - top) / total
             out[b, i] = vs * (p @ v)

@@ -218,7 +218,7 @@ def test_decode_small_queries_of_an_e4m3_cache(A):
 
 def test_decode_sinks(A):
     c = Case(rows=3, slots=60, seed=7)
-    for value in (-math.inf, -100.0, 0.0, 60.0):
+    for value in (-math.inf, -100.0, 0.0, 60.0, math.inf):
         check_decode(A, c, [60, 0, 7], 4, sink=torch.full((4,), value), weights=True)
 
 
@@ -343,9 +343,10 @@ def test_decode_offsets_beyond_32_bits(A):
 
 @pytest.mark.parametrize("lens", [[90000, 1, 88001], [60000, 0, 120001], [3, 5, 40]])
 def test_decode_of_long_lists(A, lens):
-    # enough tiles that most shares are claimed while the kernel runs; and short lists in the same room.
+    # enough tiles (16 slots each; over 64 for each of 1216 warps) that shares are claimed while the kernel runs; and
+    # short lists in the same room.
     # Definition in 64 bits on the GPU; nothing may depend on who claims what.
-    rows, hkv, heads, dim, page = 3, 8, 16, 64, 256
+    rows, hkv, heads, dim, page = 3, 8, 16, 128, 256
     width = -(-120001 // page)
     gen = torch.Generator(device="cuda").manual_seed(77)
     shape = (rows * width, hkv, page, dim)
@@ -374,11 +375,11 @@ def test_decode_of_long_lists(A, lens):
         for h in range(hkv):
             kk, vv = (x[table[b].long(), h].reshape(-1, dim)[:m].double() for x in (k, v))
             qq = q[b, 2 * h: 2 * h + 2].double()
-            s = qq @ kk.T / 8.0
+            s = qq @ kk.T / math.sqrt(dim)
             ref_lse = torch.logsumexp(s, dim=1)
             p = torch.exp(s - ref_lse[:, None])
             ref = p @ vv
-            mag = float((qq.abs() @ kk.abs().T).max()) / 8.0
+            mag = float((qq.abs() @ kk.abs().T).max()) / math.sqrt(dim)
             ds, sums = (dim + 8) * 2.0 ** -23 * mag, (m / 16 + 64) * 2.0 ** -23
             # (sums: as above; they grow with the rows of one share, not with m, but the bound need not be tight)
             tol = (2 * ds + 2.0 ** -20 + 2.0 ** -16 + sums) * (p @ vv.abs()) + (2.0 ** -8 + 2.0 ** -22) * ref.abs()
@@ -386,6 +387,48 @@ def test_decode_of_long_lists(A, lens):
             assert float((lse[b, 2 * h: 2 * h + 2].double() - ref_lse).abs().max()) <= ds + sums + 2.0 ** -18
             tw = p.sum(0) * (2 * ds + 2.0 ** -19 + sums)
             assert bool(((wo[b, h, :m].double() - p.sum(0)).abs() <= tw + 1e-12).all())
+
+
+def test_long_lists_at_once_and_in_graphs(A):
+    # two calls with claims on two streams: each grid's CTAs come and go as the other leaves room, so a CTA may take
+    # over one that would have been resident; results stay bit for bit those of a call alone
+    rows, hkv, heads, dim, page, n = 2, 8, 8, 128, 256, 90000
+    width = -(-n // page)
+    gen = torch.Generator(device="cuda").manual_seed(78)
+    sets = []
+    for i in range(2):
+        k, v = (torch.randn(rows * width, hkv, page, dim, generator=gen, device="cuda", dtype=HF) for _ in range(2))
+        table = torch.randperm(rows * width, generator=gen, device="cuda").view(rows, width).to(torch.int32)
+        cache = A.make_gqa_cache(k, v, table)
+        q = torch.randn(rows, heads, dim, generator=gen, device="cuda", dtype=HF)
+        lens = torch.tensor([n, n - 777 * i - 1], dtype=torch.int32).cuda()
+        sets.append((cache, q, lens, A.dsv4_gqa_decode(q, lens, cache)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(8):
+        got = []
+        for s, (cache, q, lens, _) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    got.append(A.dsv4_gqa_decode(q, lens, cache))
+        torch.cuda.synchronize()
+        for i, (out, lse) in enumerate(got):
+            want = sets[i // 3][3]
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    graphs = []
+    for cache, q, lens, _ in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = A.dsv4_gqa_decode(q, lens, cache)
+        graphs.append((g, res))
+    for _ in range(4):
+        for s, (g, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, res), (_, _, _, want) in zip(graphs, sets):
+            assert torch.equal(res[0], want[0]) and torch.equal(res[1], want[1])
+    assert A.dsv4_attn_get_device_error() == 0
 
 
 # ---------------------------------------------------------------- store

@@ -174,7 +174,9 @@ def test_binding_refuses_mismatched_arguments(A):
         lambda: A.dsv4_gqa_decode(q, lens, c),                       # the pools are not on a CUDA device
         lambda: A.dsv4_gqa_store(q[:, :2], q[:, :2], lens[:2], lens, c),
         lambda: A.dsv4_gqa_store(q[:, :2], q[:, :2].half(), lens, lens, c),
-        lambda: A.dsv4_gqa_store(q, q, lens, lens, c),
+        lambda: A.dsv4_gqa_store(q, q, lens, lens, c), lambda: A.dsv4_gqa_store(q[0], q[0], lens, lens, c),
+        lambda: A.dsv4_gqa_store(q[:, :2], q[0], lens, lens, c),
+        lambda: A.dsv4_gqa_store(q[:, :2].float(), q[:, :2].float(), lens, lens, c),
         lambda: A.dsv4_gqa_store(q[:, :2], q[:, :2], lens, lens, c, positions=ints),
         lambda: A.dsv4_gqa_store(q[:, :2], q[:, :2], lens, lens, c, token_positions=lens),
         lambda: A.dsv4_gqa_store(q[:, :2], q[:, :2], lens, lens, c, weights=w[:, :1]),
