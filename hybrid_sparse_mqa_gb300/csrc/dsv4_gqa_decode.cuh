@@ -16,8 +16,8 @@
 // heads of 64.)
 //
 // SMs do not get equal bandwidth (equal shares ended between 117 and 165 us
-// for 2 x 131072 rows), so of a long list the last eighth of every warp's part
-// is given out to whoever is free.  A share for each warp of a CTA makes up one
+// for 2 x 131072 rows), so of a long list the last 3/32 of every warp's part
+// are given out to whoever is free.  A share for each warp of a CTA makes up one
 // more CTA of the grid, which a resident CTA that runs out of tiles takes over
 // before it is launched (clusterlaunchcontrol.try_cancel): the hardware's own
 // queue, with no counter in memory.  What a share holds does not depend on who
@@ -55,12 +55,13 @@ constexpr int kWarps = 4;                  // warps per CTA
 constexpr int kMaxCtas = 304;              // resident at once: two per SM
 // What is kept back of a warp's part of a long list, in 32nds.  Taking another
 // share costs a piece to write and join and some stalled loads: 32 x
-// 2048..32768 rows (230 tiles per warp) go from 352 to 336 us, 2 x 131072 rows
-// (108) from 171 to 165, while 64 x 1024..16384 e4m3 rows (34) would go from 99
-// to 102.  Two or three rounds of smaller shares gained no more.
-constexpr int kTail = 4;
+// 2048..32768 rows (230 tiles per warp) go from 345 to 328 us, 2 x 131072 rows
+// (108) from 170 to 163, while 64 x 1024..16384 e4m3 rows (57) would go from 98
+// to 99 and 48 x up to 2000 rows of 64 (15) from 34 to 36.  Two or three rounds
+// of smaller shares gained no more.
+constexpr int kTail = 3;
 constexpr int kClaimTiles = 64;            // a list is long from so many tiles per resident warp
-constexpr int kClaimAhead = 6;             // tiles before the end of a share at which the next is asked for
+constexpr int kClaimAhead = 4;             // tiles before the end of a share at which the next is asked for
 constexpr int kClaimRing = 16;             // claims that a warp may be behind another of its CTA
 constexpr int kWaitLimit = 1 << 20;        // polls before a claim is given up
 
@@ -219,6 +220,10 @@ __device__ __forceinline__ uint64_t evict_first_policy() {
 __device__ __forceinline__ void cp_async_16_hint(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(src_bytes),
                  "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_16_whole(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
                  : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -471,6 +476,13 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     int page = -1;                                 // lane m < MT: page of 16-slot group m of the next tile
     bool wanted = false;                           // that group holds slots to attend
     const uint32_t qbuf = smem_u32(smem) + S::RING_BYTES + warp * S::Q_BYTES;
+    int pslot = 0;                                 // first slot of prod's tile
+    long long phead = 0;                           // byte offset of its KV head, and of this lane's first piece
+    auto come_to = [&]() {
+        pslot = (prod.rg.lo / TT + static_cast<int>(prod.at - prod.seg)) * TT;
+        phead = (prod.hc / p.chunks) * p.c.head_stride + lane_off;
+    };
+    come_to();
     int pieces = 0, piece = 0;                     // pieces (a share's part of a segment) that prod has come to; cons's
     int q_piece = -1;                              // piece whose queries the buffer holds or is getting
     bool q_free = true, fresh = true;              // they have been read; prod has just come to its piece
@@ -505,11 +517,12 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                     prod.bound(p1);
                 }
             }
+            come_to();
         }
         page = -1;
         wanted = false;
         if (more && lane < MT) {
-            const int slot = (prod.rg.lo / TT + static_cast<int>(prod.at - prod.seg)) * TT + lane * 16;
+            const int slot = pslot + lane * 16;
             wanted = slot < prod.rg.n && slot + 16 > prod.rg.lo;
             if (wanted) page = __ldg(p.c.table + (long long)prod.rq.row * p.c.table_stride + (slot >> p.c.page_shift));
         }
@@ -530,29 +543,39 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         }
         fresh = false;
         if (more) {
-            const int slot0 = (prod.rg.lo / TT + static_cast<int>(prod.at - prod.seg)) * TT;
             const bool ok = page >= 0 && page < p.c.num_pages;
             if (wanted && !ok) atomicOr(p.err, DSV4_DEV_ERR_GQA_PAGE);
             const unsigned okm = __ballot_sync(0xffffffffu, ok);
             if (lane == 0) s_ok[warp][stage] = okm;
-            const long long head = (prod.hc / p.chunks) * p.c.head_stride + lane_off;
             const uint32_t kd = ring + stage * 2 * S::TILE_BYTES, vd = kd + S::TILE_BYTES;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int pg = __shfl_sync(0xffffffffu, page, m);
                 const bool have = (okm >> m) & 1;
-                const int s = slot0 + m * 16;
-                const long long base =
-                    have ? pg * p.c.page_stride + (s & page_mask) * p.c.row_stride + head : 0;
+                const int s = pslot + m * 16;
+                const long long base = have ? pg * p.c.page_stride + (s & page_mask) * p.c.row_stride + phead : 0;
+                const uint8_t *ks = p.c.k + base, *vs = p.c.v + base;
+                if (have && s >= prod.rg.lo && s + 16 <= prod.rg.n) {
 #pragma unroll
-                for (int i = 0; i < 16 / S::RPI; ++i) {
-                    const int r = i * S::RPI + lane_row;        // row in the group
-                    const bool in = have && s + r < prod.rg.n && s + r >= prod.rg.lo;
-                    const long long off = in ? base + i * S::RPI * p.c.row_stride : 0;
-                    cp_async_16_hint(kd + k_offset<S>(m * 16 + r, lane_piece), p.c.k + off, in ? 16u : 0u, policy);
-                    cp_async_16_hint(vd + v_offset<S>(m * 16 + r, lane_piece), p.c.v + off, in ? 16u : 0u, policy);
+                    for (int i = 0; i < 16 / S::RPI; ++i) {
+                        const int r = m * 16 + i * S::RPI + lane_row;
+                        cp_async_16_whole(kd + k_offset<S>(r, lane_piece), ks, policy);
+                        cp_async_16_whole(vd + v_offset<S>(r, lane_piece), vs, policy);
+                        ks += S::RPI * p.c.row_stride;
+                        vs += S::RPI * p.c.row_stride;
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < 16 / S::RPI; ++i) {
+                        const int r = i * S::RPI + lane_row;        // row in the group
+                        const bool in = have && s + r < prod.rg.n && s + r >= prod.rg.lo;
+                        const long long off = in ? i * S::RPI * p.c.row_stride : 0;
+                        cp_async_16_hint(kd + k_offset<S>(m * 16 + r, lane_piece), in ? ks + off : p.c.k, in ? 16u : 0u, policy);
+                        cp_async_16_hint(vd + v_offset<S>(m * 16 + r, lane_piece), in ? vs + off : p.c.v, in ? 16u : 0u, policy);
+                    }
                 }
             }
+            pslot += TT;
             ++prod.at;
             settle();
         }
@@ -648,7 +671,9 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
             const unsigned okm = s_ok[warp][stage];
             const int slot0 = (cons.rg.lo / TT + static_cast<int>(tile - cons.seg)) * TT;
 
-            // S^T = K Q^T
+            // S^T = K Q^T (a lone accumulator as two chains of MMAs)
+            constexpr int kChains = MT * NT == 1 ? 2 : 1;
+            float s2[1][1][4] = {};
             float s[MT][NT][4];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
@@ -665,8 +690,12 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                         uint32_t a[4];
                         ldsm4(a, ks + k_offset<S>(m * 16 + mrow, 2 * kk + mpiece));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816<S::BF16>(s[m][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<S::BF16>(kChains > 1 && kk & 1 ? s2[0][0] : s[m][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
                     }
+                if constexpr (kChains > 1)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[0][0][c] += s2[0][0][c];
             } else {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
@@ -840,14 +869,18 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                     const int c = nt * 8 + 2 * t4 + u;
                     if (c >= nheads) continue;
                     float* to = p.part_o + ((size_t)entry * HEADS + c) * D;
+                    if constexpr (!S::FP8) {
 #pragma unroll
-                    for (int j = 0; j < DT; ++j) {
-                        if constexpr (!S::FP8) {
+                        for (int j = 0; j < DT; ++j) {
                             to[16 * j + g] = o[j][nt][u];
                             to[16 * j + 8 + g] = o[j][nt][u + 2];
-                        } else {
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < DT; j += 2) {
                             const int d = D == 64 ? 8 * g + 2 * j : 16 * (g + 8 * (j >> 3)) + 2 * (j & 7);
-                            *reinterpret_cast<float2*>(to + d) = make_float2(o[j][nt][u], o[j][nt][u + 2]);
+                            *reinterpret_cast<float4*>(to + d) =
+                                make_float4(o[j][nt][u], o[j][nt][u + 2], o[j + 1][nt][u], o[j + 1][nt][u + 2]);
                         }
                     }
                     if (g == 0) p.part_ml[entry * HEADS + c] = make_float2(mref[nt][u], lsum[nt][u]);
