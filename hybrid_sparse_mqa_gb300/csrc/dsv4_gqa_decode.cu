@@ -2,6 +2,8 @@
 // grouped-query cache, and the two kernels behind the attention kernel
 // (dsv4_gqa_decode.cuh): the join of split requests and the accumulation of
 // weights.
+#include <algorithm>
+
 #include "dsv4_gqa_decode.cuh"
 
 namespace dsv4 {
@@ -10,26 +12,30 @@ namespace {
 
 constexpr int kWeightThreads = 256;
 constexpr int kWeightSlots = 4;            // slots per thread
-constexpr int kMinTiles = 2;               // per share: below, more warps would not shorten the chain of loads
+// Tiles per share at least: 1 where no segment has more than kFewTiles, else 2.
+// (One request, 8 KV heads: 333 rows 6.7 us with 1 and 7.7 with 2, 1000 rows
+// 8.6 and 8.3, 3000 rows 11.3 and 9.6, the difference being the pieces to join.)
+constexpr int kFewTiles = 32;
 
 // Joins the pieces of cut segments.  With M = max_i m_i,
 //   out = sum_i 2^(m_i - M) o_i / (sum_i 2^(m_i - M) l_i + sink term).
-// Block (segment, 8 / PW heads or one): PW warps per head share its pieces, so
-// that a long segment's many pieces are read at once (PW = 8, or 16) and short
-// segments do not cost a block per head (PW = 1).  Every block finds its segment's tiles
-// from the lengths, as the attention kernel did; that part runs before the
-// wait for it (the attention kernel itself starts behind the call's inputs,
-// and only then lets this one go).  Requests without rows get their output
-// here.
-template <int D, int TT, int HEADS, int PW>
+// Block (segment, 8 / PW heads or one, slice of D / SLICES dims): PW warps per
+// head share its pieces, so that a long segment's many pieces are read at once,
+// and short segments do not cost a block per head (PW = 1).  Every block finds
+// its segment's tiles from the lengths, as the attention kernel did; that part
+// runs before the wait for it (the attention kernel itself starts behind the
+// call's inputs, and only then lets this one go).  Requests without rows get
+// their output here.  Bound by latency: a round trip for the lengths, one per
+// batch of pieces.
+template <int D, int TT, int HEADS, int PW, int SLICES>
 __global__ void __launch_bounds__(PW > 8 ? PW * 32 : 256) dsv4_gqa_join_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int kHeads = PW < 8 ? 8 / PW : 1;              // per block
     constexpr int kThreads = PW * kHeads * 32;
-    constexpr int V = D / 32;                  // values per lane
+    constexpr int DS = D / SLICES, V = DS / 32;              // dims of the block, values per lane
     __shared__ unsigned s_sum[2][kThreads / 32];
     __shared__ int s_near[2][kThreads / 32];
     __shared__ float2 s_ml[PW * kHeads];
-    __shared__ float s_o[PW > 1 ? PW : 1][PW > 1 ? D : 1];
+    __shared__ float s_o[PW > 1 ? PW : 1][PW > 1 ? DS : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hcs = p.c.kv_heads * p.chunks;
     const int b = blockIdx.x / hcs, hc = blockIdx.x % hcs;
@@ -38,7 +44,7 @@ __global__ void __launch_bounds__(PW > 8 ? PW * 32 : 256) dsv4_gqa_join_kernel(c
     int next = 0x7fffffff, earlier = 0;
     const Request rq = read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, err);
     const Range rg = key_range<TT>(p, rq.n);
-    const bool link = p.info && hc == 0 && blockIdx.y == 0;
+    const bool link = p.info && hc == 0 && blockIdx.y == 0 && blockIdx.z == 0;
     for (int e = tid; e < p.batch; e += kThreads) {
         const Request x = read_request(p.lens, p.req, p.c.table_rows, p.max_len, e, err);
         const unsigned cnt = key_range<TT>(p, x.n).tiles * hcs;
@@ -86,13 +92,14 @@ __global__ void __launch_bounds__(PW > 8 ? PW * 32 : 256) dsv4_gqa_join_kernel(c
     const int head = blockIdx.y * kHeads + warp / PW;          // in the segment
     const bool mine = chunk * HEADS + head < p.group;
     const size_t at = (size_t)b * p.heads + h * p.group + chunk * HEADS + head;
-    uint16_t* out = static_cast<uint16_t*>(p.out) + at * D + lane * V;
+    const int d0 = SLICES > 1 ? blockIdx.z * DS : 0;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + at * D + d0 + lane * V;
     const float sk = p.sink && mine ? __ldg(p.sink + h * p.group + chunk * HEADS + head) * kLog2e : -INFINITY;
     if (rg.tiles == 0) {
         if (mine && warp % PW == 0) {
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) reinterpret_cast<uint32_t*>(out)[i] = 0u;
-            if (lane == 0) {
+            for (int i = 0; i < V; ++i) out[i] = 0;
+            if (lane == 0 && d0 == 0) {
                 if (p.lse) p.lse[at] = sk * kLn2;
                 if (p.lse2) p.lse2[at] = sk;
             }
@@ -104,7 +111,7 @@ __global__ void __launch_bounds__(PW > 8 ? PW * 32 : 256) dsv4_gqa_join_kernel(c
     float a[V] = {}, mx = kNoMax, l = 0.f;
     if (mine) {
         // this warp's pieces, kBatch at a time; the reference moves between batches
-        constexpr int kBatch = V > 4 ? 4 : 8;
+        constexpr int kBatch = V > 4 ? 4 : V > 1 ? 8 : 16;
         for (int i0 = warp % PW; i0 < pieces; i0 += PW * kBatch) {
             float2 ml[kBatch];
             float x[kBatch][V];
@@ -115,8 +122,10 @@ __global__ void __launch_bounds__(PW > 8 ? PW * 32 : 256) dsv4_gqa_join_kernel(c
                 if (i < pieces) {
                     const size_t e = (size_t)piece_entry(c0 + i, i == 0) * HEADS + head;
                     ml[k] = p.part_ml[e];
-                    const float* from = p.part_o + e * D + lane * V;
-                    if constexpr (V == 2) {
+                    const float* from = p.part_o + e * D + d0 + lane * V;
+                    if constexpr (V == 1) {
+                        x[k][0] = *from;
+                    } else if constexpr (V == 2) {
                         const float2 y = *reinterpret_cast<const float2*>(from);
                         x[k][0] = y.x; x[k][1] = y.y;
                     } else {
@@ -154,7 +163,7 @@ __global__ void __launch_bounds__(PW > 8 ? PW * 32 : 256) dsv4_gqa_join_kernel(c
 #pragma unroll
         for (int q = 0; q < V; ++q) s_o[warp][lane * V + q] = a[q];
         __syncthreads();
-        if (tid >= D || !mine) return;
+        if (tid >= DS || !mine) return;
         mx = kNoMax;
 #pragma unroll
         for (int w = 0; w < PW; ++w) mx = fmaxf(mx, s_ml[w].x);
@@ -172,8 +181,8 @@ __global__ void __launch_bounds__(PW > 8 ? PW * 32 : 256) dsv4_gqa_join_kernel(c
         const bool any = l > 0.f || l != l;
         x *= any ? (p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f) * f / l : 0.f;
         const uint32_t w2 = p.q_bf16 ? pack2<true>(x, 0.f) : pack2<false>(x, 0.f);
-        static_cast<uint16_t*>(p.out)[at * D + tid] = static_cast<uint16_t>(w2);
-        if (tid == 0) {
+        static_cast<uint16_t*>(p.out)[at * D + d0 + tid] = static_cast<uint16_t>(w2);
+        if (tid == 0 && d0 == 0) {
             const float l2 = any ? top + log2f(l) : -INFINITY;
             if (p.lse) p.lse[at] = l2 * kLn2;
             if (p.lse2) p.lse2[at] = l2;
@@ -277,7 +286,7 @@ int tile_slots(int format, int head_dim) {
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct Plan {
-    int group, nt, chunks, tt;
+    int group, nt, chunks, tt, min_tiles;
     long long tiles;                       // bound on the tile list
     int ctas, claims;                      // resident CTAs of the attention kernel, and claimable ones
     size_t part_o, part_ml, lse2, info, logits, bytes;      // offsets, size
@@ -298,7 +307,8 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
     if (pl.tiles >= 1LL << 31 || segments >= 1LL << 31) return DSV4_ERR_UNSUPPORTED;
     // (512-byte rows: one CTA's ring fills an SM's shared memory)
     const int most = c->head_dim * (c->format == DSV4_GQA_E4M3 ? 1 : 2) > 256 ? kMaxCtas / 2 : kMaxCtas;
-    const long long want = pl.tiles / kMinTiles;
+    pl.min_tiles = (max_len + pl.tt - 1) / pl.tt <= kFewTiles ? 1 : 2;
+    const long long want = pl.tiles / pl.min_tiles;
     pl.ctas = want < 1 ? 1 : (want < most ? static_cast<int>(want) : most);
     pl.claims = pl.ctas == most && pl.tiles >= (long long)most * kWarps * kClaimTiles ? most : 0;
     const size_t entries = size_t(2) * (pl.ctas + pl.claims) * kWarps * 8 * pl.nt;
@@ -314,13 +324,18 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
 template <int D, int TT, int HEADS>
 int launch_join_heads(const DecodeParams& p, void* stream) {
     const unsigned segments = p.batch * p.c.kv_heads * p.chunks;
-    // pieces of a segment, if all are about as long
-    const unsigned pieces = (p.warps + p.claims * kWarps) / segments + 1;
+    // pieces of a segment, if all are about as long, and blocks of one head each.  (us of a whole decode call with the
+    // choice made and with the other: 1 segment x 131072 rows, 1216 pieces of 8 heads: slices 26.6, no slices 35.9;
+    // 16 segments, 85 pieces: PW = 16 165, slices 171, PW = 1 180; 8 segments, 10 pieces: PW = 8 7.7, PW = 1 8.1;
+    // 256 segments, 5 pieces: PW = 1 98, PW = 8 105)
+    const unsigned pieces = p.pieces / segments + 1, heads = segments * HEADS;
+    if (pieces > 96 && heads <= 64)
+        return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 16, D / 32>, dim3(segments, HEADS, D / 32), 512, 0, stream, 1, p);
     if (pieces > 96)
-        return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 16>, dim3(segments, HEADS), 512, 0, stream, 1, p);
-    if (pieces > 32)
-        return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 8>, dim3(segments, HEADS), 256, 0, stream, 1, p);
-    return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 1>, dim3(segments, HEADS / 8), 256, 0, stream, 1, p);
+        return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 16, 1>, dim3(segments, HEADS), 512, 0, stream, 1, p);
+    if (pieces > 8 && heads <= 1024)
+        return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 8, 1>, dim3(segments, HEADS), 256, 0, stream, 1, p);
+    return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 1, 1>, dim3(segments, HEADS / 8), 256, 0, stream, 1, p);
 }
 
 template <int D, int TT>
@@ -395,9 +410,10 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     p.w_out = weights_out;
     p.width = width;
     p.decay = decay;
-    p.min_tiles = kMinTiles;
+    p.min_tiles = pl.min_tiles;
     p.warps = pl.ctas * kWarps;
     p.claims = pl.claims;
+    p.pieces = static_cast<int>(std::min<long long>(p.warps + p.claims * kWarps, pl.tiles / pl.min_tiles));
     p.err = err;
 
     const int d = cache->head_dim;

@@ -93,6 +93,7 @@ struct DecodeParams {
     int min_tiles;                         // a share has at least this many tiles (where there are as many)
     int warps;                             // of the resident CTAs
     int claims;                            // CTAs of the grid behind those, to be claimed (0: none)
+    int pieces;                            // bound on the shares (for the host)
     unsigned int* err;
 };
 

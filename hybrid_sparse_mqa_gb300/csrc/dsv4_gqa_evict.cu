@@ -13,9 +13,13 @@
 // chunks that have any are visited again.  Histograms and
 // counts are combined over the cluster through distributed shared memory;
 // every count is exact and every order is that of the slots, so the result
-// does not depend on timing.  The move kernel copies the listed rows: only
-// rows that change their slot are read and written, each once.  It is bound by
-// HBM (4 head_dim bytes x element size per moved row and direction).
+// does not depend on timing.  Bound by the chain of round trips and barriers:
+// 13 us for 256 heads of 4200 to 5120 rows (load 4, then 1.3 per digit), 18 us
+// for 64 of 20000 to 32768 with clusters of four.  The move kernel copies the
+// listed rows: only rows that change their slot are read and written, each
+// once.  It is bound by HBM: 38 us for 188 MB of 256-byte rows from anywhere
+// in 32768 slots (4.9 TB/s).  One kernel for both took as long for few rows and
+// longer for many.
 #include "dsv4_gqa.cuh"
 
 namespace dsv4 {
@@ -221,8 +225,8 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
     int* movers = p.movers + (size_t)id * p.most;
     if constexpr (CLUSTER == 1 && KEYS > 0) {
         // A cache just over its bound, as after every step of a decode loop: the few rows to go are looked for one by
-        // one, smallest key first, of equal ones the highest slot.  (One of 2049 rows, 512 rows of weights: 17 us
-        // together with the move kernel by the radix select, NEW_STEP us so.)
+        // one, smallest key first, of equal ones the highest slot.  (One of 2049 rows for each of 512 heads, with the
+        // move: 17 us by the radix select, 8 us so; four of 2052: 15.8 and 12.7.)
         if (n - p.keep <= kFew) {
             int gone[kFew];
             for (int e = 0; e < n - p.keep; ++e) {
@@ -573,6 +577,9 @@ int launch_select_cluster(const EvictParams& p, int per, void* stream) {
 
 // The smallest CTA that holds a row's keys, or a cluster of them: where there
 // are few rows, several CTAs share one, as long as each has 2048 slots or more.
+// (64 rows of 32768: one CTA each 77.8 us with the move, clusters of four 57.8,
+// of eight 73.1, which no longer run all at once; 8 rows of 100000: clusters
+// of four, the fewest that hold the keys, 44 us, of eight 28.7.)
 int launch_select(const EvictParams& p, void* stream) {
     const int ids = p.batch * p.c.kv_heads;
     int cluster = 1;
