@@ -23,6 +23,11 @@
 // queue, with no counter in memory.  What a share holds does not depend on who
 // takes it, so results do not either.
 //
+// Short lists (SEG) are done in one launch: a cluster of 1 to 8 CTAs takes a
+// segment, its warps equal parts of the tiles, and they merge through
+// distributed shared memory.  That spares the second launch (2.4 us of host
+// time of 9.4), and the pieces' way through L2.
+//
 // A warp streams its tiles through its own ring of cp.async stages, which runs
 // ahead over segment and share boundaries, and the queries of the next segment
 // with them.  Scores are computed transposed, S^T = K Q^T,
@@ -94,6 +99,7 @@ struct DecodeParams {
     int warps;                             // of the resident CTAs
     int claims;                            // CTAs of the grid behind those, to be claimed (0: none)
     int pieces;                            // bound on the shares (for the host)
+    int cluster;                           // CTAs per segment, where segments are not cut (0: by shares)
     unsigned int* err;
 };
 
@@ -252,6 +258,12 @@ __device__ __forceinline__ int claim_result(uint32_t result) {
     return ok ? static_cast<int>(x) : -1;
 }
 
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
 // ---------------------------------------------------------------- shape
 // KIND: DSV4_GQA_BF16 / F16 / E4M3.  A warp's stage is TT rows of K and of V.
 template <int KIND_, int D_, int NT_>
@@ -360,7 +372,8 @@ struct Cursor {
     }
 };
 
-template <class S>
+// SEG: a cluster per segment; else a share of the list per warp.
+template <class S, bool SEG>
 __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int D = S::D, NT = S::NT, W = S::W, TT = S::TT, MT = S::MT, DT = S::DT, HEADS = S::HEADS;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -370,12 +383,13 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     __shared__ int s_cta[kClaimRing], s_known, s_done[W], s_lock, s_phase;
     __shared__ __align__(16) uint8_t s_answer[16];
     __shared__ __align__(8) uint64_t s_bar;
+    __shared__ float2 s_ml[SEG ? W : 1][SEG ? HEADS : 1];     // references and sums of the warps
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     const int hcs = p.c.kv_heads * p.chunks;
     const uint32_t bar = smem_u32(&s_bar);
-    if (tid == 0) {
+    if (!SEG && tid == 0) {
         s_cta[0] = blockIdx.x;
         s_known = 1;
         s_lock = s_phase = 0;
@@ -384,32 +398,49 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         mbar_init(bar, 1);
         fence_mbar_init_cluster();
     }
-    __syncthreads();
+    if constexpr (!SEG) __syncthreads();
     grid_dependency_wait();
     grid_dependents_go();
 
-    // one request per lane; the first 32 stay in registers
     unsigned err = 0;
     auto request_of = [&](int b) {
         Request r{0, 0};
         return b < p.batch ? read_request(p.lens, p.req, p.c.table_rows, p.max_len, b, err) : r;
     };
-    const Request early = request_of(lane);
-    unsigned total = key_range<TT>(p, early.n).tiles;
-    for (int b = lane + 32; b < p.batch; b += 32) total += key_range<TT>(p, request_of(b).n).tiles;
-    total = __reduce_add_sync(0xffffffffu, total) * hcs;
-    if (err && blockIdx.x == 0 && warp == 0) atomicOr(p.err, err);
-    if (total == 0) return;
-    const Shares shares = make_shares(p, total);
+    Request early{0, 0};                          // one request per lane: the first 32 stay in registers
+    Shares shares{};
+    Cursor<TT> cons;
+    unsigned c1 = 0;                              // end of cons's share
+    if constexpr (SEG) {
+        const int seg = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+        cons.b = seg / hcs;
+        cons.hc = seg % hcs;
+        cons.rq = read_request(p.lens, p.req, p.c.table_rows, p.max_len, cons.b, err);
+        if (err && cons.hc == 0 && rank == 0 && tid == 0) atomicOr(p.err, err);
+        cons.rg = key_range<TT>(p, cons.rq.n);
+        cons.seg = 0;
+        const int i = warp * p.cluster + rank, n = W * p.cluster;        // this warp's part
+        cons.at = cons.rg.tiles * i / n;
+        c1 = cons.end = cons.rg.tiles * (i + 1) / n;
+    } else {
+        early = request_of(lane);
+        unsigned total = key_range<TT>(p, early.n).tiles;
+        for (int b = lane + 32; b < p.batch; b += 32) total += key_range<TT>(p, request_of(b).n).tiles;
+        total = __reduce_add_sync(0xffffffffu, total) * hcs;
+        if (err && blockIdx.x == 0 && warp == 0) atomicOr(p.err, err);
+        if (total == 0) return;
+        shares = make_shares(p, total);
+    }
+    const unsigned tail = SEG ? 0u : shares.tail;
     // warps of one resident CTA take shares far apart, so that few shares spread over all SMs
     const int ctas = p.warps / W;
     auto share_id = [&](int cta) {
-        if (cta < ctas) return (warp * ctas + cta) * (shares.tail ? 2 : 1);
+        if (cta < ctas) return (warp * ctas + cta) * (tail ? 2 : 1);
         const int j = (cta - ctas) * W + warp;
-        return shares.tail ? 2 * j + 1 : shares.count;       // (short list: nothing)
+        return tail ? 2 * j + 1 : shares.count;       // (short list: nothing)
     };
-    const int first = share_id(blockIdx.x);
-    if (first >= shares.count) {
+    const int first = SEG ? 0 : share_id(blockIdx.x);
+    if (!SEG && first >= shares.count) {
         if (lane == 0) *(volatile int*)&s_done[warp] = 0x3fffffff;
         return;
     }
@@ -452,9 +483,8 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         return __shfl_sync(0xffffffffu, got, 0);
     };
 
-    Cursor<TT> cons;
-    unsigned c1 = share_begin(shares, first + 1);
-    {
+    if constexpr (!SEG) {
+        c1 = share_begin(shares, first + 1);
         cons.at = share_begin(shares, first);
         cons.locate(p, hcs, lane, early, request_of);
         cons.bound(c1);
@@ -473,7 +503,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     unsigned p1 = c1;
     int entry_p = 0, next_p = -2;                  // prod's entry of s_cta; the one behind it, once it is known
     bool asking = false;
-    bool more = true;
+    bool more = !SEG || cons.at < cons.end;
     int page = -1;                                 // lane m < MT: page of 16-slot group m of the next tile
     bool wanted = false;                           // that group holds slots to attend
     const uint32_t qbuf = smem_u32(smem) + S::RING_BYTES + warp * S::Q_BYTES;
@@ -490,7 +520,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
 
     // prod to the tile that is copied next; its page ids are loaded one tile ahead of their use
     auto settle = [&]() {
-        if (shares.tail && more) {
+        if (tail && more) {
             // the next share is asked for a little before this one ends
             asking |= prod.at + kClaimAhead >= p1;
             if (asking && next_p == -2) next_p = taken(entry_p + 1);
@@ -498,8 +528,10 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         if (more && prod.at >= prod.end) {
             fresh = true;
             ++pieces;
-            if (!prod.next_segment(p, hcs, p1)) {
-                for (int tries = 0; shares.tail && next_p == -2; ++tries) {
+            if (SEG) {
+                more = false;
+            } else if (!prod.next_segment(p, hcs, p1)) {
+                for (int tries = 0; tail && next_p == -2; ++tries) {
                     next_p = taken(entry_p + 1);
                     if (tries >= kWaitLimit) {
                         if (lane == 0) atomicOr(p.err, DSV4_DEV_ERR_TIMEOUT);
@@ -849,6 +881,75 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         // the next piece, if there is one
         const bool cut = !begins || cons.end != cons.seg + cons.rg.tiles;
         const int here_b = cons.b, here = share;
+        if constexpr (SEG) {
+            // the warps' rings become their outputs, [HEADS][D] fp32 (padded rows), and the cluster adds them up
+            constexpr int kRow = D + 4;
+            static_assert(HEADS * kRow * 4 <= S::STAGES * 2 * S::TILE_BYTES, "a warp's output fits its ring");
+            cp_async_wait_group<0>();
+            __syncwarp();
+            float* mine = reinterpret_cast<float*>(smem + warp * (S::STAGES * 2 * S::TILE_BYTES));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int c = nt * 8 + 2 * t4 + u;
+                    if (g == 0) s_ml[warp][c] = make_float2(mref[nt][u], lsum[nt][u]);
+#pragma unroll
+                    for (int j = 0; j < DT; ++j) {
+                        if constexpr (!S::FP8) {
+                            mine[c * kRow + 16 * j + g] = o[j][nt][u];
+                            mine[c * kRow + 16 * j + 8 + g] = o[j][nt][u + 2];
+                        } else {
+                            const int d = D == 64 ? 8 * g + 2 * j : 16 * (g + 8 * (j >> 3)) + 2 * (j & 7);
+                            *reinterpret_cast<float2*>(mine + c * kRow + d) = make_float2(o[j][nt][u], o[j][nt][u + 2]);
+                        }
+                    }
+                }
+            cluster_sync();
+            const int rank = blockIdx.x % p.cluster;
+            const float vmul = S::FP8 && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
+            const uint32_t ml0 = smem_u32(&s_ml[0][0]), o0 = smem_u32(smem);
+            for (int e = rank * W * 32 + tid; e < nheads * D / 2; e += p.cluster * W * 32) {
+                const int c = e / (D / 2), d = e % (D / 2) * 2;
+                // one CTA's warps after another; the reference moves between CTAs
+                float mx = kNoMax, l = 0.f, x = 0.f, y = 0.f;
+                for (int r = 0; r < p.cluster; ++r) {
+                    float2 ml[W], v[W];
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        ml[w] = ld_cluster_f2(mapa(ml0 + (w * HEADS + c) * 8, r));
+                        v[w] = ld_cluster_f2(mapa(o0 + w * (S::STAGES * 2 * S::TILE_BYTES) + (c * kRow + d) * 4, r));
+                    }
+                    float top = mx;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w].x);
+                    const float f = fast_exp2(mx - top);
+                    mx = top;
+                    l *= f;
+                    x *= f;
+                    y *= f;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        const float k = fast_exp2(ml[w].x - top);
+                        l += k * ml[w].y;
+                        x += k * v[w].x;
+                        y += k * v[w].y;
+                    }
+                }
+                const float sk = p.sink ? __ldg(p.sink + head0 + c) * kLog2e : -INFINITY;
+                const float top = fminf(fmaxf(mx, sk), 3e38f);
+                const float f = fast_exp2(mx - top);
+                l = l * f + fast_exp2(sk - top);
+                const bool any = l > 0.f || l != l;
+                const float inv = any ? vmul * f / l : 0.f;
+                const size_t at = (size_t)here_b * p.heads + head0 + c;
+                *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at * D + d) =
+                    p.q_bf16 ? pack2<true>(x * inv, y * inv) : pack2<false>(x * inv, y * inv);
+                if (d == 0 && p.lse) p.lse[at] = any ? (top + log2f(l)) * kLn2 : -INFINITY;
+            }
+            cluster_sync();                       // (no CTA may end while another reads its shared memory)
+            return;
+        }
         on = cons.next_segment(p, hcs, c1);
         if (!on && entry_c < entry_p) {
             ++entry_c;
@@ -947,22 +1048,29 @@ int launch_decode_bf16(const DecodeParams& p, int head_dim, int nt, void* stream
 int launch_decode_f16(const DecodeParams& p, int head_dim, int nt, void* stream);
 int launch_decode_e4m3(const DecodeParams& p, int head_dim, int nt, void* stream);
 
-template <class S>
-inline int launch_decode_shape(const DecodeParams& p, void* stream) {
+template <class S, bool SEG>
+inline int launch_decode_kernel(const DecodeParams& p, unsigned grid, int cluster, void* stream) {
     // shared memory beyond 48 KB is asked for once per device
     static unsigned long long ready = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DSV4_ERR_CUDA;
     if (dev < 0 || dev >= 64) return DSV4_ERR_CUDA;
     if (!(__atomic_load_n(&ready, __ATOMIC_ACQUIRE) >> dev & 1)) {
-        if (cudaFuncSetAttribute(dsv4_gqa_decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) !=
+        if (cudaFuncSetAttribute(dsv4_gqa_decode_kernel<S, SEG>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) !=
             cudaSuccess) {
             cudaGetLastError();
             return DSV4_ERR_CUDA;
         }
         __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELEASE);
     }
-    return launch(dsv4_gqa_decode_kernel<S>, dim3(p.warps / S::W + p.claims), S::W * 32, S::SMEM, stream, 1, p);
+    return launch(dsv4_gqa_decode_kernel<S, SEG>, dim3(grid), S::W * 32, S::SMEM, stream, cluster, p);
+}
+
+template <class S>
+inline int launch_decode_shape(const DecodeParams& p, void* stream) {
+    if (p.cluster)
+        return launch_decode_kernel<S, true>(p, p.batch * p.c.kv_heads * p.chunks * p.cluster, p.cluster, stream);
+    return launch_decode_kernel<S, false>(p, p.warps / S::W + p.claims, 1, stream);
 }
 
 template <int KIND>

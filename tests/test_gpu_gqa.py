@@ -133,13 +133,22 @@ def check_decode(A, case, lens, heads, *, window=0, sink=None, req=None, weights
     tail = 2.0 ** -25 * sp["tail"]
     tiny = 2.0 ** -25 if case.qt == HF else 0.0
     tol = rel[..., None] * sp["soft"] + tail[..., None] + (half + 2.0 ** -22) * np.abs(ref) + tiny
-    e = np.abs(out.double().cpu().numpy() - ref)
-    assert np.isfinite(out.double().cpu().numpy()).all()
-    assert (e <= tol).all(), (float((e / np.maximum(tol, 1e-300)).max()), np.argwhere(e > tol)[:4].tolist())
-    g = lse.double().cpu().numpy()
-    assert np.array_equal(np.isinf(g), np.isinf(rlse))
-    fin = np.isfinite(rlse)
-    assert (np.abs(g[fin] - rlse[fin]) <= (ds + 2.0 ** -20 + sums + np.abs(np.where(fin, rlse, 0)) * 2.0 ** -22)[fin]).all()
+    results = [(out, lse)]
+    if weights:                       # without weights, short lists go another way
+        results.append(A.dsv4_gqa_decode(d(q), lens_t.cuda(), cache, sink=d(sink), window=window, max_len=max_len,
+                                         req_pool_indices=None if req is None else torch.tensor(req, dtype=torch.int32).cuda(),
+                                         **kw))
+        torch.cuda.synchronize()
+        assert A.dsv4_attn_get_device_error() == want_flags
+    for o, l in results:
+        e = np.abs(o.double().cpu().numpy() - ref)
+        assert np.isfinite(o.double().cpu().numpy()).all()
+        assert (e <= tol).all(), (float((e / np.maximum(tol, 1e-300)).max()), np.argwhere(e > tol)[:4].tolist())
+        g = l.double().cpu().numpy()
+        assert np.array_equal(np.isinf(g), np.isinf(rlse))
+        fin = np.isfinite(rlse)
+        assert (np.abs(g[fin] - rlse[fin]) <=
+                (ds + 2.0 ** -20 + sums + np.abs(np.where(fin, rlse, 0)) * 2.0 ** -22)[fin]).all()
     if weights:
         gw = wo_d.double().cpu().numpy()
         tolw = sp["wslack"] * (2 * (case.dim + 8) * 2.0 ** -23 + 2.0 ** -19 + float(sums.max())) + np.abs(rw) * 2.0 ** -22
@@ -292,6 +301,10 @@ def test_decode_in_a_graph_and_on_streams(A):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         out, lse = A.dsv4_gqa_decode(q, lens, cache, weights=w, weights_out=wo)
+    A.dsv4_gqa_decode(q, lens, cache)
+    short = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(short):
+        res = A.dsv4_gqa_decode(q, lens, cache)
     for now in ([2000, 3, 700, 0], [1, 1999, 0, 64], [0, 0, 0, 0]):
         lens.copy_(torch.tensor(now, dtype=torch.int32))
         q.copy_(c.query(4, 8))
@@ -301,6 +314,10 @@ def test_decode_in_a_graph_and_on_streams(A):
         x = torch.full_like(w, -1.0)
         o2, l2 = A.dsv4_gqa_decode(q, lens, cache, weights=w, weights_out=x)
         assert torch.equal(out, o2) and torch.equal(lse, l2) and torch.equal(wo, x)
+        plain = A.dsv4_gqa_decode(q, lens, cache)
+        short.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(res[0], plain[0]) and torch.equal(res[1], plain[1])
     # two calls at once, each with its own workspace
     lens.copy_(torch.tensor([2000, 3, 700, 0], dtype=torch.int32))
     want = A.dsv4_gqa_decode(q, lens, cache)
