@@ -324,18 +324,19 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
 // CTAs per segment where every segment is done by a cluster of its own, or 0
 // where the list is shared out: as many as keep the grid within two CTAs per
 // slot (the hardware hands out what does not run at once), if that leaves their
-// warps few tiles of the longest segment.  With weights the list's numbering is
-// needed.  (us, cluster and list: 1 request x 8 KV heads, 333 rows 5.0 and 6.7,
+// warps few tiles of the longest segment.  (us, cluster and list: 1 request x 8 KV heads, 333 rows 5.0 and 6.7,
 // 4000 rows 8.9 and 11.2, 10000 rows 15.8 and 15.2; 8 x 1000..2000 rows 11.7 and
 // 15.5; 48 x 16 heads of 64, up to 1024 rows 31.3 and 35.0; 16 x 2048..8192 rows
 // 55 and 59; 64 x 4 heads, 1024..16384 e4m3 rows, 64 tiles per warp, 118 and 98;
-// 1 KV head x 5000 rows on 8 CTAs 9.9 and 8.0.)
+// 1 KV head x 5000 rows on 8 CTAs 9.9 and 8.0.  With weights, whose phase at the
+// end hides less behind another CTA, what runs at once: 8 x 500..1000 rows 9.3,
+// with twice the CTAs 16.2, list 14.6.)
 int segment_cluster(const DecodeParams& p, const Plan& pl) {
     const long long segments = (long long)p.batch * p.c.kv_heads * p.chunks;
     const int span = p.window > 0 ? std::min<long long>(p.max_len, (long long)p.window + pl.tt) : p.max_len;
     const int tiles = (span + pl.tt - 1) / pl.tt;
     int c = 8;
-    while (c > 1 && segments * c > 2 * kMaxCtas) c /= 2;
+    while (c > 1 && segments * c > (p.w_out ? 1 : 2) * kMaxCtas) c /= 2;
     const int most = segments * c >= kMaxCtas / 2 ? 32 : 8;  // tiles per warp
     return tiles <= c * kWarps * most && segments * c <= 0x7fffffffLL ? c : 0;
 }
@@ -433,7 +434,8 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     p.warps = pl.ctas * kWarps;
     p.claims = pl.claims;
     p.pieces = static_cast<int>(std::min<long long>(p.warps + p.claims * kWarps, pl.tiles / pl.min_tiles));
-    p.cluster = weights ? 0 : segment_cluster(p, pl);
+    // (with weights, requests may add to one row only through the list's kernels, and so may several chunks of heads)
+    p.cluster = weights && (req_pool_indices || pl.chunks > 1) ? 0 : segment_cluster(p, pl);
     p.err = err;
 
     const int d = cache->head_dim;

@@ -25,8 +25,9 @@
 //
 // Short lists (SEG) are done in one launch: a cluster of 1 to 8 CTAs takes a
 // segment, its warps equal parts of the tiles, and they merge through
-// distributed shared memory.  That spares the second launch (2.4 us of host
-// time of 9.4), and the pieces' way through L2.
+// distributed shared memory; with weights, every warp then adds those of its
+// own tiles.  That spares the other launches (2.4 us of host time each) and the
+// pieces' way through L2.
 //
 // A warp streams its tiles through its own ring of cp.async stages, which runs
 // ahead over segment and share boundaries, and the queries of the next segment
@@ -384,6 +385,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     __shared__ __align__(16) uint8_t s_answer[16];
     __shared__ __align__(8) uint64_t s_bar;
     __shared__ float2 s_ml[SEG ? W : 1][SEG ? HEADS : 1];     // references and sums of the warps
+    __shared__ __align__(16) float s_lse[SEG ? HEADS : 4];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -418,10 +420,10 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         cons.rq = read_request(p.lens, p.req, p.c.table_rows, p.max_len, cons.b, err);
         if (err && cons.hc == 0 && rank == 0 && tid == 0) atomicOr(p.err, err);
         cons.rg = key_range<TT>(p, cons.rq.n);
-        cons.seg = 0;
+        cons.seg = seg * ((p.max_len + TT - 1) / TT);          // (numbers the tiles' scores)
         const int i = warp * p.cluster + rank, n = W * p.cluster;        // this warp's part
-        cons.at = cons.rg.tiles * i / n;
-        c1 = cons.end = cons.rg.tiles * (i + 1) / n;
+        cons.at = cons.seg + cons.rg.tiles * i / n;
+        c1 = cons.end = cons.seg + cons.rg.tiles * (i + 1) / n;
     } else {
         early = request_of(lane);
         unsigned total = key_range<TT>(p, early.n).tiles;
@@ -946,6 +948,57 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at * D + d) =
                     p.q_bf16 ? pack2<true>(x * inv, y * inv) : pack2<false>(x * inv, y * inv);
                 if (d == 0 && p.lse) p.lse[at] = any ? (top + log2f(l)) * kLn2 : -INFINITY;
+            }
+            if (p.w_out) {
+                // lse of every head, by a warp each; then the weights of this warp's own tiles, whose scores it wrote
+                for (int c = warp; c < HEADS; c += W) {
+                    const bool in = lane < W * p.cluster && c < nheads;
+                    const float2 ml = in ? ld_cluster_f2(mapa(ml0 + (lane % W * HEADS + c) * 8, lane / W))
+                                         : make_float2(kNoMax, 0.f);
+                    float mx = ml.x;
+#pragma unroll
+                    for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+                    const float sk = p.sink && c < nheads ? __ldg(p.sink + head0 + c) * kLog2e : -INFINITY;
+                    const float top = fminf(fmaxf(mx, sk), 3e38f);
+                    float l = ml.y * fast_exp2(ml.x - top);
+#pragma unroll
+                    for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+                    l += fast_exp2(sk - top);
+                    // +inf makes a head contribute nothing: padding, and heads none of whose rows could be read
+                    if (lane == 0) s_lse[c] = c < nheads && (l > 0.f || l != l) ? top + log2f(l) : INFINITY;
+                }
+                __syncthreads();
+                const size_t to = ((size_t)cons.rq.row * p.c.kv_heads + h) * p.width;
+                const int t0 = cons.rg.lo / TT - static_cast<int>(cons.seg);
+                const int s0 = (t0 + static_cast<int>(cons.at)) * TT, s1 = (t0 + static_cast<int>(cons.end)) * TT;
+                const int first_s = max(s0, cons.rg.lo), end_s = min(s1, cons.rg.n);
+                constexpr int kAtOnce = HEADS > 8 ? 2 : 4;        // slots per lane whose loads go out together
+                for (int s = first_s + lane; s < end_s; s += 32 * kAtOnce) {
+                    float prior[kAtOnce];
+                    float4 x[kAtOnce][HEADS / 4];
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) {
+                        const int at = min(s + 32 * i, end_s - 1);
+                        prior[i] = p.w_in[to + at];
+                        const float4* from =
+                            reinterpret_cast<const float4*>(p.logits + ((size_t)cons.at * TT + (at - s0)) * HEADS);
+#pragma unroll
+                        for (int k = 0; k < HEADS / 4; ++k) x[i][k] = __ldcg(from + k);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) {
+                        float add = 0.f;
+#pragma unroll
+                        for (int k = 0; k < HEADS / 4; ++k) {
+                            const float4 l = *reinterpret_cast<const float4*>(s_lse + 4 * k);
+                            add += (fast_exp2(x[i][k].x - l.x) + fast_exp2(x[i][k].y - l.y)) +
+                                   (fast_exp2(x[i][k].z - l.z) + fast_exp2(x[i][k].w - l.w));
+                        }
+                        if (s + 32 * i < end_s) p.w_out[to + s + 32 * i] = p.decay * prior[i] + add;
+                    }
+                }
+                for (int s = rank * W * 32 + tid; s < cons.rg.lo; s += p.cluster * W * 32)
+                    p.w_out[to + s] = p.decay * p.w_in[to + s];
             }
             cluster_sync();                       // (no CTA may end while another reads its shared memory)
             return;

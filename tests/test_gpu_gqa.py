@@ -133,13 +133,16 @@ def check_decode(A, case, lens, heads, *, window=0, sink=None, req=None, weights
     tail = 2.0 ** -25 * sp["tail"]
     tiny = 2.0 ** -25 if case.qt == HF else 0.0
     tol = rel[..., None] * sp["soft"] + tail[..., None] + (half + 2.0 ** -22) * np.abs(ref) + tiny
-    results = [(out, lse)]
-    if weights:                       # without weights, short lists go another way
-        results.append(A.dsv4_gqa_decode(d(q), lens_t.cuda(), cache, sink=d(sink), window=window, max_len=max_len,
-                                         req_pool_indices=None if req is None else torch.tensor(req, dtype=torch.int32).cuda(),
-                                         **kw))
-        torch.cuda.synchronize()
-        assert A.dsv4_attn_get_device_error() == want_flags
+    results, tracked = [(out, lse)], [wo_d]
+    if weights:      # short lists go other ways without weights, and where request rows may repeat
+        for named, kept in ((req, False), (list(range(batch)) if req is None else req, True)):
+            extra = {"weights": w_d, "weights_out": d(wo), "decay": decay} if kept else {}
+            results.append(A.dsv4_gqa_decode(
+                d(q), lens_t.cuda(), cache, sink=d(sink), window=window, max_len=max_len,
+                req_pool_indices=None if named is None else torch.tensor(named, dtype=torch.int32).cuda(), **extra, **kw))
+            torch.cuda.synchronize()
+            assert A.dsv4_attn_get_device_error() == want_flags
+            tracked.append(extra.get("weights_out"))
     for o, l in results:
         e = np.abs(o.double().cpu().numpy() - ref)
         assert np.isfinite(o.double().cpu().numpy()).all()
@@ -149,8 +152,8 @@ def check_decode(A, case, lens, heads, *, window=0, sink=None, req=None, weights
         fin = np.isfinite(rlse)
         assert (np.abs(g[fin] - rlse[fin]) <=
                 (ds + 2.0 ** -20 + sums + np.abs(np.where(fin, rlse, 0)) * 2.0 ** -22)[fin]).all()
-    if weights:
-        gw = wo_d.double().cpu().numpy()
+    for got in (x for x in tracked if x is not None):
+        gw = got.double().cpu().numpy()
         tolw = sp["wslack"] * (2 * (case.dim + 8) * 2.0 ** -23 + 2.0 ** -19 + float(sums.max())) + np.abs(rw) * 2.0 ** -22
         assert (np.abs(gw - rw) <= tolw).all(), float((np.abs(gw - rw) / np.maximum(tolw, 1e-300)).max())
     return out, lse, wo_d
