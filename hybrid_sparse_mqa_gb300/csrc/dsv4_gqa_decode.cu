@@ -288,6 +288,7 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 struct Plan {
     int group, nt, chunks, tt, min_tiles;
     long long tiles;                       // bound on the tile list
+    int places;                            // CTAs that run at once
     int ctas, claims;                      // resident CTAs of the attention kernel, and claimable ones
     size_t part_o, part_ml, lse2, info, logits, bytes;      // offsets, size
 };
@@ -307,6 +308,7 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
     if (pl.tiles >= 1LL << 31 || segments >= 1LL << 31) return DSV4_ERR_UNSUPPORTED;
     // (512-byte rows: one CTA's ring fills an SM's shared memory)
     const int most = c->head_dim * (c->format == DSV4_GQA_E4M3 ? 1 : 2) > 256 ? kMaxCtas / 2 : kMaxCtas;
+    pl.places = most;
     pl.min_tiles = (max_len + pl.tt - 1) / pl.tt <= kFewTiles ? 1 : 2;
     const long long want = pl.tiles / pl.min_tiles;
     pl.ctas = want < 1 ? 1 : (want < most ? static_cast<int>(want) : most);
@@ -322,23 +324,28 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
 }
 
 // CTAs per segment where every segment is done by a cluster of its own, or 0
-// where the list is shared out: as many as keep the grid within two CTAs per
-// slot (the hardware hands out what does not run at once), if that leaves their
-// warps few tiles of the longest segment.  (us, cluster and list: 1 request x 8 KV heads, 333 rows 5.0 and 6.7,
-// 4000 rows 8.9 and 11.2, 10000 rows 15.8 and 15.2; 8 x 1000..2000 rows 11.7 and
-// 15.5; 48 x 16 heads of 64, up to 1024 rows 31.3 and 35.0; 16 x 2048..8192 rows
-// 55 and 59; 64 x 4 heads, 1024..16384 e4m3 rows, 64 tiles per warp, 118 and 98;
-// 1 KV head x 5000 rows on 8 CTAs 9.9 and 8.0.  With weights, whose phase at the
-// end hides less behind another CTA, what runs at once: 8 x 500..1000 rows 9.3,
-// with twice the CTAs 16.2, list 14.6.)
+// where the list is shared out.  Clusters are as large as run at once, and
+// taken where they leave their warps few tiles of the longest segment: 8 where
+// they do not fill the GPU or a second wave would be mostly empty, 16 where
+// they run at once (a ragged batch then ends with its longest request), 32
+// where the hardware hands them out in several waves.  In us, cluster and list:
+//   1 request x 8 KV heads: 333 rows 5.0 and 6.7, 4000 rows 8.9 and 11.2, 10000
+//   rows (not taken) 15.8 and 15.2; 1 KV head x 5000 rows (not taken) 9.9 and 8.0
+//   8 x 1000..2000 rows 11.8 and 15.7; 64 x 4 KV heads of 100..4000 e4m3 rows,
+//   31 tiles per warp (not taken), 37.3 and 33.2
+//   40 x 1000 rows, 320 CTAs for 304 places (not taken), 36.5 and 32.1
+//   64 x 1..2048 rows 48.8 and 51.9; 64 x 2000..2048 rows 79.2 and 88.8; 128 x
+//   1..2048 rows 85.5 and 96.6; 48 x 16 heads of 64, up to 1024 rows 31.5 and 34.2
+//   with weights, 1 x 333 rows 6.2 and 8.8, 8 x 500..1000 rows 9.3 and 14.6
 int segment_cluster(const DecodeParams& p, const Plan& pl) {
     const long long segments = (long long)p.batch * p.c.kv_heads * p.chunks;
     const int span = p.window > 0 ? std::min<long long>(p.max_len, (long long)p.window + pl.tt) : p.max_len;
     const int tiles = (span + pl.tt - 1) / pl.tt;
     int c = 8;
-    while (c > 1 && segments * c > (p.w_out ? 1 : 2) * kMaxCtas) c /= 2;
-    const int most = segments * c >= kMaxCtas / 2 ? 32 : 8;  // tiles per warp
-    return tiles <= c * kWarps * most && segments * c <= 0x7fffffffLL ? c : 0;
+    while (c > 1 && segments * c > pl.places) c /= 2;
+    const long long ctas = segments * c;
+    const int most = ctas < pl.places / 2 ? 8 : ctas <= pl.places ? 16 : ctas < pl.places * 14 / 10 ? 8 : 32;
+    return tiles <= c * kWarps * most && ctas <= 0x7fffffffLL ? c : 0;
 }
 
 template <int D, int TT, int HEADS>
