@@ -18,8 +18,8 @@
 // for 64 of 20000 to 32768 with clusters of four.  The move kernel copies the
 // listed rows: only rows that change their slot are read and written, each
 // once.  It is bound by HBM: 38 us for 188 MB of 256-byte rows from anywhere
-// in 32768 slots (4.9 TB/s).  One kernel for both took as long for few rows and
-// longer for many.
+// in 32768 slots (4.9 TB/s).  One kernel for both took longer (61 us and not 58
+// for those), except where each head moves a few rows at most.
 #include "dsv4_gqa.cuh"
 
 namespace dsv4 {
@@ -53,6 +53,8 @@ struct EvictParams {
     int* movers;                           // [batch][KV heads][most] their slots
     int most;
     int row_pieces;                        // 16-byte pieces of a row
+    int alone;                             // no request can be more than kFew rows over the bound: the select kernel
+                                           // moves them itself and writes the new lengths
     unsigned int* err;
 };
 
@@ -85,6 +87,7 @@ struct SelectShared {
     uint4 bins[2][kBins / 4];              // this CTA's sums, for the cluster (by digit parity)
     uint32_t warp_sum[2][WARPS];
     uint32_t count[2][2];                  // this CTA's ties; holes and movers, for the cluster
+    int few[2][4], few_count;              // slots freed and refilled, where they are few
     uint32_t pick[3];                      // chosen bin, rows wanted in it, rows in it
     int skip;
 };
@@ -152,6 +155,7 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
     int* p_out = p.p_out ? p.p_out + at : nullptr;
     const bool copy_w = w_in != w_out, copy_p = p_in != p_out;
     const bool skip = err & DSV4_DEV_ERR_REQ_ROW;
+    if (p.alone && h == 0 && rank == 0 && tid == 0) p.lens_out[b] = min(rq.n, p.keep);
     if (rq.n <= p.keep || skip) {            // (uniform over the cluster)
         if (rank == 0 && tid == 0) p.counts[id] = 0;
         if ((copy_w || copy_p) && !skip)
@@ -226,7 +230,8 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
     if constexpr (CLUSTER == 1 && KEYS > 0) {
         // A cache just over its bound, as after every step of a decode loop: the few rows to go are looked for one by
         // one, smallest key first, of equal ones the highest slot.  (One of 2049 rows for each of 512 heads, with the
-        // move: 17 us by the radix select, 8 us so; four of 2052: 15.8 and 12.7.)
+        // move: 17 us by the radix select, 8.2 so, 6.5 where no other kernel has to move rows; four of 2052: 15.8,
+        // 12.7 and 11.4.)
         if (n - p.keep <= kFew) {
             int gone[kFew];
             for (int e = 0; e < n - p.keep; ++e) {
@@ -260,23 +265,52 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
             }
             if (tid == 0) {
                 // freed slots below `keep` in ascending order, and the rows behind it that stay
-                int count = 0;
-                for (int last = -1;; ++count) {
+                int count = 0, last = -1;
+                for (;;) {
                     int next = p.keep;
 #pragma unroll
                     for (int q = 0; q < kFew; ++q)
                         if (q < n - p.keep && gone[q] > last) next = min(next, gone[q]);
                     if (next >= p.keep) break;
-                    holes[count] = last = next;
+                    sh.few[0][count++] = last = next;
                 }
-                p.counts[id] = count;
+                sh.few_count = count;
                 int to = 0;
                 for (int s = p.keep; s < n; ++s) {
                     bool stays = true;
 #pragma unroll
                     for (int q = 0; q < kFew; ++q) stays &= !(q < n - p.keep && gone[q] == s);
-                    if (stays) movers[to++] = s;
+                    if (stays) sh.few[1][to++] = s;
                 }
+            }
+            __syncthreads();
+            const int count = sh.few_count;
+            if (!p.alone) {
+                if (tid == 0) p.counts[id] = count;
+                if (tid < count) {
+                    holes[tid] = sh.few[0][tid];
+                    movers[tid] = sh.few[1][tid];
+                }
+                return;
+            }
+            // a 16-byte piece of a K or V row per thread
+            const int* table = p.c.table + (long long)rq.row * p.c.table_stride;
+            const int in_page = (1 << p.c.page_shift) - 1, pieces = 2 * p.row_pieces;
+            for (int e = tid; e < count * pieces; e += THREADS) {
+                const int j = e / pieces, piece = e % pieces, dst = sh.few[0][j], src = sh.few[1][j];
+                const int tp = __ldg(table + (dst >> p.c.page_shift)), fp = __ldg(table + (src >> p.c.page_shift));
+                if (piece == 0) {
+                    w_out[dst] = w_in[src];
+                    if (p_out) p_out[dst] = p_in[src];
+                }
+                if (tp < 0 || tp >= p.c.num_pages || fp < 0 || fp >= p.c.num_pages) {
+                    if (piece == 0) atomicOr(p.err, DSV4_DEV_ERR_GQA_PAGE);
+                    continue;
+                }
+                uint8_t* pool = (piece < p.row_pieces ? p.c.k : p.c.v) + h * p.c.head_stride +
+                                (piece < p.row_pieces ? piece : piece - p.row_pieces) * 16;
+                *reinterpret_cast<uint4*>(pool + tp * p.c.page_stride + (dst & in_page) * p.c.row_stride) =
+                    *reinterpret_cast<const uint4*>(pool + fp * p.c.page_stride + (src & in_page) * p.c.row_stride);
             }
             return;
         }
@@ -583,7 +617,7 @@ int launch_select_cluster(const EvictParams& p, int per, void* stream) {
 int launch_select(const EvictParams& p, void* stream) {
     const int ids = p.batch * p.c.kv_heads;
     int cluster = 1;
-    while (cluster < kMaxCluster &&
+    while (!p.alone && cluster < kMaxCluster &&
            (p.max_len > cluster * kHeldKeys || (ids * cluster < 152 && p.max_len > 4096 * cluster)))
         cluster *= 2;
     const int per = (p.max_len + cluster - 1) / cluster;
@@ -646,8 +680,10 @@ int dsv4_gqa_evict(int32_t batch, const int32_t* lens, const int32_t* seq_lens, 
     p.row_pieces = cache->head_dim * (cache->format == DSV4_GQA_E4M3 ? 1 : 2) / 16;
     p.err = err;
 
+    // (new lengths that replace the old ones have to wait for every head's CTA to have read those: the move kernel does)
+    p.alone = max_len - keep <= kFew && max_len <= kHeldKeys && (lens_out + batch <= lens || lens + batch <= lens_out);
     const int r = launch_select(p, stream);
-    if (r) return r;
+    if (r || p.alone) return r;
     switch (p.row_pieces) {
         case 4: return launch_move<8>(p, stream);
         case 8: return launch_move<16>(p, stream);

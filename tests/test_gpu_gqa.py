@@ -656,6 +656,32 @@ def test_evict_equal_and_special_weights(A):
         check_evict(A, c, [300, 298, 120, 150], 296, w=w, recent=296, inplace=True)
 
 
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("kv,dim,token_major", [(BF, 64, False), (HF, 256, True), (F8, 64, True), (F8, 128, False)])
+def test_evict_a_step_of_a_full_cache(A, kv, dim, token_major, inplace):
+    # no request can be more than four rows over the bound
+    c = Case(kv=kv, hkv=3, dim=dim, rows=9, slots=140, seed=dim, token_major=token_major)
+    lens = [132, 131, 130, 129, 128, 100, 1, 0, 132]
+    seen = [n + 50 for n in lens]
+    pos = _positions(c, seen, lens)
+    check_evict(A, c, lens, 128, max_len=132, inplace=inplace)
+    check_evict(A, c, lens, 128, max_len=132, first=3, recent=20, seen=seen, positions=pos, inplace=inplace)
+    check_evict(A, c, lens, 128, max_len=132, recent=128, inplace=inplace)
+    check_evict(A, c, [132, 3, 140, 0, 129], 128, req=[8, 40, 0, 77, 0], max_len=132, inplace=inplace,
+                want_flags=O.ERR_REQ_ROW | O.ERR_GQA_LENGTH)
+    w = torch.zeros(9, 3, 147)
+    w[:, :, ::3] = math.nan
+    check_evict(A, c, lens, 128, max_len=132, w=w, inplace=inplace)
+    c.table[0, 8], c.table[1, 0] = -1, 10 ** 6
+    check_evict(A, c, lens, 128, max_len=132, w=w, inplace=inplace, want_flags=O.ERR_GQA_PAGE)
+
+
+def test_evict_a_step_of_long_caches(A):
+    for slots in (5000, 12000, 30000, 40000):
+        c = Case(hkv=2, rows=2, slots=slots, page=1024, seed=slots)
+        check_evict(A, c, [slots, slots - 2], slots - 3, first=4, recent=100, max_len=slots)
+
+
 def test_evict_rows_named_in_any_order_twice_or_not_at_all(A):
     c = Case(hkv=2, rows=5, slots=96, seed=32)
     check_evict(A, c, [90, 0, 70], 40, req=[3, 77, 0])
