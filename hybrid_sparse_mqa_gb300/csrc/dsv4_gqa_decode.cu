@@ -355,7 +355,8 @@ int launch_join_heads(const DecodeParams& p, void* stream) {
     // choice made and with the other: 1 segment x 131072 rows, 1216 pieces of 8 heads: slices 26.6, no slices 35.9;
     // 16 segments, 85 pieces: PW = 16 165, slices 171, PW = 1 180; 8 segments, 10 pieces: PW = 8 7.7, PW = 1 8.1;
     // 256 segments, 5 pieces: PW = 1 98, PW = 8 105)
-    const unsigned pieces = p.pieces / segments + 1, heads = segments * HEADS;
+    const unsigned pieces = p.pieces / segments + 1;
+    const unsigned long long heads = (unsigned long long)segments * HEADS;
     if (pieces > 96 && heads <= 64)
         return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 16, D / 32>, dim3(segments, HEADS, D / 32), 512, 0, stream, 1, p);
     if (pieces > 96)

@@ -31,13 +31,18 @@
 //
 // A warp streams its tiles through its own ring of cp.async stages, which runs
 // ahead over segment and share boundaries, and the queries of the next segment
-// with them.  Scores are computed transposed, S^T = K Q^T,
-// so the 16 rows of an m16n8k16 MMA are slots and its 8 columns query heads: a
-// group of 8 heads wastes nothing.  The exponentials become the B operand of
+// with them.  Scores are computed transposed, S^T = K Q^T, so the 16 rows of an
+// m16n8k16 MMA are slots and its 8 columns query heads: a group of 8 heads
+// wastes nothing.  The exponentials become the B operand of
 // O^T = V^T P^T by one 8x8 transposition in registers (movmatrix).  The
 // softmax is online with a lazy reference: a tile's scores are compared with
 // the running reference by one vote, and the reference moves (and O and the
 // sums are rescaled) only when some score exceeds it by more than 2^8.
+//
+// Bound by HBM for lists of 100 tiles per warp and more: 334 us for 2.34 GB (32 x
+// 2048..32768 rows, 8 KV heads of 128, bf16: 7.0 TB/s), 165 us for 1.07 GB (2 x
+// 131072).  Shorter lists lose to the uneven end (98 us for 566 MB, 64 x
+// 1024..16384 e4m3 rows), the start (3 us: length, page, rows) and the join (4 us).
 //
 // Precision: scores, references, sums, O and the merge are fp32.  For 16-bit
 // caches P enters the MMA as the sum of two 16-bit values (the rounded value
@@ -58,7 +63,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -1e30f;           // reference of a head that has seen no score
 constexpr int kWarps = 4;                  // warps per CTA
-constexpr int kMaxCtas = 304;              // resident at once: two per SM
+constexpr int kMaxCtas = 304;              // resident at once: two on each of 152 SMs
 // What is kept back of a warp's part of a long list, in 32nds.  Taking another
 // share costs a piece to write and join and some stalled loads: 32 x
 // 2048..32768 rows (230 tiles per warp) go from 345 to 328 us, 2 x 131072 rows
