@@ -222,12 +222,17 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// 16-byte global -> shared copy through L2 lines that are the first to go (a
-// cache row is read once per call; what is written for the kernels behind
-// stays); src_bytes = 0 writes zeros and reads nothing.
-__device__ __forceinline__ uint64_t evict_first_policy() {
+// How the copies below use L2: lines that are the first to go where a cache row
+// is read once per call (what is written for the kernels behind stays: with
+// weights 37 MB of scores), ordinary ones where every 16 query heads read it
+// again (64 heads per KV head: 635 us and not 665).  16-byte global -> shared
+// copy; src_bytes = 0 writes zeros and reads nothing.
+__device__ __forceinline__ uint64_t read_policy(bool once) {
     uint64_t p;
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    if (once)
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    else
+        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
 __device__ __forceinline__ void cp_async_16_hint(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     const int lane_row = lane / S::PPR, lane_piece = lane % S::PPR;
     const long long lane_off = lane_row * p.c.row_stride + lane_piece * 16;
     const int page_mask = (1 << p.c.page_shift) - 1;
-    const uint64_t policy = evict_first_policy();
+    const uint64_t policy = read_policy(p.chunks == 1);
     // the K scale of cons's KV head, loaded as soon as cons comes to it: ahead of the copies
     auto load_kscale = [&]() { return S::FP8 && p.c.k_scale ? __ldg(p.c.k_scale + cons.hc / p.chunks) : 1.f; };
     float kscale = load_kscale();
