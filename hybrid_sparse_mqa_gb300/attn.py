@@ -384,7 +384,7 @@ def make_gqa_cache(k_pages, v_pages, page_table, *, k_scale=None, v_scale=None):
     lib()                       # (a descriptor is only good for the library's calls)
     c._index = k_pages.get_device()
     c._rows = torch.Size((heads, dim))
-    c._slots = page_table.shape[1] * page_size
+    c._slots = min(page_table.shape[1] * page_size, 1 << 30)     # (a call's bound on lengths)
     c._scale = 1.0 / math.sqrt(dim)
     return c
 

@@ -87,9 +87,13 @@ inline int check_cache(const dsv4_gqa_cache* c) {
     return DSV4_OK;
 }
 
-// 0 < max_len <= the slots that a request's table row addresses.
+// Bound on lengths and on the tokens of a store: slots and tokens are ints, and
+// a tile or a run of them may end up to 2^25 behind the last.
+constexpr int kMostSlots = 1 << 30;
+
+// 0 < max_len <= the slots that a request's table row addresses, and the bound.
 inline bool max_len_fits(const dsv4_gqa_cache* c, int max_len) {
-    return max_len >= 1 && max_len <= static_cast<long long>(c->page_table_width) * c->page_size;
+    return max_len >= 1 && max_len <= kMostSlots && max_len <= static_cast<long long>(c->page_table_width) * c->page_size;
 }
 
 // Launch on `stream` with programmatic stream serialisation (every kernel

@@ -305,7 +305,7 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
     pl.tt = tile_slots(c->format, c->head_dim);
     const long long segments = (long long)batch * c->num_kv_heads * pl.chunks;
     pl.tiles = segments * ((max_len + pl.tt - 1) / pl.tt);
-    if (pl.tiles >= 1LL << 31 || segments >= 1LL << 31) return DSV4_ERR_UNSUPPORTED;
+    if (pl.tiles >= 1LL << 31 || segments > kMostSlots) return DSV4_ERR_UNSUPPORTED;
     // (512-byte rows: one CTA's ring fills an SM's shared memory)
     const int most = c->head_dim * (c->format == DSV4_GQA_E4M3 ? 1 : 2) > 256 ? kMaxCtas / 2 : kMaxCtas;
     pl.places = most;

@@ -226,7 +226,7 @@ extern "C" int dsv4_gqa_store(const void* k, int64_t k_token_stride, int64_t k_h
     using namespace dsv4::gqa;
     const int rc = check_cache(cache);
     if (rc) return rc;
-    if (n < 0) return DSV4_ERR_INVALID;
+    if (n < 0 || n > kMostSlots) return DSV4_ERR_INVALID;
     if (type != DSV4_GQA_BF16 && type != DSV4_GQA_F16) return DSV4_ERR_UNSUPPORTED;
     if (cache->format != DSV4_GQA_E4M3 && cache->format != type) return DSV4_ERR_UNSUPPORTED;
     if (n == 0) return DSV4_OK;

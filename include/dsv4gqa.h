@@ -79,8 +79,8 @@
  *   request b is row b.
  *   weights (fp32) and positions (int32): [page_table_rows, num_kv_heads,
  *   width], width >= max_len.
- *   max_len: bound on lens; at most page_table_width * page_size.  It sizes
- *   launches and workspaces.
+ *   max_len: bound on lens; at most page_table_width * page_size and 2^30.  It
+ *   sizes launches and workspaces.
  *   workspace: device scratch of at least the size that the matching
  *   _workspace_size function gives, 16-byte aligned; need not be initialised
  *   and holds nothing between calls.  Calls that may run at the same time
@@ -126,7 +126,7 @@ typedef struct dsv4_gqa_cache {
     const float*   v_scale;
 } dsv4_gqa_cache;
 
-/* k, v: n tokens of num_kv_heads rows, type BF16 or F16 (the cache's own type
+/* k, v: n tokens (at most 2^30) of num_kv_heads rows, type BF16 or F16 (the cache's own type
    unless that is E4M3); strides in elements, multiples of 8; 16-byte aligned.
    weights / positions may be NULL; token_positions int32 [n] goes with
    positions; width as above. */

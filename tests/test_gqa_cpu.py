@@ -272,3 +272,16 @@ def test_oracle_evict_ties_go_to_the_lower_slot():
     w = np.zeros((3, 2, 48))
     _, k, _, _, _, _ = O.gqa_evict([30, 0, 0], c, w, 12, max_len=48)
     assert np.array_equal(k, c["k"])            # slots 0 .. 11 are kept, nothing moves
+
+
+def test_counts_whose_arithmetic_would_wrap_are_refused(A):
+    # slots and tokens are ints, and tiles and runs of them end behind the last
+    wide = ctypes.addressof(_cache(A, page_size=1024, page_table_width=1 << 21, page_table_stride=1 << 21))
+    most = 1 << 30
+    assert A.lib().dsv4_gqa_decode_workspace_size(wide, 1, 4, most, 0) > 0
+    for max_len in (most + 1, 2**31 - 1):
+        assert _decode(A, wide, batch=1, heads=4, max_len=max_len) == -1
+        assert _evict(A, wide, batch=1, max_len=max_len, width=2**31) == -1
+        assert A.lib().dsv4_gqa_decode_workspace_size(wide, 1, 4, max_len, 0) == 0
+        assert A.lib().dsv4_gqa_evict_workspace_size(wide, 1, max_len, 10) == 0
+        assert _store(A, wide, n=max_len) == -1
