@@ -61,7 +61,7 @@ namespace gqa {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -1e30f;           // reference of a head that has seen no score
+constexpr float kNoMax = -3e38f;           // reference of a head that has seen no score: below every finite one
 constexpr int kWarps = 4;                  // warps per CTA
 constexpr int kMaxCtas = 304;              // resident at once: two on each of 152 SMs
 // What is kept back of a warp's part of a long list, in 32nds.  Taking another

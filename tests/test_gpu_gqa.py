@@ -221,6 +221,24 @@ def test_decode_one_row_takes_all(A):
     check_decode(A, c, [500, 499, 1], 8, spread=30.0, weights=True)
 
 
+@pytest.mark.parametrize("slots,lens", [(100, [100, 17]), (9000, [9000, 4001])])
+def test_decode_of_scores_far_below_zero(A, slots, lens):
+    # Every score is -2^109 (7 rows of 8) or -2^110: products and sums of powers of two are exact, so the equal ones
+    # share the weight and the output is their values' mean: fp32 sums of 16-bit values, and half a step of bf16.
+    c = Case(hkv=1, dim=64, rows=2, slots=slots, seed=7)
+    c.k.fill_(-2.0 ** 53)
+    c.k[:, :, ::8] *= 2
+    q = torch.full((2, 8, 64), 2.0 ** 53, dtype=BF)
+    out, lse = A.dsv4_gqa_decode(q.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), c.handle(A), scale=2.0 ** -3)
+    assert A.dsv4_attn_get_device_error() == 0
+    for b, n in enumerate(lens):
+        s = np.array([x for x in range(n) if x % 8])
+        v = c.v[c.table[b].long()[s // c.page], 0, s % c.page].double()
+        tol = v.abs().mean(0) * ((n / 16 + 64) * 2.0 ** -23 + 2.0 ** -16) + v.mean(0).abs() * (2.0 ** -8 + 2.0 ** -22)
+        assert ((out[b].double().cpu() - v.mean(0)).abs() <= tol).all()
+        assert (lse[b].double().cpu() / -2.0 ** 109 - 1).abs().max() <= 4 * 2.0 ** -23
+
+
 def test_decode_small_queries_of_an_e4m3_cache(A):
     # queries whose f16 value would be zero or infinite
     for spread in (1e-12, 1e25):
