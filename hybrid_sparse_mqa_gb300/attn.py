@@ -564,7 +564,8 @@ def dsv4_gqa_evict(lens, cache, weights, keep, *, seq_lens=None, positions=None,
     the `recent` newest of seq_lens tokens, then the largest weights.  Rows
     that stay but stand behind the bound move into the freed slots, with their
     weights and positions (in place unless weights_out / positions_out are
-    given).  Returns lens_out (a new tensor unless given; may be lens)."""
+    given).  Returns lens_out (a new tensor unless given; may be lens
+    or seq_lens)."""
     index = cache._index
     batch = lens.numel()
     _need(lens, "lens", torch.int32, batch, index)

@@ -680,8 +680,10 @@ int dsv4_gqa_evict(int32_t batch, const int32_t* lens, const int32_t* seq_lens, 
     p.row_pieces = cache->head_dim * (cache->format == DSV4_GQA_E4M3 ? 1 : 2) / 16;
     p.err = err;
 
-    // (new lengths that replace the old ones have to wait for every head's CTA to have read those: the move kernel does)
-    p.alone = max_len - keep <= kFew && max_len <= kHeldKeys && (lens_out + batch <= lens || lens + batch <= lens_out);
+    // (new lengths that replace the old ones, or the tokens seen, have to wait for every head's CTA to have read those:
+    // the move kernel does)
+    auto apart = [&](const int* x) { return !x || lens_out + batch <= x || x + batch <= lens_out; };
+    p.alone = max_len - keep <= kFew && max_len <= kHeldKeys && apart(lens) && apart(seq_lens);
     const int r = launch_select(p, stream);
     if (r || p.alone) return r;
     switch (p.row_pieces) {

@@ -157,7 +157,8 @@ size_t dsv4_gqa_decode_workspace_size(const dsv4_gqa_cache* cache, int32_t batch
 
 /* keep >= 1, first >= 0, recent >= 0, first + recent <= keep.  seq_lens:
    tokens that each request has seen (NULL: as many as it has rows).
-   positions and positions_out: both or neither.  lens_out may be lens. */
+   positions and positions_out: both or neither.  lens_out may be lens
+   or seq_lens. */
 int dsv4_gqa_evict(int32_t batch, const int32_t* lens, const int32_t* seq_lens,
                    const int32_t* req_pool_indices, const dsv4_gqa_cache* cache, int32_t max_len,
                    int32_t keep, int32_t first, int32_t recent,

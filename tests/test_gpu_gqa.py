@@ -694,6 +694,24 @@ def test_evict_a_step_of_a_full_cache(A, kv, dim, token_major, inplace):
     check_evict(A, c, lens, 128, max_len=132, w=w, inplace=inplace, want_flags=O.ERR_GQA_PAGE)
 
 
+@pytest.mark.parametrize("slack", [2, 40])
+def test_evict_with_new_lengths_in_place_of_the_tokens_seen(A, slack):
+    # slack 2: one launch, whose CTAs read the tokens seen for every KV head
+    rows, keep = 40, 128
+    c = Case(hkv=8, dim=64, rows=rows, slots=keep + slack, seed=slack)
+    lens = torch.full((rows,), keep + slack, dtype=torch.int32, device="cuda")
+    w = torch.rand(rows, 8, keep + slack, generator=c.gen)
+    results = []
+    for same in (False, True):
+        cache, w_d, seen = c.handle(A), w.cuda(), lens.clone()
+        got = A.dsv4_gqa_evict(lens, cache, w_d, keep, seq_lens=seen, recent=30, max_len=keep + slack,
+                               lens_out=seen if same else None)
+        results.append((got, w_d[:, :, :keep], c.k_d, c.v_d))
+    assert A.dsv4_attn_get_device_error() == 0
+    for x, y in zip(*results):
+        assert torch.equal(x.view(torch.int16) if x.dtype == BF else x, y.view(torch.int16) if y.dtype == BF else y)
+
+
 def test_evict_a_step_of_long_caches(A):
     for slots in (5000, 12000, 30000, 40000):
         c = Case(hkv=2, rows=2, slots=slots, page=1024, seed=slots)
