@@ -179,6 +179,20 @@ def test_decode_groups(A, kv, group):
     check_decode(A, c, [300, 5, 0, 129], 3 * group, weights=True, decay=0.75)
 
 
+@pytest.mark.parametrize("group", [17, 32, 33, 48, 49, 64])
+@pytest.mark.parametrize("kv,dim", [(BF, 64), (BF, 128), (HF, 256), (F8, 64), (F8, 128), (F8, 256)])
+def test_decode_of_wide_groups_over_long_lists(A, kv, dim, group):
+    # several passes over the cache: parts that end inside requests, shared rows, pages outside the pool
+    lens = [2500, 0, 7, 1203, 40, 1]
+    c = Case(kv=kv, hkv=2, dim=dim, rows=6, slots=2500, seed=group + dim, token_major=group % 2 == 1)
+    c.poison(lens)
+    c.table[3, 30:33] = torch.tensor([-1, 10 ** 6, c.k.shape[0]])
+    sink = torch.randn(2 * group, generator=c.gen)
+    check_decode(A, c, lens, 2 * group, weights=True, sink=sink, want_flags=O.ERR_GQA_PAGE)
+    check_decode(A, c, [1203, 2500, 40, 0, 7, 1203], 2 * group, window=700, req=[0, 0, 3, 1, 2, 3], weights=True,
+                 want_flags=O.ERR_GQA_PAGE)
+
+
 @pytest.mark.parametrize("window", [1, 15, 16, 40, 64, 1000])
 @pytest.mark.parametrize("kv,dim", [(BF, 64), (BF, 128), (F8, 64), (HF, 256)])
 def test_decode_windows(A, kv, dim, window):
