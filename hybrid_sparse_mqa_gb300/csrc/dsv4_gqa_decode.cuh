@@ -294,7 +294,9 @@ struct Shape {
     static constexpr int RING_BYTES = W * STAGES * 2 * TILE_BYTES;
     // queries of a segment, a row per head (16 bytes of padding spread the rows over the banks where there is room)
     static constexpr int QROW = D * 2 + (NT == 1 ? 16 : 0);
-    static constexpr int Q_BYTES = HEADS * QROW;
+    // (16 heads of 256 beside e4m3 rows: two CTAs fit an SM only without the buffers; 64 x 1024..16384 rows, 64 / 4
+    // heads: 354 us with them and 246 without)
+    static constexpr int Q_BYTES = FP8 && D == 256 && NT == 2 ? 0 : HEADS * QROW;
     static constexpr int SMEM = RING_BYTES + W * Q_BYTES;
     static constexpr int PPR = ROWB / 16;                    // 16-byte pieces per row
     static constexpr int RPI = 32 / PPR;                     // rows per warp-wide copy
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     come_to();
     int pieces = 0, piece = 0;                     // pieces (a share's part of a segment) that prod has come to; cons's
     int q_piece = -1;                              // piece whose queries the buffer holds or is getting
-    bool q_free = true, fresh = true;              // they have been read; prod has just come to its piece
+    bool q_free = S::Q_BYTES > 0, fresh = true;              // they have been read; prod has just come to its piece
 
     // prod to the tile that is copied next; its page ids are loaded one tile ahead of their use
     auto settle = [&]() {
