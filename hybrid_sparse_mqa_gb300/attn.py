@@ -3,7 +3,10 @@
 Argument marshalling only: every step of the attention computation runs in
 the library's CUDA kernels.  PyTorch supplies device memory (outputs and the
 workspace are allocated here when the caller passes none) and the current
-stream.  Loading fails loudly when the library has not been built; there is
+stream.  With stream= the kernels are queued on that stream instead, which
+waits for nothing queued on the current one: ordering the two, and keeping
+what is passed in alive until that stream has used it, is the caller's part.
+Loading fails loudly when the library has not been built; there is
 no fallback path.
 
 The entry points mirror include/dsv4attn.h:
@@ -153,6 +156,23 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _new(shape, dtype, device, stream):
+    """A tensor that kernels on `stream` (None: the current one) write.  It comes from that stream's own memory: a
+    block of the current stream's may still be in use by kernels queued there, which `stream` does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new_output(shape, dtype, device, stream):
+    """As _new, for a tensor that the caller gets and reads on the current stream."""
+    x = _new(shape, dtype, device, stream)
+    if stream is not None:
+        x.record_stream(torch.cuda.current_stream())
+    return x
 
 
 def make_pool(rows, page_table, kv_format=None):
@@ -422,9 +442,7 @@ def _raw_stream(stream, index):
 
 def _scratch(workspace, need, cache, stream):
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=cache._keep[0].device)
-        if stream is not None:
-            workspace.record_stream(stream)     # freed here, still read there
+        workspace = _new(need, torch.uint8, cache._keep[0].device, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != cache._index:
         raise Dsv4Error("workspace must be a contiguous tensor on the cache's device")
     return workspace, workspace.numel() * workspace.element_size()
@@ -528,15 +546,11 @@ def dsv4_gqa_decode(q, lens, cache, *, sink=None, scale=None, window=0, max_len=
     elif weights_out is not None:
         raise Dsv4Error("weights_out goes with weights")
     if out is None:
-        out = torch.empty(batch, heads, dim, dtype=q.dtype, device=q.device)
-        if stream is not None:
-            out.record_stream(stream)
+        out = _new_output((batch, heads, dim), q.dtype, q.device, stream)
     elif out.shape != q.shape or not _is(out, q.dtype, batch * heads * dim, index):
         raise Dsv4Error("out must be a contiguous tensor like q")
     if lse is None:
-        lse = torch.empty(batch, heads, dtype=torch.float32, device=q.device)
-        if stream is not None:
-            lse.record_stream(stream)
+        lse = _new_output((batch, heads), torch.float32, q.device, stream)
     else:
         _need(lse, "lse", torch.float32, batch * heads, index)
     if batch == 0:
@@ -600,9 +614,7 @@ def dsv4_gqa_evict(lens, cache, weights, keep, *, seq_lens=None, positions=None,
     if max_len > width:
         raise Dsv4Error("weights must be at least max_len wide")
     if lens_out is None:
-        lens_out = torch.empty_like(lens)
-        if stream is not None:
-            lens_out.record_stream(stream)
+        lens_out = _new_output(lens.shape, torch.int32, lens.device, stream)
     else:
         _need(lens_out, "lens_out", torch.int32, batch, index)
     if batch == 0:

@@ -369,6 +369,49 @@ def test_decode_in_a_graph_and_on_streams(A):
         assert torch.equal(o, want[0]) and torch.equal(l, want[1])
 
 
+def test_calls_on_two_streams_without_workspaces(A):
+    # a call on the current stream gives its scratch back when it returns, with its kernels still queued; the next
+    # call, on another stream and of the same sizes, must not get it
+    sets = []
+    for i in range(2):
+        c = Case(hkv=8, dim=128, page=64, rows=4, slots=20000, seed=80 + i)
+        w = torch.rand(4, 8, 20032, generator=c.gen).cuda()
+        lens = torch.tensor([20000, 7, 15000 - i, 19999], dtype=torch.int32).cuda()
+        sets.append((c.handle(A), c.query(4, 16).cuda(), lens, w, c))
+    s = torch.cuda.Stream()
+    keep = 3000
+
+    def call(i, stream, kept):
+        cache, q, lens, w, c = sets[i]
+        if kept == "evict":
+            return [A.dsv4_gqa_evict(lens, cache, w, keep, weights_out=kept_out[i], stream=stream), kept_out[i]]
+        wo = kept_out[i]
+        return list(A.dsv4_gqa_decode(q, lens, cache, weights=w if kept else None, weights_out=wo if kept else None,
+                                      stream=stream)) + [wo]
+
+    for kept in (False, True, "evict"):
+        pools = [(c.k_d.clone(), c.v_d.clone()) for *_, c in sets]
+        kept_out = [torch.zeros_like(sets[i][3]) for i in range(2)]
+        want = []
+        for i in range(2):
+            want.append([x.clone() for x in call(i, None, kept)])
+            torch.cuda.synchronize()
+        moved = [(c.k_d.clone(), c.v_d.clone()) for *_, c in sets]
+        for _ in range(4):
+            for (*_, c), (k, v) in zip(sets, pools):
+                c.k_d.copy_(k)
+                c.v_d.copy_(v)
+            kept_out = [torch.zeros_like(sets[i][3]) for i in range(2)]
+            torch.cuda.synchronize()
+            got = [call(0, None, kept), call(1, s, kept)]
+            torch.cuda.synchronize()
+            for x, y in zip(got, want):
+                assert all(torch.equal(p, r) for p, r in zip(x, y))
+            for (*_, c), (k, v) in zip(sets, moved):
+                assert np.array_equal(_bits(c.k_d), _bits(k)) and np.array_equal(_bits(c.v_d), _bits(v))
+    assert A.dsv4_attn_get_device_error() == 0
+
+
 def test_decode_of_nothing(A):
     c = Case(rows=2, slots=32)
     cache = c.handle(A)
