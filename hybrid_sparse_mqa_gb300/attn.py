@@ -199,19 +199,19 @@ def _check(rc):
         raise Dsv4Error(f"dsv4attn: {lib().dsv4_attn_strerror(rc).decode()} ({rc})")
 
 
-def _outputs(q, out, lse):
+def _outputs(q, out, lse, stream):
     T, H = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_output(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty(T, H, dtype=torch.float32, device=q.device)
+        lse = _new_output((T, H), torch.float32, q.device, stream)
     return out, lse
 
 
-def _workspace(workspace, T, H, ratio, window, topk, max_seq_len, num_splits, device):
+def _workspace(workspace, T, H, ratio, window, topk, max_seq_len, num_splits, device, stream):
     need = lib().dsv4_attn_workspace_size(T, H, ratio, window, topk, max_seq_len, num_splits)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _new(need, torch.uint8, device, stream)
     return workspace, (0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
@@ -224,8 +224,8 @@ def dsv4_attn_swa(q, seq_lens, swa_pool, sink, *, scale=1.0 / math.sqrt(512), wi
                   req_pool_indices=None, out=None, lse=None, num_splits=0, workspace=None,
                   debug_rows=None, stream=None):
     T, H = q.shape[0], q.shape[1]
-    out, lse = _outputs(q, out, lse)
-    workspace, wsb = _workspace(workspace, T, H, 0, window, 0, 0, num_splits, q.device)
+    out, lse = _outputs(q, out, lse, stream)
+    workspace, wsb = _workspace(workspace, T, H, 0, window, 0, 0, num_splits, q.device, stream)
     _check(lib().dsv4_attn_swa(_ptr(q), T, H, _ptr(seq_lens), _ptr(req_pool_indices),
                                ctypes.byref(swa_pool), window, _ptr(sink), scale, _ptr(out), _ptr(lse),
                                num_splits, _ptr(workspace), wsb, _ptr(debug_rows), _stream(stream)))
@@ -237,8 +237,8 @@ def dsv4_attn_c4_sparse(q, seq_lens, swa_pool, extra_pool, topk_idx, sink, *,
                         lse=None, num_splits=0, workspace=None, debug_rows=None, stream=None):
     T, H = q.shape[0], q.shape[1]
     topk = topk_idx.shape[1]
-    out, lse = _outputs(q, out, lse)
-    workspace, wsb = _workspace(workspace, T, H, 4, window, topk, 0, num_splits, q.device)
+    out, lse = _outputs(q, out, lse, stream)
+    workspace, wsb = _workspace(workspace, T, H, 4, window, topk, 0, num_splits, q.device, stream)
     _check(lib().dsv4_attn_c4_sparse(_ptr(q), T, H, _ptr(seq_lens), _ptr(req_pool_indices),
                                      ctypes.byref(swa_pool), window, ctypes.byref(extra_pool),
                                      _ptr(topk_idx), topk, _ptr(sink), scale, _ptr(out), _ptr(lse),
@@ -255,7 +255,7 @@ def dsv4_attn_c4_sparse_noalloc(q, seq_lens, swa_pool, extra_pool, topk_idx, sin
     T, H = q.shape[0], q.shape[1]
     topk = topk_idx.shape[1]
     if out is None or lse is None:
-        out, lse = _outputs(q, out, lse)
+        out, lse = _outputs(q, out, lse, stream)
     _check(lib().dsv4_attn_c4_sparse_noalloc(_ptr(q), T, H, _ptr(seq_lens), _ptr(req_pool_indices),
                                              ctypes.byref(swa_pool), window, ctypes.byref(extra_pool),
                                              _ptr(topk_idx), topk, _ptr(sink), scale, _ptr(out), _ptr(lse),
@@ -267,8 +267,8 @@ def dsv4_attn_c128_dense(q, seq_lens, swa_pool, extra_pool, sink, *, max_seq_len
                          scale=1.0 / math.sqrt(512), window=128, req_pool_indices=None, out=None,
                          lse=None, num_splits=0, workspace=None, debug_rows=None, stream=None):
     T, H = q.shape[0], q.shape[1]
-    out, lse = _outputs(q, out, lse)
-    workspace, wsb = _workspace(workspace, T, H, 128, window, 0, max_seq_len, num_splits, q.device)
+    out, lse = _outputs(q, out, lse, stream)
+    workspace, wsb = _workspace(workspace, T, H, 128, window, 0, max_seq_len, num_splits, q.device, stream)
     _check(lib().dsv4_attn_c128_dense(_ptr(q), T, H, _ptr(seq_lens), _ptr(req_pool_indices),
                                       ctypes.byref(swa_pool), window, ctypes.byref(extra_pool),
                                       max_seq_len, _ptr(sink), scale, _ptr(out), _ptr(lse), num_splits,
@@ -282,9 +282,9 @@ def dsv4_attn_verify(q, seq_lens, cu_seqlens_q, swa_pool, sink, *, compress_rati
                      workspace=None, debug_rows=None, stream=None):
     T, H = q.shape[0], q.shape[1]
     topk = 0 if topk_idx is None else topk_idx.shape[1]
-    out, lse = _outputs(q, out, lse)
+    out, lse = _outputs(q, out, lse, stream)
     workspace, wsb = _workspace(workspace, T, H, compress_ratio, window, topk, max_seq_len,
-                                num_splits, q.device)
+                                num_splits, q.device, stream)
     _check(lib().dsv4_attn_verify(_ptr(q), T, batch, H, _ptr(seq_lens), _ptr(cu_seqlens_q),
                                   _ptr(req_pool_indices), ctypes.byref(swa_pool), window,
                                   compress_ratio,
@@ -349,7 +349,7 @@ def dsv4_topk(scores, lengths, k, *, max_length=None, out=None, stream=None):
     if max_length is None:
         max_length = scores.shape[1]
     if out is None:
-        out = torch.empty(rows, k, dtype=torch.int32, device=scores.device)
+        out = _new_output((rows, k), torch.int32, scores.device, stream)
     _check(lib().dsv4_topk(_ptr(scores), rows, scores.stride(0), _ptr(lengths), max_length, k, _ptr(out),
                            _stream(stream)))
     return out

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from oracle import gqa_oracle as O
+from tests._streams import Streams
 
 
 @pytest.fixture(scope="module")
@@ -287,54 +288,6 @@ def test_counts_whose_arithmetic_would_wrap_are_refused(A):
         assert _store(A, wide, n=max_len) == -1
 
 
-class _Streams:
-    """Stand-ins for the device side of the binding: calls return 0, and every torch.empty notes the stream whose
-    memory it would come from."""
-
-    def __init__(self, A, monkeypatch):
-        self.now, self.made, self.recorded = "current", [], []
-        fake = self
-
-        class Within:
-            def __init__(self, stream):
-                self.stream = stream
-
-            def __enter__(self):
-                fake.before, fake.now = fake.now, self.stream
-
-            def __exit__(self, *_):
-                fake.now = fake.before
-
-        real = {name: getattr(torch, name) for name in ("empty", "empty_like")}
-
-        def making(name):
-            def make(*args, **kw):
-                x = real[name](*args, **kw)
-                fake.made.append((fake.now, x.data_ptr()))
-                return x
-            return make
-
-        class Library:
-            def __getattr__(self, name):
-                return lambda *args: 4096 if name.endswith("_size") else 0
-
-        monkeypatch.setattr(A, "_lib", Library())
-        monkeypatch.setattr(A, "_raw_stream", lambda stream, index: 0)
-        monkeypatch.setattr(A, "_stream", lambda stream: None)
-        monkeypatch.setattr(torch.cuda, "stream", Within)
-        monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: "current")
-        monkeypatch.setattr(torch.Tensor, "record_stream", lambda x, s: fake.recorded.append((s, x.data_ptr())),
-                            raising=False)
-        for name in real:
-            monkeypatch.setattr(torch, name, making(name))
-
-    def check(self, returned):
-        """All memory was the given stream's, and the caller's stream is on record for what it gets."""
-        assert self.made and all(stream == "given" for stream, _ in self.made), self.made
-        for x in returned:
-            assert ("current", x.data_ptr()) in self.recorded
-
-
 def test_what_a_call_allocates_is_its_streams_own(A, monkeypatch):
     k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
     c = A.make_gqa_cache(k, k.clone(), torch.zeros(3, 2, dtype=torch.int32))
@@ -345,9 +298,9 @@ def test_what_a_call_allocates_is_its_streams_own(A, monkeypatch):
     ]
     for call in calls:
         with monkeypatch.context() as m:
-            streams = _Streams(A, m)
+            streams = Streams(A, m)
             streams.check(call("given"))
         with monkeypatch.context() as m:
-            streams = _Streams(A, m)
+            streams = Streams(A, m)
             call(None)
             assert all(stream == "current" for stream, _ in streams.made) and not streams.recorded

@@ -5,6 +5,9 @@ import os
 import re
 
 import pytest
+import torch
+
+from tests._streams import Streams
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -148,3 +151,21 @@ def test_plan_without_device_reports_cuda_error(A):
         pytest.skip("a device is present")
     sc, sg = ctypes.c_int32(), ctypes.c_int32()
     assert A.lib().dsv4_attn_plan(32, 64, 4, 128, 512, 0, 0, ctypes.byref(sc), ctypes.byref(sg)) == -4
+
+
+def test_what_a_call_allocates_is_its_streams_own(A, monkeypatch):
+    q, sink, lens = torch.zeros(2, 4, 512, dtype=torch.bfloat16), torch.zeros(4), torch.ones(2, dtype=torch.int32)
+    pool = A.make_pool(torch.zeros(256, 512, dtype=torch.bfloat16), torch.zeros(2, 1, dtype=torch.int32))
+    idx, scores = torch.zeros(2, 512, dtype=torch.int32), torch.zeros(2, 1024)
+    calls = [
+        lambda s: A.dsv4_attn_swa(q, lens, pool, sink, stream=s),
+        lambda s: A.dsv4_attn_c4_sparse(q, lens, pool, pool, idx, sink, stream=s),
+        lambda s: A.dsv4_attn_c4_sparse_noalloc(q, lens, pool, pool, idx, sink, stream=s),
+        lambda s: A.dsv4_attn_c128_dense(q, lens, pool, pool, sink, max_seq_len=1024, stream=s),
+        lambda s: A.dsv4_attn_verify(q, lens, lens, pool, sink, compress_ratio=0, batch=1, stream=s),
+        lambda s: [A.dsv4_topk(scores, lens, 64, stream=s)],
+    ]
+    for call in calls:
+        with monkeypatch.context() as m:
+            streams = Streams(A, m)
+            streams.check(call("given"))
