@@ -3,6 +3,7 @@
 // (dsv4_gqa_decode.cuh): the join of split requests and the accumulation of
 // weights.
 #include <algorithm>
+#include <atomic>
 
 #include "dsv4_gqa_decode.cuh"
 
@@ -283,6 +284,8 @@ int tile_slots(int format, int head_dim) {
     return rows < 16 ? 16 : rows;
 }
 
+std::atomic<int> g_claim_ahead{kClaimAhead}, g_claim_polls{kWaitLimit};
+
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct Plan {
@@ -385,6 +388,11 @@ int launch_weights(const DecodeParams& p, int nt, void* stream) {
 
 extern "C" {
 
+void dsv4_gqa_test_claim_limits(int32_t ahead, int32_t polls) {
+    dsv4::gqa::g_claim_ahead = ahead < 0 ? dsv4::gqa::kClaimAhead : ahead;
+    dsv4::gqa::g_claim_polls = polls < 0 ? dsv4::gqa::kWaitLimit : polls;
+}
+
 size_t dsv4_gqa_decode_workspace_size(const dsv4_gqa_cache* cache, int32_t batch, int32_t num_heads, int32_t max_len,
                                       int32_t with_weights) {
     dsv4::gqa::Plan pl;
@@ -441,6 +449,8 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     p.min_tiles = pl.min_tiles;
     p.warps = pl.ctas * kWarps;
     p.claims = pl.claims;
+    p.claim_ahead = g_claim_ahead.load(std::memory_order_relaxed);
+    p.claim_polls = g_claim_polls.load(std::memory_order_relaxed);
     p.pieces = static_cast<int>(std::min<long long>(p.warps + p.claims * kWarps, pl.tiles / pl.min_tiles));
     // (with weights, requests may add to one row only through the list's kernels, and so may several chunks of heads)
     p.cluster = weights && (req_pool_indices || pl.chunks > 1) ? 0 : segment_cluster(p, pl);

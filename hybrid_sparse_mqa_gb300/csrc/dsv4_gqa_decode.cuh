@@ -74,7 +74,7 @@ constexpr int kTail = 3;
 constexpr int kClaimTiles = 64;            // a list is long from so many tiles per resident warp
 constexpr int kClaimAhead = 4;             // tiles before the end of a share at which the next is asked for
 constexpr int kClaimRing = 16;             // claims that a warp may be behind another of its CTA
-constexpr int kWaitLimit = 1 << 20;        // polls before a claim is given up
+constexpr int kWaitLimit = 1 << 20;        // polls (some ten ns each) before a claim is given up
 
 struct DecodeParams {
     Cache c;
@@ -104,6 +104,7 @@ struct DecodeParams {
     int min_tiles;                         // a share has at least this many tiles (where there are as many)
     int warps;                             // of the resident CTAs
     int claims;                            // CTAs of the grid behind those, to be claimed (0: none)
+    int claim_ahead, claim_polls;          // kClaimAhead, kWaitLimit (a test sets others)
     int pieces;                            // bound on the shares (for the host)
     int cluster;                           // CTAs per segment, where segments are not cut (0: by shares)
     unsigned int* err;
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     auto settle = [&]() {
         if (tail && more) {
             // the next share is asked for a little before this one ends
-            asking |= prod.at + kClaimAhead >= p1;
+            asking |= prod.at + p.claim_ahead >= p1;
             if (asking && next_p == -2) next_p = taken(entry_p + 1);
         }
         if (more && prod.at >= prod.end) {
@@ -546,11 +547,15 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 more = false;
             } else if (!prod.next_segment(p, hcs, p1)) {
                 for (int tries = 0; tail && next_p == -2; ++tries) {
-                    next_p = taken(entry_p + 1);
-                    if (tries >= kWaitLimit) {
-                        if (lane == 0) atomicOr(p.err, DSV4_DEV_ERR_TIMEOUT);
-                        next_p = -1;
+                    if (tries < p.claim_polls) {
+                        next_p = taken(entry_p + 1);
+                        continue;
                     }
+                    // given up: nobody computes this warp's part of what the CTA took over.  An answer on its way to
+                    // this warp lands before the CTA may end (and is published to its other warps)
+                    if (lane == 0) atomicOr(p.err, DSV4_DEV_ERR_TIMEOUT);
+                    for (int i = 0; i < kWaitLimit && __shfl_sync(0xffffffffu, sent, 0); ++i) taken(entry_p + 1);
+                    next_p = -1;
                 }
                 more = next_p >= 0;
                 if (more) {
@@ -1018,6 +1023,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         on = cons.next_segment(p, hcs, c1);
         if (!on && entry_c < entry_p) {
             ++entry_c;
+            // (the entry is overwritten only once every warp's s_done is past it, which takes this warp's next time here)
             share = share_id(*(volatile int*)&s_cta[entry_c % kClaimRing]);
             if (lane == 0) *(volatile int*)&s_done[warp] = entry_c;
             c1 = share_begin(shares, share + 1);

@@ -20,4 +20,10 @@ __attribute__((visibility("hidden"))) unsigned int* device_error_word();
 
 }  // namespace dsv4
 
+// For tests of what a claim that is given up leaves behind (dsv4_gqa_decode):
+// how many tiles before the end of its share a warp asks for another one, and
+// how often it then looks for the answer.  Negative: the library's own value.
+// Holds for the calls of the process that follow.
+extern "C" void dsv4_gqa_test_claim_limits(int32_t ahead, int32_t polls);
+
 #endif

@@ -71,7 +71,9 @@
  *   request without rows (DSV4_DEV_ERR_REQ_ROW; unreported for length 0, so
  *   a padded batch may hold any row there), rows on a page id outside the
  *   pool are skipped (DSV4_DEV_ERR_GQA_PAGE), a stored row that has no place
- *   is skipped (DSV4_DEV_ERR_STORE_ROW).
+ *   is skipped (DSV4_DEV_ERR_STORE_ROW).  DSV4_DEV_ERR_TIMEOUT after a decode
+ *   call: a wait inside its kernel was given up (a library bug), and what the
+ *   call wrote to its outputs is undefined; later calls are not affected.
  *   Every kernel can be captured into a graph; make the first call of a
  *   function on a device before any capture (its kernels are loaded then).
  *   A captured call reads lens, tables and rows anew at every replay.

@@ -526,6 +526,31 @@ def test_long_lists_at_once_and_in_graphs(A):
     assert A.dsv4_attn_get_device_error() == 0
 
 
+def test_claims_that_are_given_up(A):
+    # with one look for each answer, warps give up while theirs is on its way: the call ends and says so, and the next
+    # one is right
+    rows, hkv, heads, dim, page, n = 2, 8, 8, 128, 256, 90000
+    width = -(-n // page)
+    gen = torch.Generator(device="cuda").manual_seed(79)
+    k, v = (torch.randn(rows * width, hkv, page, dim, generator=gen, device="cuda", dtype=BF) for _ in range(2))
+    table = torch.arange(rows * width, device="cuda").view(rows, width).to(torch.int32)
+    cache = A.make_gqa_cache(k, v, table)
+    q = torch.randn(rows, heads, dim, generator=gen, device="cuda", dtype=BF)
+    lens = torch.tensor([n, n - 5], dtype=torch.int32).cuda()
+    want = A.dsv4_gqa_decode(q, lens, cache)
+    assert A.dsv4_attn_get_device_error() == 0
+    for _ in range(3):
+        try:
+            A.lib().dsv4_gqa_test_claim_limits(0, 1)
+            A.dsv4_gqa_decode(q, lens, cache)
+        finally:
+            A.lib().dsv4_gqa_test_claim_limits(-1, -1)
+        assert A.dsv4_attn_get_device_error() == A.DEV_ERR["TIMEOUT"]
+        got = A.dsv4_gqa_decode(q, lens, cache)
+        assert A.dsv4_attn_get_device_error() == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ---------------------------------------------------------------- store
 def _bits(x):
     x = x.detach().cpu()
