@@ -386,6 +386,29 @@ struct Cursor {
     }
 };
 
+// The infinities among the values of slots s0 .. s1 - 1 of a request row, 16-bit caches: two bits for each of the D / 32
+// dims from lane D / 32 on, 1 for +inf and 2 for -inf (both: a NaN too).  The whole warp calls.
+template <class S>
+__device__ __noinline__ uint32_t infinite_values(const DecodeParams& p, int row, int h, int s0, int s1) {
+    constexpr int V = S::D / 32;
+    constexpr uint32_t kInf = S::BF16 ? 0x7f80u : 0x7c00u;
+    const int* table = p.c.table + (long long)row * p.c.table_stride;
+    const uint8_t* base = p.c.v + h * p.c.head_stride + (threadIdx.x & 31) * (V * 2);
+    uint32_t found = 0;
+    for (int s = s0; s < s1; ++s) {
+        const int page = __ldg(table + (s >> p.c.page_shift));
+        if (page < 0 || page >= p.c.num_pages) continue;
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(
+            base + page * p.c.page_stride + (s & ((1 << p.c.page_shift) - 1)) * p.c.row_stride);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t x = from[i / 2] >> (16 * (i & 1)), size = x & 0x7fffu;
+            if (size >= kInf) found |= (size > kInf ? 3u : x & 0x8000u ? 2u : 1u) << (2 * i);
+        }
+    }
+    return found;
+}
+
 // SEG: a cluster per segment; else a share of the list per warp.
 template <class S, bool SEG>
 __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(const __grid_constant__ DecodeParams p) {
@@ -897,6 +920,40 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 lsum[nt][u] += __shfl_xor_sync(0xffffffffu, lsum[nt][u], 8);
                 lsum[nt][u] += __shfl_xor_sync(0xffffffffu, lsum[nt][u], 16);
             }
+        if constexpr (!S::FP8) {
+            // P's two parts times an infinite value can be inf - inf or 0 inf, which is NaN where the sum is infinite:
+            // where a NaN comes of finite scores, the infinities are looked up
+            bool odd = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    bool any = false;
+#pragma unroll
+                    for (int j = 0; j < DT; ++j) any |= isnan(o[j][nt][u]) || isnan(o[j][nt][u + 2]);
+                    odd |= any && !isnan(lsum[nt][u]);
+                }
+            if (__any_sync(0xffffffffu, odd)) {
+                const int t0 = cons.rg.lo / TT - static_cast<int>(cons.seg);
+                const uint32_t found = infinite_values<S>(p, cons.rq.row, h,
+                                                          max(cons.rg.lo, (t0 + static_cast<int>(cons.at)) * TT),
+                                                          min(cons.rg.n, (t0 + static_cast<int>(cons.end)) * TT));
+#pragma unroll
+                for (int j = 0; j < DT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; c += 2) {
+                        const int d = 16 * j + 4 * c + g;
+                        const uint32_t f = __shfl_sync(0xffffffffu, found, d / (D / 32)) >> (2 * (d % (D / 32))) & 3u;
+                        if (f == 1u || f == 2u)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u)
+                                    if (isnan(o[j][nt][c + u]) && !isnan(lsum[nt][u]))
+                                        o[j][nt][c + u] = f == 1u ? INFINITY : -INFINITY;
+                    }
+            }
+        }
         // the next piece, if there is one
         const bool cut = !begins || cons.end != cons.seg + cons.rg.tiles;
         const int here_b = cons.b, here = share;

@@ -36,7 +36,10 @@
  *     s_j = scale * <q_i, K_j>,  j = lo .. n-1
  *     L   = exp(sink[i]) + sum_j exp(s_j)          (no sink: that term is 0)
  *     out = sum_j exp(s_j) V_j / L       lse = ln L
- *   A request with no rows gets out = 0 and lse = sink[i] (or -inf).  With
+ *   A request with no rows gets out = 0 and lse = sink[i] (or -inf).  An
+ *   infinite value of an attended V row makes its dim of out infinite (NaN
+ *   where both signs or a NaN meet), as the sum does; finite bf16 values must
+ *   stay below 2^90, where fp32 sums of 2^30 rows cannot overflow.  With
  *   `weights_out`, for j = 0 .. n-1,
  *     weights_out[r][h][j] = decay * weights[r][h][j]
  *                            + sum over the heads i of h of exp(s_j - lse_i)

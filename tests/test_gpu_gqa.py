@@ -260,6 +260,52 @@ def test_decode_small_queries_of_an_e4m3_cache(A):
         check_decode(A, c, [60, 33], 4, spread=spread, scale=0.125 / spread)
 
 
+@pytest.mark.parametrize("heads", [2, 8, 24])
+@pytest.mark.parametrize("kv,dim", [(BF, 64), (BF, 128), (HF, 64), (HF, 128), (HF, 256)])
+@pytest.mark.parametrize("slots,lens", [(100, [100, 1, 17]), (9000, [9000, 4001, 40])])
+def test_decode_of_infinite_values(A, kv, dim, heads, slots, lens):
+    # a value that overflowed when it was written: infinite where every infinity of the dim has one sign, NaN where
+    # both signs or a NaN meet, and all other dims as if it were not there
+    c = Case(kv=kv, hkv=2, dim=dim, rows=3, slots=slots, seed=dim + heads)
+    q = c.query(3, heads)
+    lens_t = torch.tensor(lens, dtype=torch.int32).cuda()
+    plain = A.dsv4_gqa_decode(q.cuda(), lens_t, c.handle(A), max_len=slots)
+
+    def put(b, h, s, d, x):
+        c.v[int(c.table[b, s // c.page]), h, s % c.page, d] = x
+
+    marks = {}                                    # (request, KV head, dim): what its outputs are
+    for b, n in enumerate(lens):
+        for h in range(2):
+            for i in range(6):
+                d = int(torch.randint(0, dim // 8, (1,), generator=c.gen)) * 8 + i
+                for s in torch.randint(0, n, (1 + i,), generator=c.gen).tolist():
+                    put(b, h, s, d, -math.inf if i % 2 else math.inf)
+                marks[b, h, d] = -math.inf if i % 2 else math.inf
+            put(b, h, n - 1, dim - 1, math.nan)
+            marks[b, h, dim - 1] = math.nan
+            put(b, h, 0, dim - 2, math.inf)
+            put(b, h, n - 1, dim - 2, -math.inf)
+            marks[b, h, dim - 2] = math.nan if n > 1 else -math.inf
+    c.poison(lens)
+    w = torch.zeros(3, 2, c.width * c.page).cuda()
+    cache = c.handle(A)
+    results = [A.dsv4_gqa_decode(q.cuda(), lens_t, cache, max_len=slots),
+               A.dsv4_gqa_decode(q.cuda(), lens_t, cache, max_len=slots, weights=w,
+                                 req_pool_indices=torch.arange(3, dtype=torch.int32).cuda())]
+    assert A.dsv4_attn_get_device_error() == 0
+    group = heads // 2
+    for i, (out, lse) in enumerate(results):
+        want = results[1][0].clone() if i else plain[0].clone()
+        for (b, h, d), x in marks.items():
+            want[b, h * group: (h + 1) * group, d] = x
+        assert torch.equal(out.isnan(), want.isnan())
+        assert torch.equal(out.nan_to_num(nan=0.0, posinf=math.inf, neginf=-math.inf),
+                           want.nan_to_num(nan=0.0, posinf=math.inf, neginf=-math.inf))
+        if i == 0:
+            assert torch.equal(lse, plain[1])
+
+
 def test_decode_sinks(A):
     c = Case(rows=3, slots=60, seed=7)
     for value in (-math.inf, -100.0, 0.0, 60.0, math.inf):
