@@ -37,7 +37,8 @@
 // O^T = V^T P^T by one 8x8 transposition in registers (movmatrix).  The
 // softmax is online with a lazy reference: a tile's scores are compared with
 // the running reference by one vote, and the reference moves (and O and the
-// sums are rescaled) only when some score exceeds it by more than 2^8.
+// sums are rescaled) only when some score exceeds it by more than 2^8 (f16
+// operands: 2^15, see Shape).
 //
 // Bound by HBM for lists of 100 tiles per warp and more: 334 us for 2.34 GB (32 x
 // 2048..32768 rows, 8 KV heads of 128, bf16: 7.0 TB/s), 165 us for 1.07 GB (2 x
@@ -46,12 +47,15 @@
 //
 // Precision: scores, references, sums, O and the merge are fp32.  For 16-bit
 // caches P enters the MMA as the sum of two 16-bit values (the rounded value
-// and the rounded rest), so its rounding stays below 2^-16 and the output's
-// own rounding is what remains; the second MMA costs nothing measurable in a
-// kernel bound by memory.  For e4m3 caches codes are exact in f16 and P is
-// one f16 (2^-11 relative, below the output's bf16 2^-8 or equal to its f16
-// step); q is scaled by a power of two per head so that its largest value
-// lies in [2^14, 2^15), which keeps every bf16 value down to 2^-39 of it.
+// and the rounded rest), so its rounding stays below 2^-16 of it and the
+// output's own rounding is what remains; the second MMA costs nothing
+// measurable in a kernel bound by memory.  For e4m3 caches codes are exact in
+// f16 and P is one f16: 2^-12 of it, an eighth of a bf16 output's rounding and
+// as much as an f16 output's.  Pieces of f16 end at 2^-24, which adds 2^-36 of
+// the largest P at most (Shape::DROP).  q beside e4m3 rows is scaled by a power
+// of two per head so that its largest value lies in [2^14, 2^15): a bf16 value
+// keeps all its bits down to 2^-31 of the largest, and below that is off by at
+// most 2^-39 of it.
 #pragma once
 
 #include "dsv4_gqa.cuh"
@@ -288,6 +292,11 @@ struct Shape {
     static constexpr int MT = TT / 16;                       // 16-slot MMA tiles
     static constexpr int DT = D / 16;                        // 16-dim tiles
     static constexpr int HEADS = 8 * NT;                     // query heads of a segment (padded)
+    // The reference of a softmax lies DROP below the largest score when it moves, and moves when a score exceeds that
+    // score by more than SLACK (log2 units).  P as f16 ends at 2^-24, so it is kept as large as f16 allows: its largest
+    // values lie in [2^11, 2^15], and rounding to zero or to subnormals is off by at most 2^-25 2^-DROP = 2^-36 of the
+    // largest.  (bf16 has the exponents of fp32 and does without.)
+    static constexpr float DROP = BF16 ? 0.f : 11.f, SLACK = BF16 ? 8.f : 4.f;
     static constexpr int W = kWarps;
     static constexpr int TILE_BYTES = TT * ROWB;             // K or V of a stage
     static constexpr int STAGES = 3;
@@ -805,7 +814,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                             if (slot < cons.rg.lo || slot >= cons.rg.n || !((okm >> m) & 1)) x = -INFINITY;
                         }
                         s[m][nt][c] = x;
-                        above |= x > mref[nt][c & 1] + 8.f;
+                        above |= x > mref[nt][c & 1] + (S::DROP + S::SLACK);
                     }
             if (p.logits) {
                 float* to = p.logits + (size_t)tile * TT * HEADS;
@@ -823,12 +832,13 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        float mx = mref[nt][u];
+                        float mx = -INFINITY;
 #pragma unroll
                         for (int m = 0; m < MT; ++m) mx = fmaxf(mx, fmaxf(s[m][nt][u], s[m][nt][u + 2]));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        mx = fmaxf(mref[nt][u], mx - S::DROP);
                         const float f = fast_exp2(mref[nt][u] - mx);
                         mref[nt][u] = mx;
                         lsum[nt][u] *= f;

@@ -306,6 +306,43 @@ def test_decode_of_infinite_values(A, kv, dim, heads, slots, lens):
             assert torch.equal(lse, plain[1])
 
 
+@pytest.mark.parametrize("slots,lens", [(900, [900, 333]), (9000, [9000, 4001])])
+@pytest.mark.parametrize("kv,q", [(BF, BF), (HF, HF), (F8, BF), (F8, HF)])
+@pytest.mark.parametrize("below", [12, 18, 22, 26, 30])
+def test_decode_of_many_rows_far_below_one(A, kv, q, below, slots, lens):
+    # the first row takes nearly all the weight and has the value zero, so the output is the sum of thousands of weights
+    # of about 2^-below.  The scores are exact (one nonzero product); p is 2^x of them: 2^-20, and its half step for
+    # the MMA, which is 2^-17 of p (two pieces) or 2^-12 (one), and below f16's normal numbers 2^-36 of the largest p.
+    c = Case(kv=kv, q=q, hkv=1, dim=64, rows=2, slots=slots, seed=below)
+    c.ks = c.vs = None
+    k, v = torch.zeros(c.k.shape), torch.ones(c.v.shape)
+    k[..., 0] = -below
+    v[:, :, ::3, 1::2] = 0.5
+    for b in range(2):
+        k[int(c.table[b, 0]), :, 0] = 0.0
+        v[int(c.table[b, 0]), :, 0] = 0.0
+    c.k, c.v = k.to(kv), v.to(kv)
+    assert torch.equal(c.k.float(), k)
+    query = torch.zeros(2, 8, 64)
+    query[:, :, 0] = 1.0
+    scale = 0.71                                      # weights of 2^-1.024 below
+    out, lse = A.dsv4_gqa_decode(query.to(q).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), c.handle(A),
+                                 scale=scale, max_len=slots)
+    assert A.dsv4_attn_get_device_error() == 0
+    p = math.exp(-float(np.float32(scale)) * below)
+    for b, n in enumerate(lens):
+        rows = c.v.double()[c.table[b].long()].transpose(1, 2).reshape(-1, 64)[1:n]
+        total = 1 + (n - 1) * p
+        ref = rows.sum(0) * p / total
+        exponents = below * 2.0 ** -23                # the rounding of the score and of its difference from the reference
+        rel = 2.0 ** -19 + 4 * exponents + (n / 16 + 64) * 2.0 ** -23 + (2.0 ** -17 if kv != F8 else 2.0 ** -12)
+        tol = ref * (rel + torch.finfo(q).eps / 2) + (0 if kv == BF else (n - 1) * 2.0 ** -36 / total)
+        if q == HF:
+            tol = tol + 2.0 ** -25                    # an output below f16's normal numbers
+        assert ((out[b].double().cpu() - ref).abs() <= tol).all(), float(((out[b].double().cpu() - ref).abs() / tol).max())
+        assert (lse[b].double().cpu() - math.log(total)).abs().max() <= 2.0 ** -19 + (n / 16 + 64) * 2.0 ** -23 + 2.0 ** -20
+
+
 def test_decode_sinks(A):
     c = Case(rows=3, slots=60, seed=7)
     for value in (-math.inf, -100.0, 0.0, 60.0, math.inf):
