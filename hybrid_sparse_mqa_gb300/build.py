@@ -13,7 +13,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", name) for name in (
     "dsv4_attn.cu", "dsv4_kv_store.cu", "dsv4_topk.cu", "dsv4_gqa_store.cu", "dsv4_gqa_decode.cu",
-    "dsv4_gqa_decode_bf16.cu", "dsv4_gqa_decode_f16.cu", "dsv4_gqa_decode_e4m3.cu", "dsv4_gqa_evict.cu")]
+    "dsv4_gqa_decode_bf16.cu", "dsv4_gqa_decode_f16.cu", "dsv4_gqa_decode_e4m3.cu",
+    "dsv4_gqa_decode_e4m3_f16.cu", "dsv4_gqa_evict.cu")]
 DEPS = SOURCES + [os.path.join(PKG, "csrc", "dsv4_device.cuh"), os.path.join(PKG, "csrc", "dsv4_internal.h"),
                   os.path.join(ROOT, "include", "dsv4attn.h"), os.path.join(ROOT, "include", "dsv4kvstore.h"),
                   os.path.join(ROOT, "include", "dsv4topk.h"), os.path.join(ROOT, "include", "dsv4gqa.h"),

@@ -459,7 +459,8 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     const int d = cache->head_dim;
     rc = cache->format == DSV4_GQA_BF16  ? launch_decode_bf16(p, d, pl.nt, stream)
          : cache->format == DSV4_GQA_F16 ? launch_decode_f16(p, d, pl.nt, stream)
-                                         : launch_decode_e4m3(p, d, pl.nt, stream);
+         : p.q_bf16                      ? launch_decode_e4m3(p, d, pl.nt, stream)
+                                         : launch_decode_e4m3_f16(p, d, pl.nt, stream);
     if (rc || p.cluster) return rc;
     if (d == 64)
         rc = pl.tt == 32 ? launch_join<64, 32>(p, pl.nt, stream) : launch_join<64, 64>(p, pl.nt, stream);

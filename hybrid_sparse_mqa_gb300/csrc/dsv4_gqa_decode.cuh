@@ -1,7 +1,7 @@
 // dsv4_gqa_decode.cuh - one-token attention over a paged grouped-query cache
 // (include/dsv4gqa.h states what is computed).  The kernel is a template over
 // the cache's element type, compiled once per type in
-// dsv4_gqa_decode_{bf16,f16,e4m3}.cu; dsv4_gqa_decode.cu holds the host side
+// dsv4_gqa_decode_{bf16,f16,e4m3,e4m3_f16}.cu; dsv4_gqa_decode.cu holds the host side
 // and the kernels that join split requests and accumulate weights.
 //
 // Work: a segment is one (request, KV head, group of up to 8 NT query heads);
@@ -50,12 +50,12 @@
 // and the rounded rest), so its rounding stays below 2^-16 of it and the
 // output's own rounding is what remains; the second MMA costs nothing
 // measurable in a kernel bound by memory.  For e4m3 caches codes are exact in
-// f16 and P is one f16: 2^-12 of it, an eighth of a bf16 output's rounding and
-// as much as an f16 output's.  Pieces of f16 end at 2^-24, which adds 2^-36 of
-// the largest P at most (Shape::DROP).  q beside e4m3 rows is scaled by a power
-// of two per head so that its largest value lies in [2^14, 2^15): a bf16 value
-// keeps all its bits down to 2^-31 of the largest, and below that is off by at
-// most 2^-39 of it.
+// f16, and P is two f16 values where the output is f16, one where it is bf16
+// (Shape::TWO).  Pieces of f16 end at 2^-24, which adds 2^-36 of the largest P
+// at most (Shape::DROP).  q beside e4m3 rows is scaled by a power of two per
+// head so that its largest value lies in [2^14, 2^15): a bf16 value keeps all
+// its bits down to 2^-31 of the largest, and below that is off by at most
+// 2^-39 of it.
 #pragma once
 
 #include "dsv4_gqa.cuh"
@@ -281,12 +281,19 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
 }
 
 // ---------------------------------------------------------------- shape
-// KIND: DSV4_GQA_BF16 / F16 / E4M3.  A warp's stage is TT rows of K and of V.
-template <int KIND_, int D_, int NT_>
+// KIND: DSV4_GQA_BF16 / F16 / E4M3; QKIND: of the queries and the output, BF16
+// or F16.  A warp's stage is TT rows of K and of V.
+template <int KIND_, int QKIND, int D_, int NT_>
 struct Shape {
     static constexpr int KIND = KIND_, D = D_, NT = NT_;
     static constexpr bool FP8 = KIND == DSV4_GQA_E4M3;
     static constexpr bool BF16 = KIND == DSV4_GQA_BF16;      // operand type of the MMAs (e4m3: f16)
+    static constexpr bool QBF16 = QKIND == DSV4_GQA_BF16;
+    static_assert(FP8 || QKIND == KIND, "only e4m3 rows are read by queries of another type");
+    // P in two pieces.  One f16 is off by 2^-12 of it, an eighth of a bf16 output's rounding but as much as an f16
+    // output's: 8 x 1024..16384 e4m3 rows of 128, 32 / 4 heads, f16 out: an error of 5.7e-6 (rms) with one piece and of
+    // 4.3e-6, the output's own rounding, with two
+    static constexpr bool TWO = !FP8 || !QBF16;
     static constexpr int ROWB = D * (FP8 ? 1 : 2);           // bytes of a row
     static constexpr int TT = 4096 / ROWB < 16 ? 16 : 4096 / ROWB;
     static constexpr int MT = TT / 16;                       // 16-slot MMA tiles
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         qf[kk][nt][u] = have ? qr[d2 + u] : 0u;
-                        const float2 f = p.q_bf16 ? unpack2<true>(qf[kk][nt][u]) : unpack2<false>(qf[kk][nt][u]);
+                        const float2 f = unpack2<S::QBF16>(qf[kk][nt][u]);
                         amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
                 }
@@ -724,7 +731,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 for (int kk = 0; kk < DT; ++kk)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const float2 f = p.q_bf16 ? unpack2<true>(qf[kk][nt][u]) : unpack2<false>(qf[kk][nt][u]);
+                        const float2 f = unpack2<S::QBF16>(qf[kk][nt][u]);
                         qf[kk][nt][u] = pack2<false>(f.x * up, f.y * up);
                     }
                 const float mul = p.scale_log2 * kscale * down;
@@ -864,7 +871,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                         lsum[nt][1] += y;
                         const uint32_t w = pack2<S::BF16>(x, y);
                         hi[nt][u] = transpose8x8(w);
-                        if constexpr (!S::FP8) {
+                        if constexpr (S::TWO) {
                             const float2 r = unpack2<S::BF16>(w);
                             lo[nt][u] = transpose8x8(pack2<S::BF16>(x - r.x, y - r.y));
                         }
@@ -910,8 +917,10 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                             const uint32_t a[4] = {e4m3x2_f16x2(x), e4m3x2_hi_f16x2(x), e4m3x2_f16x2(y),
                                                    e4m3x2_hi_f16x2(y)};
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < NT; ++nt) {
                                 mma16816<false>(o[hh * 8 + jj][nt], a, hi[nt][0], hi[nt][1]);
+                                if constexpr (S::TWO) mma16816<false>(o[hh * 8 + jj][nt], a, lo[nt][0], lo[nt][1]);
+                            }
                         }
                     }
                 }
@@ -1030,7 +1039,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 const float inv = any ? vmul * f / l : 0.f;
                 const size_t at = (size_t)here_b * p.heads + head0 + c;
                 *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at * D + d) =
-                    p.q_bf16 ? pack2<true>(x * inv, y * inv) : pack2<false>(x * inv, y * inv);
+                    pack2<S::QBF16>(x * inv, y * inv);
                 if (d == 0 && p.lse) p.lse[at] = any ? (top + log2f(l)) * kLn2 : -INFINITY;
             }
             if (p.w_out) {
@@ -1170,7 +1179,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float x = o[j + i][nt][u] * inv[u], y = o[j + i][nt][u + 2] * inv[u];
-                            w[i] = p.q_bf16 ? pack2<true>(x, y) : pack2<false>(x, y);
+                            w[i] = pack2<S::QBF16>(x, y);
                         }
                         const int d = D == 64 ? 8 * g : 16 * (g + 8 * (j >> 3)) + 2 * (j & 7);
                         *reinterpret_cast<uint4*>(out + (row + c) * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -1181,10 +1190,11 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     }
 }
 
-// The host side of one cache type.
+// The host side of one cache type (and type of queries, where they differ).
 int launch_decode_bf16(const DecodeParams& p, int head_dim, int nt, void* stream);
 int launch_decode_f16(const DecodeParams& p, int head_dim, int nt, void* stream);
 int launch_decode_e4m3(const DecodeParams& p, int head_dim, int nt, void* stream);
+int launch_decode_e4m3_f16(const DecodeParams& p, int head_dim, int nt, void* stream);
 
 template <class S, bool SEG>
 inline int launch_decode_kernel(const DecodeParams& p, unsigned grid, int cluster, void* stream) {
@@ -1211,16 +1221,16 @@ inline int launch_decode_shape(const DecodeParams& p, void* stream) {
     return launch_decode_kernel<S, false>(p, p.warps / S::W + p.claims, 1, stream);
 }
 
-template <int KIND>
+template <int KIND, int QKIND>
 inline int launch_decode_kind(const DecodeParams& p, int head_dim, int nt, void* stream) {
     if (nt == 1) {
-        if (head_dim == 64) return launch_decode_shape<Shape<KIND, 64, 1>>(p, stream);
-        if (head_dim == 128) return launch_decode_shape<Shape<KIND, 128, 1>>(p, stream);
-        return launch_decode_shape<Shape<KIND, 256, 1>>(p, stream);
+        if (head_dim == 64) return launch_decode_shape<Shape<KIND, QKIND, 64, 1>>(p, stream);
+        if (head_dim == 128) return launch_decode_shape<Shape<KIND, QKIND, 128, 1>>(p, stream);
+        return launch_decode_shape<Shape<KIND, QKIND, 256, 1>>(p, stream);
     }
-    if (head_dim == 64) return launch_decode_shape<Shape<KIND, 64, 2>>(p, stream);
-    if (head_dim == 128) return launch_decode_shape<Shape<KIND, 128, 2>>(p, stream);
-    return launch_decode_shape<Shape<KIND, 256, 2>>(p, stream);
+    if (head_dim == 64) return launch_decode_shape<Shape<KIND, QKIND, 64, 2>>(p, stream);
+    if (head_dim == 128) return launch_decode_shape<Shape<KIND, QKIND, 128, 2>>(p, stream);
+    return launch_decode_shape<Shape<KIND, QKIND, 256, 2>>(p, stream);
 }
 
 }  // namespace gqa

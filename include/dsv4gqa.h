@@ -36,6 +36,10 @@
  *     s_j = scale * <q_i, K_j>,  j = lo .. n-1
  *     L   = exp(sink[i]) + sum_j exp(s_j)          (no sink: that term is 0)
  *     out = sum_j exp(s_j) V_j / L       lse = ln L
+ *   Scores, softmax statistics and sums are fp32, products of 16-bit values
+ *   exact; the weight of a row enters its product with V with an error of at
+ *   most 2^-17 of it, or 2^-12 where the cache is E4M3 and out bf16, and 2^-36
+ *   of the largest weight (F16 and E4M3 caches).
  *   A request with no rows gets out = 0 and lse = sink[i] (or -inf).  An
  *   infinite value of an attended V row makes its dim of out infinite (NaN
  *   where both signs or a NaN meet), as the sum does; finite bf16 values must

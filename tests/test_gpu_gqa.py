@@ -343,6 +343,28 @@ def test_decode_of_many_rows_far_below_one(A, kv, q, below, slots, lens):
         assert (lse[b].double().cpu() - math.log(total)).abs().max() <= 2.0 ** -19 + (n / 16 + 64) * 2.0 ** -23 + 2.0 ** -20
 
 
+@pytest.mark.parametrize("scale", [0.71, 0.9, 1.3, 1.7, 2.2])
+@pytest.mark.parametrize("kv,q", [(BF, BF), (HF, HF), (F8, HF)])
+def test_decode_of_values_that_cancel(A, kv, q, scale):
+    # half the rows have the value 1 and half -1, with weights that differ little, so that the rounding of P shows
+    # beside the output's: 2^-17 of the sum of all weights at most (two pieces), while one f16 would leave up to 2^-12
+    c = Case(kv=kv, q=q, hkv=1, dim=64, rows=1, slots=640, seed=3)
+    c.ks = c.vs = None
+    k, v = torch.zeros(c.k.shape), torch.ones(c.v.shape)
+    k[:, :, ::2, 0], k[:, :, 1::2, 0] = 1.0, 0.9375
+    v[:, :, 1::2] = -1.0
+    c.k, c.v = k.to(kv), v.to(kv)
+    query = torch.zeros(1, 8, 64)
+    query[:, :, 0] = 1.0
+    out, _ = A.dsv4_gqa_decode(query.to(q).cuda(), torch.tensor([640], dtype=torch.int32).cuda(), c.handle(A),
+                               scale=scale, max_len=640)
+    x = float(np.float32(scale))
+    ref = (math.exp(x) - math.exp(0.9375 * x)) / (math.exp(x) + math.exp(0.9375 * x))
+    # (sums as above; the scores are exact up to their rounding, 2^-23 of 4 log2 units)
+    tol = 2.0 ** -17 + 2.0 ** -19 + 2.0 ** -20 + (640 / 16 + 64) * 2.0 ** -23 + ref * torch.finfo(q).eps / 2
+    assert float((out.double() - ref).abs().max()) <= tol
+
+
 def test_decode_sinks(A):
     c = Case(rows=3, slots=60, seed=7)
     for value in (-math.inf, -100.0, 0.0, 60.0, math.inf):
