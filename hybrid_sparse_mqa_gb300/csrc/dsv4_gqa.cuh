@@ -122,6 +122,29 @@ inline int launch(void (*kernel)(KA...), dim3 grid, int threads, size_t smem, vo
     return DSV4_OK;
 }
 
+// Loads kernels on the current device.  CUDA does so at a kernel's first launch
+// otherwise, which a stream that is being captured does not take.
+template <class... K>
+inline bool load_kernels(K... kernels) {
+    cudaFuncAttributes a;
+    return ((cudaFuncGetAttributes(&a, kernels) == cudaSuccess) && ...);
+}
+
+// prepare() where the current device's bit of `ready` is not set yet (two
+// threads at once may both do it).
+template <class F>
+inline int once_per_device(unsigned long long& ready, F&& prepare) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSV4_ERR_CUDA;
+    if (__atomic_load_n(&ready, __ATOMIC_ACQUIRE) >> dev & 1) return DSV4_OK;
+    if (!prepare()) {
+        cudaGetLastError();
+        return DSV4_ERR_CUDA;
+    }
+    __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELEASE);
+    return DSV4_OK;
+}
+
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -382,6 +382,26 @@ int launch_weights(const DecodeParams& p, int nt, void* stream) {
                    : launch(dsv4_gqa_weight_kernel<TT, 16>, grid, kWeightThreads, 0, stream, 1, p);
 }
 
+template <int D, int TT, int HEADS>
+bool load_join_heads() {
+    return load_kernels(dsv4_gqa_join_kernel<D, TT, HEADS, 16, D / 32>, dsv4_gqa_join_kernel<D, TT, HEADS, 16, 1>,
+                        dsv4_gqa_join_kernel<D, TT, HEADS, 8, 1>, dsv4_gqa_join_kernel<D, TT, HEADS, 1, 1>,
+                        dsv4_gqa_weight_kernel<TT, HEADS>);
+}
+
+// Every kernel behind the attention kernel for rows of this size, at the first call with such rows (one that takes a
+// cluster per segment too).
+template <int D, int TT>
+int load_join() {
+    static unsigned long long ready = 0;
+    return once_per_device(ready, [] { return load_join_heads<D, TT, 8>() && load_join_heads<D, TT, 16>(); });
+}
+int load_joins(int d, int tt) {
+    if (d == 64) return tt == 32 ? load_join<64, 32>() : load_join<64, 64>();
+    if (d == 128) return tt == 16 ? load_join<128, 16>() : load_join<128, 32>();
+    return load_join<256, 16>();
+}
+
 }  // namespace
 }  // namespace gqa
 }  // namespace dsv4
@@ -457,6 +477,8 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     p.err = err;
 
     const int d = cache->head_dim;
+    rc = load_joins(d, pl.tt);
+    if (rc) return rc;
     rc = cache->format == DSV4_GQA_BF16  ? launch_decode_bf16(p, d, pl.nt, stream)
          : cache->format == DSV4_GQA_F16 ? launch_decode_f16(p, d, pl.nt, stream)
          : p.q_bf16                      ? launch_decode_e4m3(p, d, pl.nt, stream)

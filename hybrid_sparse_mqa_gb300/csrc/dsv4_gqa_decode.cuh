@@ -1196,41 +1196,40 @@ int launch_decode_f16(const DecodeParams& p, int head_dim, int nt, void* stream)
 int launch_decode_e4m3(const DecodeParams& p, int head_dim, int nt, void* stream);
 int launch_decode_e4m3_f16(const DecodeParams& p, int head_dim, int nt, void* stream);
 
-template <class S, bool SEG>
-inline int launch_decode_kernel(const DecodeParams& p, unsigned grid, int cluster, void* stream) {
-    // shared memory beyond 48 KB is asked for once per device
-    static unsigned long long ready = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return DSV4_ERR_CUDA;
-    if (dev < 0 || dev >= 64) return DSV4_ERR_CUDA;
-    if (!(__atomic_load_n(&ready, __ATOMIC_ACQUIRE) >> dev & 1)) {
-        if (cudaFuncSetAttribute(dsv4_gqa_decode_kernel<S, SEG>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) !=
-            cudaSuccess) {
-            cudaGetLastError();
-            return DSV4_ERR_CUDA;
-        }
-        __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELEASE);
-    }
-    return launch(dsv4_gqa_decode_kernel<S, SEG>, dim3(grid), S::W * 32, S::SMEM, stream, cluster, p);
-}
-
 template <class S>
 inline int launch_decode_shape(const DecodeParams& p, void* stream) {
     if (p.cluster)
-        return launch_decode_kernel<S, true>(p, p.batch * p.c.kv_heads * p.chunks * p.cluster, p.cluster, stream);
-    return launch_decode_kernel<S, false>(p, p.warps / S::W + p.claims, 1, stream);
+        return launch(dsv4_gqa_decode_kernel<S, true>, dim3(p.batch * p.c.kv_heads * p.chunks * p.cluster), S::W * 32,
+                      S::SMEM, stream, p.cluster, p);
+    return launch(dsv4_gqa_decode_kernel<S, false>, dim3(p.warps / S::W + p.claims), S::W * 32, S::SMEM, stream, 1, p);
+}
+
+// shared memory beyond 48 KB is asked for once (which loads the kernel)
+template <class S>
+inline bool prepare_decode_shape() {
+    return cudaFuncSetAttribute(dsv4_gqa_decode_kernel<S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) ==
+               cudaSuccess &&
+           cudaFuncSetAttribute(dsv4_gqa_decode_kernel<S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) ==
+               cudaSuccess &&
+           load_kernels(dsv4_gqa_decode_kernel<S, false>, dsv4_gqa_decode_kernel<S, true>);
+}
+
+template <int KIND, int QKIND, int D>
+inline int launch_decode_dim(const DecodeParams& p, int nt, void* stream) {
+    static unsigned long long ready = 0;
+    const int rc = once_per_device(ready, [] {
+        return prepare_decode_shape<Shape<KIND, QKIND, D, 1>>() && prepare_decode_shape<Shape<KIND, QKIND, D, 2>>();
+    });
+    if (rc) return rc;
+    return nt == 1 ? launch_decode_shape<Shape<KIND, QKIND, D, 1>>(p, stream)
+                   : launch_decode_shape<Shape<KIND, QKIND, D, 2>>(p, stream);
 }
 
 template <int KIND, int QKIND>
 inline int launch_decode_kind(const DecodeParams& p, int head_dim, int nt, void* stream) {
-    if (nt == 1) {
-        if (head_dim == 64) return launch_decode_shape<Shape<KIND, QKIND, 64, 1>>(p, stream);
-        if (head_dim == 128) return launch_decode_shape<Shape<KIND, QKIND, 128, 1>>(p, stream);
-        return launch_decode_shape<Shape<KIND, QKIND, 256, 1>>(p, stream);
-    }
-    if (head_dim == 64) return launch_decode_shape<Shape<KIND, QKIND, 64, 2>>(p, stream);
-    if (head_dim == 128) return launch_decode_shape<Shape<KIND, QKIND, 128, 2>>(p, stream);
-    return launch_decode_shape<Shape<KIND, QKIND, 256, 2>>(p, stream);
+    if (head_dim == 64) return launch_decode_dim<KIND, QKIND, 64>(p, nt, stream);
+    if (head_dim == 128) return launch_decode_dim<KIND, QKIND, 128>(p, nt, stream);
+    return launch_decode_dim<KIND, QKIND, 256>(p, nt, stream);
 }
 
 }  // namespace gqa

@@ -630,6 +630,20 @@ int launch_select(const EvictParams& p, void* stream) {
     }
 }
 
+template <int CLUSTER>
+bool load_select_cluster() {
+    return load_kernels(dsv4_gqa_select_kernel<512, 16, CLUSTER>, dsv4_gqa_select_kernel<512, 32, CLUSTER>,
+                        dsv4_gqa_select_kernel<512, 64, CLUSTER>);
+}
+int load_all() {
+    static unsigned long long ready = 0;
+    return once_per_device(ready, [] {
+        return load_select_cluster<1>() && load_select_cluster<2>() && load_select_cluster<4>() && load_select_cluster<8>() &&
+               load_kernels(dsv4_gqa_select_kernel<256, 16, 1>, dsv4_gqa_select_kernel<512, 0, 8>, dsv4_gqa_move_kernel<8>,
+                            dsv4_gqa_move_kernel<16>, dsv4_gqa_move_kernel<32>, dsv4_gqa_move_kernel<64>);
+    });
+}
+
 }  // namespace
 }  // namespace gqa
 }  // namespace dsv4
@@ -684,7 +698,9 @@ int dsv4_gqa_evict(int32_t batch, const int32_t* lens, const int32_t* seq_lens, 
     // the move kernel does)
     auto apart = [&](const int* x) { return !x || lens_out + batch <= x || x + batch <= lens_out; };
     p.alone = max_len - keep <= kFew && max_len <= kHeldKeys && apart(lens) && apart(seq_lens);
-    const int r = launch_select(p, stream);
+    int r = load_all();
+    if (r) return r;
+    r = launch_select(p, stream);
     if (r || p.alone) return r;
     switch (p.row_pieces) {
         case 4: return launch_move<8>(p, stream);

@@ -213,6 +213,18 @@ int launch_store(const StoreParams& p, int head_dim, void* stream) {
     return launch(dsv4_gqa_store_kernel<TYPE, PACK, 16>, grid, kStoreThreads, 0, stream, 1, p);
 }
 
+template <int TYPE, bool PACK>
+bool load_store() {
+    return load_kernels(dsv4_gqa_store_kernel<TYPE, PACK, 4>, dsv4_gqa_store_kernel<TYPE, PACK, 8>,
+                        dsv4_gqa_store_kernel<TYPE, PACK, 16>);
+}
+int load_all() {
+    static unsigned long long ready = 0;
+    return once_per_device(ready, [] {
+        return load_store<DSV4_GQA_BF16, false>() && load_store<DSV4_GQA_BF16, true>() && load_store<DSV4_GQA_F16, true>();
+    });
+}
+
 }  // namespace
 }  // namespace gqa
 }  // namespace dsv4
@@ -224,7 +236,7 @@ extern "C" int dsv4_gqa_store(const void* k, int64_t k_token_stride, int64_t k_h
                               void* stream) {
     using namespace dsv4;
     using namespace dsv4::gqa;
-    const int rc = check_cache(cache);
+    int rc = check_cache(cache);
     if (rc) return rc;
     if (n < 0 || n > kMostSlots) return DSV4_ERR_INVALID;
     if (type != DSV4_GQA_BF16 && type != DSV4_GQA_F16) return DSV4_ERR_UNSUPPORTED;
@@ -252,6 +264,8 @@ extern "C" int dsv4_gqa_store(const void* k, int64_t k_token_stride, int64_t k_h
     p.width = weights || positions ? width : INT64_MAX;
     p.token_positions = token_positions;
     p.err = err;
+    rc = load_all();
+    if (rc) return rc;
     const int d = cache->head_dim;
     if (cache->format != DSV4_GQA_E4M3) return launch_store<DSV4_GQA_BF16, false>(p, d, stream);
     return type == DSV4_GQA_BF16 ? launch_store<DSV4_GQA_BF16, true>(p, d, stream)

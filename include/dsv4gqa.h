@@ -81,8 +81,10 @@
  *   is skipped (DSV4_DEV_ERR_STORE_ROW).  DSV4_DEV_ERR_TIMEOUT after a decode
  *   call: a wait inside its kernel was given up (a library bug), and what the
  *   call wrote to its outputs is undefined; later calls are not affected.
- *   Every kernel can be captured into a graph; make the first call of a
- *   function on a device before any capture (its kernels are loaded then).
+ *   Every kernel can be captured into a graph.  Before any capture on a device
+ *   make one call there of each function, and of dsv4_gqa_decode one for each
+ *   cache format, query type and head_dim: it loads every kernel that calls
+ *   of these can take, whatever their sizes and optional arguments.
  *   A captured call reads lens, tables and rows anew at every replay.
  *   lens, seq_lens, req_pool_indices: int32 [batch]; req_pool_indices NULL =
  *   request b is row b.

@@ -14,6 +14,9 @@ The bound on an output is c * sum p|v| + tail + half a step * |out|, with c the
 sum of the relative terms above.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -629,6 +632,63 @@ def test_long_lists_at_once_and_in_graphs(A):
         for (_, res), (_, _, _, want) in zip(graphs, sets):
             assert torch.equal(res[0], want[0]) and torch.equal(res[1], want[1])
     assert A.dsv4_attn_get_device_error() == 0
+
+
+_CAPTURE = """
+import torch
+from hybrid_sparse_mqa_gb300 import attn as A
+BF, F8 = torch.bfloat16, torch.float8_e4m3fn
+gen = torch.Generator(device="cuda").manual_seed(1)
+def rand(*shape):
+    return torch.randn(*shape, generator=gen, device="cuda", dtype=BF)
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+pages, hkv, page, dim = 40, 2, 256, {dim}
+k, v = (rand(pages, hkv, page, dim).to({kv}) for _ in range(2))
+cache = A.make_gqa_cache(k, v, torch.arange(pages, device="cuda", dtype=torch.int32).view(2, 20))
+bits = lambda x: x.view(torch.uint8).clone()
+q, wide, lens = rand(2, 4, dim), rand(2, 32, dim), ints(5000, 4000)
+w, rows = torch.rand(2, hkv, 20 * page, device="cuda"), ints(1, 0)
+new, slots = rand(2, 2 * hkv, dim), ints(5000, 4000)
+calls = dict(
+    long=lambda: A.dsv4_gqa_decode(q, lens, cache),
+    kept=lambda: A.dsv4_gqa_decode(q, lens, cache, weights=w, weights_out=torch.zeros_like(w), req_pool_indices=rows),
+    wide=lambda: A.dsv4_gqa_decode(wide, lens, cache), wide_short=lambda: A.dsv4_gqa_decode(wide, lens, cache, max_len=100),
+    evict=lambda: [A.dsv4_gqa_evict(lens, cache, w, 1000, weights_out=torch.zeros_like(w)), bits(k), bits(v)],
+)
+# one short call of each function, of the forms with the fewest launches, is what was made before the captures
+A.dsv4_gqa_decode(q, ints(3, 2), cache, max_len=100)
+A.dsv4_gqa_store(new[:, :hkv], new[:, hkv:], ints(0, 1), slots, cache)
+A.dsv4_gqa_evict(ints(3, 2), cache, w, 100, max_len=100)
+A.dsv4_attn_get_device_error()
+k0, v0 = bits(k), bits(v)
+graphs = dict()
+for name, call in calls.items():
+    graphs[name] = (torch.cuda.CUDAGraph(), None)
+    with torch.cuda.graph(graphs[name][0]):
+        got = call()
+    graphs[name] = (graphs[name][0], got)
+for name, call in calls.items():
+    for again in range(2):
+        k.view(torch.uint8).copy_(k0), v.view(torch.uint8).copy_(v0)
+        graphs[name][0].replay()
+        torch.cuda.synchronize()
+        first = [x.clone() for x in graphs[name][1]]
+        k.view(torch.uint8).copy_(k0), v.view(torch.uint8).copy_(v0)
+        assert all(torch.equal(x, y) for x, y in zip(first, call())), name
+# (wide_short: lengths above max_len)
+assert A.dsv4_attn_get_device_error() in (0, A.DEV_ERR["GQA_LENGTH"])
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("kv,dim", [("BF", 64), ("BF", 128), ("BF", 256), ("F8", 64), ("F8", 128), ("F8", 256)])
+def test_captures_after_one_call_of_each_function(A, kv, dim):
+    # in a process of its own: what an earlier test has launched is loaded already
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", _CAPTURE.format(kv=kv, dim=dim)], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
 
 
 def test_claims_that_are_given_up(A):
