@@ -586,15 +586,16 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 more = false;
             } else if (!prod.next_segment(p, hcs, p1)) {
                 for (int tries = 0; tail && next_p == -2; ++tries) {
-                    if (tries < p.claim_polls) {
-                        next_p = taken(entry_p + 1);
-                        continue;
+                    if (tries >= p.claim_polls) {
+                        // given up: nobody may compute this warp's part of what the CTA takes over.  But an answer on its
+                        // way to this warp has to land before the CTA may end
+                        if (tries == p.claim_polls && lane == 0) atomicOr(p.err, DSV4_DEV_ERR_TIMEOUT);
+                        if (tries - p.claim_polls >= kWaitLimit || !__shfl_sync(0xffffffffu, sent, 0)) {
+                            next_p = -1;
+                            break;
+                        }
                     }
-                    // given up: nobody computes this warp's part of what the CTA took over.  An answer on its way to
-                    // this warp lands before the CTA may end (and is published to its other warps)
-                    if (lane == 0) atomicOr(p.err, DSV4_DEV_ERR_TIMEOUT);
-                    for (int i = 0; i < kWaitLimit && __shfl_sync(0xffffffffu, sent, 0); ++i) taken(entry_p + 1);
-                    next_p = -1;
+                    next_p = taken(entry_p + 1);
                 }
                 more = next_p >= 0;
                 if (more) {
