@@ -592,6 +592,90 @@ def test_decode_of_long_lists(A, lens):
             assert bool(((wo[b, h, :m].double() - p.sum(0)).abs() <= tw + 1e-12).all())
 
 
+LONG = {
+    # kv, q, head_dim, query heads per KV head, KV heads, page, window, lengths: so many tiles that shares are claimed
+    "e4m3_64": (F8, BF, 64, 4, 8, 256, 0, [400000, 7, 250001]),
+    "e4m3_64_f16": (F8, HF, 64, 10, 8, 64, 0, [350000, 300123]),
+    "e4m3_128": (F8, BF, 128, 8, 8, 128, 0, [170000, 0, 160001]),
+    "e4m3_256_wide": (F8, BF, 256, 16, 4, 256, 0, [200000, 130001]),
+    "bf16_256": (BF, BF, 256, 2, 4, 256, 0, [100000, 1, 70001]),
+    "f16_256_wide": (HF, HF, 256, 12, 2, 1024, 0, [200000, 130001]),
+    "f16_128_groups": (HF, HF, 128, 17, 4, 16, 0, [120000, 50001, 33]),
+    "bf16_64_window": (BF, BF, 64, 1, 16, 32, 5000, [5000 + 150 * i * (i % 3 > 0) + 7 * i for i in range(40)]),
+    "bf16_128_many": (BF, BF, 128, 3, 8, 64, 0, [(9000 + 137 * i) * (i % 7 > 0) for i in range(37)]),
+}
+
+
+@pytest.mark.parametrize("name", sorted(LONG))
+def test_decode_of_long_lists_of_every_shape(A, name):
+    # claimed shares of every type, width and group size, compared with the definition in 64 bits (bounds as above);
+    # with weights and without, bit for bit the same in every call
+    kv, qt, dim, group, hkv, page, window, lens = LONG[name]
+    rows, heads = len(lens), group * hkv
+    row_bytes, fp8 = dim * (1 if kv == F8 else 2), kv == F8
+    tile = max(16, 4096 // row_bytes)
+    chunks = -(-group // (16 if group > 8 else 8))
+    tiles = sum((n - 1) // tile - (max(0, n - window) if window else 0) // tile + 1 for n in lens if n) * hkv * chunks
+    assert tiles >= 64 * 4 * (152 if row_bytes > 256 else 304)          # 64 per resident warp
+    width = -(-max(lens) // page)
+    gen = torch.Generator(device="cuda").manual_seed(len(name))
+    pages = sum(-(-n // page) for n in lens)
+    k, v = (torch.randn(pages, hkv, page, dim, generator=gen, device="cuda", dtype=BF).to(kv) for _ in range(2))
+    order, table, at = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32), [], 0
+    for n in lens:                              # (a table wider than a request's pages names none behind them)
+        mine = order[at: at - (-n // page)]
+        at += mine.numel()
+        table.append(torch.nn.functional.pad(mine, (0, width - mine.numel()), value=-1))
+    table = torch.stack(table)
+    ks, vs = ((0.5 + torch.rand(hkv, generator=gen, device="cuda")) if fp8 else None for _ in range(2))
+    cache = A.make_gqa_cache(k, v, table, k_scale=ks, v_scale=vs)
+    q = torch.randn(rows, heads, dim, generator=gen, device="cuda", dtype=BF).to(qt)
+    sink = torch.randn(heads, generator=gen, device="cuda")
+    n_d = torch.tensor(lens, dtype=torch.int32).cuda()
+    w = torch.zeros(rows, hkv, width * page, device="cuda")
+    got = []
+    for _ in range(3):
+        wo = torch.full_like(w, -1.0)
+        out, lse = A.dsv4_gqa_decode(q, n_d, cache, sink=sink, window=window, weights=w, weights_out=wo)
+        plain = A.dsv4_gqa_decode(q, n_d, cache, sink=sink, window=window)
+        assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
+        got.append((out, lse, wo))
+    assert A.dsv4_attn_get_device_error() == 0
+    for x in got[1:]:
+        assert all(torch.equal(p, r) for p, r in zip(x, got[0]))
+    out, lse, wo = got[0]
+    piece = 2.0 ** -17 if not (fp8 and qt == BF) else 2.0 ** -12
+    for b, m in enumerate(lens):
+        assert bool((wo[b, :, m:] == -1.0).all())
+        lo = max(0, m - window) if window else 0
+        if m == 0:
+            # (lse = sink, by way of log2 units: two fp32 products, 2^-24 each, by factors off by 2^-25 each)
+            assert bool((out[b] == 0).all()) and bool(((lse[b] - sink).abs() <= 2.0 ** -22 * sink.abs()).all())
+            continue
+        for h in range(hkv):
+            here = table[b, : -(-m // page)].long()
+            kk, vv = ((x.view(torch.uint8)[here, h].view(F8) if fp8 else x[here, h]).reshape(-1, dim)[lo:m].double()
+                      for x in (k, v))
+            mine = slice(group * h, group * (h + 1))
+            factor = (float(ks[h]) if fp8 else 1.0) / math.sqrt(dim)
+            vmul = float(vs[h]) if fp8 else 1.0
+            s = q[b, mine].double() @ kk.T * factor
+            mag = float((q[b, mine].double().abs() @ kk.abs().T).max()) * factor
+            ref_lse = torch.logaddexp(torch.logsumexp(s, dim=1), sink[mine].double())
+            p = torch.exp(s - ref_lse[:, None])
+            ref, soft = p @ vv * vmul, p @ vv.abs() * vmul
+            ds, sums = (dim + 8) * 2.0 ** -23 * mag, ((m - lo) / 16 + 64) * 2.0 ** -23
+            tail = 0 if kv == BF else p.max(dim=1, keepdim=True).values * (m - lo) * 2.0 ** -36 * float(vv.abs().max()) * vmul
+            tol = (2 * ds + 2.0 ** -20 + piece + sums) * soft + tail + (torch.finfo(qt).eps / 2 + 2.0 ** -22) * ref.abs()
+            if qt == HF:
+                tol = tol + 2.0 ** -25
+            assert bool(((out[b, mine].double() - ref).abs() <= tol).all())
+            assert float((lse[b, mine].double() - ref_lse).abs().max()) <= ds + sums + 2.0 ** -18
+            tw = p.sum(0) * (2 * ds + 2.0 ** -19 + sums)
+            assert bool(((wo[b, h, lo:m].double() - p.sum(0)).abs() <= tw + 1e-12).all())
+            assert bool((wo[b, h, :lo] == 0).all())
+
+
 def test_long_lists_at_once_and_in_graphs(A):
     # two calls with claims on two streams: each grid's CTAs come and go as the other leaves room, so a CTA may take
     # over one that would have been resident; results stay bit for bit those of a call alone
