@@ -14,8 +14,12 @@ namespace {
 constexpr int kWeightThreads = 256;
 constexpr int kWeightSlots = 4;            // slots per thread
 // Tiles per share at least: 1 where no segment has more than kFewTiles, else 2.
-// (One request, 8 KV heads: 333 rows 6.7 us with 1 and 7.7 with 2, 1000 rows
-// 8.6 and 8.3, 3000 rows 11.3 and 9.6, the difference being the pieces to join.)
+// Lists as short as that are shared out only for calls with weights that name
+// request rows or have more than 16 heads per KV head (all others take a
+// cluster per segment).  us with 1 and with 2, weights and rows named: 1 x 8 KV
+// heads of 100 rows 8.1 and 9.6, of 333 8.9 and 9.8, of 512 9.25 and 9.4; 8 x
+// 512 12.3 and 12.0; 64 x 512 34.9 and 34.8; one KV head of 64 heads, 333 rows,
+// 11.1 and 12.9.
 constexpr int kFewTiles = 32;
 
 // Joins the pieces of cut segments.  With M = max_i m_i,
