@@ -17,9 +17,9 @@ include/dsv4kvstore.h (the cache write before the step):
   dsv4_kv_store;
 include/dsv4topk.h (the top-k selection that makes the C4 index lists):
   dsv4_topk, dsv4_topk_max_length;
-and include/dsv4gqa.h (the cache of the grouped-query model that drafts the
-tokens dsv4_attn_verify checks: its write, its one-token attention and the
-eviction of its rows):
+and include/dsv4gqa.h (the cache of a grouped-query model, such as a separate
+one that drafts the tokens dsv4_attn_verify checks: its write, its one-token
+attention and the eviction of its rows):
   make_gqa_cache, dsv4_gqa_store, dsv4_gqa_decode, dsv4_gqa_evict,
   dsv4_gqa_decode_workspace_size, dsv4_gqa_evict_workspace_size.
 """
@@ -510,7 +510,9 @@ def dsv4_gqa_decode(q, lens, cache, *, sink=None, scale=None, window=0, max_len=
     [batch, heads, head_dim] (bf16 or f16; a slice of a wider projection is
     fine), lens int32 [batch].  Returns (out, lse).  With weights (fp32
     [request rows, KV heads, width]) every cached row's weight is accumulated
-    into weights_out, by default in place."""
+    into weights_out, by default in place.  max_len: a bound on lens, by default
+    every slot of the page table; the smaller, the fewer launches and (with
+    weights) the smaller the workspace."""
     index = cache._index
     type_ = _gqa_type(q, cache)
     if q.dim() != 3 or q.get_device() != index:
@@ -579,7 +581,9 @@ def dsv4_gqa_evict(lens, cache, weights, keep, *, seq_lens=None, positions=None,
     that stay but stand behind the bound move into the freed slots, with their
     weights and positions (in place unless weights_out / positions_out are
     given).  Returns lens_out (a new tensor unless given; may be lens
-    or seq_lens)."""
+    or seq_lens).  max_len: a bound on lens, by default every slot there is; one
+    launch does it all where max_len - keep <= 4 and lens_out is a tensor of its
+    own."""
     index = cache._index
     batch = lens.numel()
     _need(lens, "lens", torch.int32, batch, index)

@@ -3,12 +3,13 @@
  * one-token attention and the eviction of a paged cache with separate K and V
  * rows.
  *
- * dsv4_attn_verify (dsv4attn.h) checks draft tokens against the DeepSeek-V4
- * cache, whose 512-wide rows are key and value at once.  The model that
- * drafts those tokens has ordinary grouped-query heads: num_kv_heads heads
+ * They serve a model with ordinary grouped-query heads (num_kv_heads heads
  * with K and V rows of head_dim values, each shared by num_heads /
- * num_kv_heads query heads.  These operators are its decode step.  They have
- * no counterpart on the source pages.
+ * num_kv_heads query heads) beside the one that dsv4attn.h serves, for
+ * instance a separate model that drafts tokens for dsv4_attn_verify.  The
+ * DeepSeek-V4 caches, whose 512-wide rows are key and value at once (those of
+ * its own draft layer too), stay with the kernels of dsv4attn.h.  These
+ * operators have no counterpart on the source pages.
  *
  * The cache (dsv4_gqa_cache)
  *   Slot s of request row r lies on physical page
@@ -91,7 +92,16 @@
  *   weights (fp32) and positions (int32): [page_table_rows, num_kv_heads,
  *   width], width >= max_len.
  *   max_len: bound on lens; at most page_table_width * page_size and 2^30.  It
- *   sizes launches and workspaces.
+ *   sizes launches and workspaces and chooses between them, so give the
+ *   smallest that is known: a decode call whose max_len is short takes one
+ *   launch, an eviction does where max_len - keep <= 4 (and lens_out is neither
+ *   lens nor seq_lens), and the workspace of a decode call with weights has 32
+ *   to 256 bytes for each slot up to max_len of each request and KV head.
+ *   Limits, beyond which a call returns DSV4_ERR_UNSUPPORTED: batch *
+ *   num_kv_heads of an eviction or of a decode call with weights is at most
+ *   65535; requests * KV heads * groups of up to 16 query heads of a decode
+ *   call is at most 2^30, and times the tiles of max_len slots (at least 16
+ *   slots each) less than 2^31.
  *   workspace: device scratch of at least the size that the matching
  *   _workspace_size function gives, 16-byte aligned; need not be initialised
  *   and holds nothing between calls.  Calls that may run at the same time
