@@ -302,7 +302,8 @@ struct Shape {
     // The reference of a softmax lies DROP below the largest score when it moves, and moves when a score exceeds that
     // score by more than SLACK (log2 units).  P as f16 ends at 2^-24, so it is kept as large as f16 allows: its largest
     // values lie in [2^11, 2^15], and rounding to zero or to subnormals is off by at most 2^-25 2^-DROP = 2^-36 of the
-    // largest.  (bf16 has the exponents of fp32 and does without.)
+    // largest.  (bf16 has the exponents of fp32 and does without.)  Both are added with the rounding that keeps P in that
+    // range where scores are so large that fp32 holds them 2 units apart or more.
     static constexpr float DROP = BF16 ? 0.f : 11.f, SLACK = BF16 ? 8.f : 4.f;
     static constexpr int W = kWarps;
     static constexpr int TILE_BYTES = TT * ROWB;             // K or V of a stage
@@ -832,7 +833,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                             if (slot < cons.rg.lo || slot >= cons.rg.n || !((okm >> m) & 1)) x = -INFINITY;
                         }
                         s[m][nt][c] = x;
-                        above |= x > mref[nt][c & 1] + (S::DROP + S::SLACK);
+                        above |= x > __fadd_rd(mref[nt][c & 1], S::DROP + S::SLACK);
                     }
             if (p.logits) {
                 float* to = p.logits + (size_t)tile * TT * HEADS;
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        mx = fmaxf(mref[nt][u], mx - S::DROP);
+                        mx = fmaxf(mref[nt][u], __fsub_ru(mx, S::DROP));
                         const float f = fast_exp2(mref[nt][u] - mx);
                         mref[nt][u] = mx;
                         lsum[nt][u] *= f;

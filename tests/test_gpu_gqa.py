@@ -368,6 +368,45 @@ def test_decode_of_values_that_cancel(A, kv, q, scale):
     assert float((out.double() - ref).abs().max()) <= tol
 
 
+@pytest.mark.parametrize("kv,q", [(BF, BF), (HF, HF), (F8, BF), (F8, HF)])
+@pytest.mark.parametrize("step", [1, 2, 4, 8, 16, 32])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_decode_of_scores_whose_spacing_is_coarse(A, kv, q, step, sign):
+    # scores of step * (2^23 + i) log2 units, exact in fp32 and `step` apart, rising by one from tile to tile: what is
+    # added to or taken from such a score is rounded to that spacing too
+    c = Case(kv=kv, q=q, hkv=1, dim=64, rows=1, slots=400, seed=step)
+    c.ks = c.vs = None
+    i = (torch.arange(400) // 48).float()                    # i = 0 .. 8
+    query = torch.zeros(1, 8, 64)
+    query[:, :, 0], query[:, :, 1] = 2.0 ** 15, 1.0
+    k = torch.zeros(400, 64)
+    k[:, 0], k[:, 1] = sign * 256.0, i
+    pages = c.table[0].long()
+    kk = c.k.float()
+    kk[pages] = k.view(-1, 16, 64)[:, None]
+    c.k = kk.to(kv)
+    assert torch.equal(c.k.float()[pages, 0].view(400, 64), k)
+    log2e = np.float32(1.4426950408889634)
+    scale = np.float32(step / 1.4426950408889634)
+    near = [np.nextafter(scale, np.float32(0)), scale, np.nextafter(scale, np.float32(1e9))]
+    scale = float([x for x in near if np.float32(x * log2e) == step][0])
+    v = c.v.double()[pages, 0].view(400, 64)
+    cache, n, w = c.handle(A), torch.tensor([400], dtype=torch.int32).cuda(), torch.zeros(1, 1, 400).cuda()
+    p = torch.exp2(step * (i - i.max()).double())
+    p /= p.sum()
+    # (2^x: 2^-20, sums of 400 rows, pieces of P; a weight below 2^-36 of the largest may be lost beside f16)
+    rel = 2.0 ** -20 + (400 / 16 + 64) * 2.0 ** -23 + (2.0 ** -12 if kv == F8 and q == BF else 2.0 ** -17)
+    tol = (p @ v.abs()) * rel + (p @ v).abs() * (torch.finfo(q).eps / 2 + 2.0 ** -22) + \
+        400 * 2.0 ** -36 * v.abs().max() + (2.0 ** -25 if q == HF else 0)
+    for kw in ({}, {"weights": w, "req_pool_indices": torch.zeros(1, dtype=torch.int32).cuda()}):
+        out, lse = A.dsv4_gqa_decode(query.to(q).cuda(), n, cache, scale=scale, max_len=400, **kw)
+        assert ((out[0].double().cpu() - p @ v).abs() <= tol).all()
+        assert float((lse.double().cpu() / (sign * step * 2.0 ** 23 * math.log(2)) - 1).abs().max()) <= 2.0 ** -19
+    # (no bound on the weights: they are 2^(score - lse), and an fp32 lse of this size is rounded to the same spacing,
+    # which is a factor of up to 2^(step / 2))
+    assert A.dsv4_attn_get_device_error() == 0
+
+
 def test_decode_sinks(A):
     c = Case(rows=3, slots=60, seed=7)
     for value in (-math.inf, -100.0, 0.0, 60.0, math.inf):
