@@ -70,6 +70,20 @@ inline Cache device_cache(const dsv4_gqa_cache* c) {
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// [a, a + na) and [b, b + nb) bytes have none in common (null: nothing there).
+inline bool apart(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return !a || !b || x + na <= y || y + nb <= x;
+}
+
+// An array and what replaces it: one and the same, or apart.
+inline bool same_or_apart(const void* a, const void* b, size_t n) { return a == b || apart(a, n, b, n); }
+
+// Bytes of a [request rows, KV heads, width] array of 4-byte entries.
+inline size_t row_array_bytes(const dsv4_gqa_cache* c, int64_t width) {
+    return size_t(c->page_table_rows) * c->num_kv_heads * width * 4;
+}
+
 // DSV4_OK, DSV4_ERR_INVALID or DSV4_ERR_UNSUPPORTED.
 inline int check_cache(const dsv4_gqa_cache* c) {
     if (!c || !c->k || !c->v || !c->page_table || !aligned16(c->k) || !aligned16(c->v)) return DSV4_ERR_INVALID;

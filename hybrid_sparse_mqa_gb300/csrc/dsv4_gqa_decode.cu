@@ -437,6 +437,7 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     if (cache->format != DSV4_GQA_E4M3 && cache->format != type) return DSV4_ERR_UNSUPPORTED;
     if (!q || !out || !lens || !aligned16(q) || !aligned16(out) || q_stride % 8 || window < 0) return DSV4_ERR_INVALID;
     if (!weights != !weights_out || (weights && width < max_len)) return DSV4_ERR_INVALID;
+    if (weights && !same_or_apart(weights, weights_out, row_array_bytes(cache, width))) return DSV4_ERR_INVALID;
     // the weight kernel's grid holds (request, KV head) in its y dimension
     if (weights && (long long)batch * cache->num_kv_heads > 65535) return DSV4_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < pl.bytes) return DSV4_ERR_WORKSPACE;

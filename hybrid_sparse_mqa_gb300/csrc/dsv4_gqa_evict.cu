@@ -666,6 +666,11 @@ int dsv4_gqa_evict(int32_t batch, const int32_t* lens, const int32_t* seq_lens, 
     if (rc) return rc;
     if (!lens || !lens_out || !weights || !weights_out || !positions != !positions_out) return DSV4_ERR_INVALID;
     if (first < 0 || recent < 0 || first > keep || recent > keep - first || width < max_len) return DSV4_ERR_INVALID;
+    const size_t list = size_t(batch) * sizeof(int), entries = row_array_bytes(cache, width);
+    if (!same_or_apart(weights, weights_out, entries) || !same_or_apart(positions, positions_out, entries) ||
+        !same_or_apart(lens, lens_out, list) || !same_or_apart(seq_lens, lens_out, list) ||
+        !apart(req_pool_indices, list, lens_out, list))
+        return DSV4_ERR_INVALID;
     if (!workspace || workspace_bytes < l.bytes) return DSV4_ERR_WORKSPACE;
     if (!aligned16(workspace)) return DSV4_ERR_INVALID;
     unsigned int* err = device_error_word();
@@ -696,8 +701,7 @@ int dsv4_gqa_evict(int32_t batch, const int32_t* lens, const int32_t* seq_lens, 
 
     // (new lengths that replace the old ones, or the tokens seen, have to wait for every head's CTA to have read those:
     // the move kernel does)
-    auto apart = [&](const int* x) { return !x || lens_out + batch <= x || x + batch <= lens_out; };
-    p.alone = max_len - keep <= kFew && max_len <= kHeldKeys && apart(lens) && apart(seq_lens);
+    p.alone = max_len - keep <= kFew && max_len <= kHeldKeys && lens != lens_out && seq_lens != lens_out;
     int r = load_all();
     if (r) return r;
     r = launch_select(p, stream);

@@ -163,7 +163,7 @@ int dsv4_gqa_store(const void* k, int64_t k_token_stride, int64_t k_head_stride,
    contiguous, 16-byte aligned.  sink fp32 [num_heads] or NULL; lse fp32
    [batch, num_heads] or NULL.  num_heads is a multiple of num_kv_heads, at
    most 64 times it.  weights and weights_out: both or neither; they may be
-   the same array. */
+   the same array, but not overlap otherwise. */
 int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch, int32_t num_heads,
                     const int32_t* lens, const int32_t* req_pool_indices,
                     const dsv4_gqa_cache* cache, int32_t window, int32_t max_len,
@@ -179,7 +179,7 @@ size_t dsv4_gqa_decode_workspace_size(const dsv4_gqa_cache* cache, int32_t batch
 /* keep >= 1, first >= 0, recent >= 0, first + recent <= keep.  seq_lens:
    tokens that each request has seen (NULL: as many as it has rows).
    positions and positions_out: both or neither.  lens_out may be lens
-   or seq_lens. */
+   or seq_lens.  Arrays that overlap otherwise are refused. */
 int dsv4_gqa_evict(int32_t batch, const int32_t* lens, const int32_t* seq_lens,
                    const int32_t* req_pool_indices, const dsv4_gqa_cache* cache, int32_t max_len,
                    int32_t keep, int32_t first, int32_t recent,

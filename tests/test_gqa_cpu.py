@@ -109,6 +109,26 @@ EVICT_REFUSALS = [
 ]
 
 
+OVERLAPS = [      # of arrays of 4 x 4 x 128 entries and of 4 lengths
+    (dict(weights_out=4096 + 4), -1), (dict(weights=1 << 20, weights_out=(1 << 20) - 4 * 2047), -1), (dict(weights_out=4096 + 4 * 2048, ws=None), -3),
+    (dict(positions=1 << 20, positions_out=(1 << 20) + 8), -1), (dict(lens_out=4096 + 4), -1), (dict(lens_out=4096 - 12), -1),
+    (dict(lens_out=4096 + 16, ws=None), -3), (dict(seen=4096 * 2, lens_out=4096 * 2 + 4), -1),
+    (dict(seen=4096 * 2, lens_out=4096 * 2, ws=None), -3), (dict(req=4096 * 2, lens_out=4096 * 2), -1),
+    (dict(req=4096 * 2, lens_out=4096 * 2 + 16, ws=None), -3),
+]
+
+
+@pytest.mark.parametrize("args,want", OVERLAPS)
+def test_evict_refuses_arrays_that_overlap(A, args, want):
+    assert _evict(A, ctypes.addressof(_cache(A)), **args) == want
+
+
+def test_decode_refuses_weights_that_overlap(A):
+    c = ctypes.addressof(_cache(A))
+    for shift, want in ((4, -1), (-4 * 2047, -1), (0, -3), (4 * 2048, -3)):
+        assert _decode(A, c, weights=1 << 20, weights_out=(1 << 20) + shift, width=128, ws=None) == want
+
+
 @pytest.mark.parametrize("args,want", EVICT_REFUSALS)
 def test_evict_refusals(A, args, want):
     assert _evict(A, ctypes.addressof(_cache(A)), **args) == want
