@@ -18,9 +18,9 @@ include/dsv4kvstore.h (the cache write before the step):
 include/dsv4topk.h (the top-k selection that makes the C4 index lists):
   dsv4_topk, dsv4_topk_max_length;
 and include/dsv4gqa.h (the cache of a grouped-query model, such as a separate
-one that drafts the tokens dsv4_attn_verify checks: its write, its one-token
-attention and the eviction of its rows):
-  make_gqa_cache, dsv4_gqa_store, dsv4_gqa_decode, dsv4_gqa_evict,
+one that drafts the tokens dsv4_attn_verify checks: its write, the reading back
+of its rows, its one-token attention and the eviction of its rows):
+  make_gqa_cache, dsv4_gqa_store, dsv4_gqa_load, dsv4_gqa_decode, dsv4_gqa_evict,
   dsv4_gqa_decode_workspace_size, dsv4_gqa_evict_workspace_size.
 """
 from __future__ import annotations
@@ -39,17 +39,18 @@ DSV4_KV_FP8_PACKED = 1
 DSV4_GQA_BF16 = 0
 DSV4_GQA_F16 = 1
 DSV4_GQA_E4M3 = 2
+DSV4_GQA_E2M1 = 4
 DEV_ERR = {
     "SWA_PAGE": 0x01, "EXTRA_PAGE": 0x02, "INDEX_RANGE": 0x04, "POSITION": 0x08,
     "PLAN": 0x10, "TIMEOUT": 0x20, "REQ_ROW": 0x40, "STORE_ROW": 0x80, "TOPK_LENGTH": 0x100,
-    "GQA_PAGE": 0x200, "GQA_LENGTH": 0x400,
+    "GQA_PAGE": 0x200, "GQA_LENGTH": 0x400, "LOAD_ROW": 0x800,
 }
 EXPORTED = [
     "dsv4_attn_swa", "dsv4_attn_c4_sparse", "dsv4_attn_c128_dense", "dsv4_attn_verify",
     "dsv4_attn_plan", "dsv4_attn_workspace_size", "dsv4_attn_get_device_error",
     "dsv4_attn_strerror", "dsv4_attn_c4_sparse_noalloc", "dsv4_kv_store",
     "dsv4_topk", "dsv4_topk_max_length",
-    "dsv4_gqa_store", "dsv4_gqa_decode", "dsv4_gqa_decode_workspace_size", "dsv4_gqa_evict",
+    "dsv4_gqa_store", "dsv4_gqa_load", "dsv4_gqa_decode", "dsv4_gqa_decode_workspace_size", "dsv4_gqa_evict",
     "dsv4_gqa_evict_workspace_size",
 ]
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -86,6 +87,11 @@ class GqaCache(ctypes.Structure):
         ("format", ctypes.c_int32),
         ("k_scale", ctypes.c_void_p),
         ("v_scale", ctypes.c_void_p),
+        ("k_blocks", ctypes.c_void_p),
+        ("v_blocks", ctypes.c_void_p),
+        ("block_page_stride", ctypes.c_int64),
+        ("block_head_stride", ctypes.c_int64),
+        ("block_row_stride", ctypes.c_int64),
     ]
 
 
@@ -125,10 +131,11 @@ def load_library(path=LIB_PATH):
     lib.dsv4_topk_max_length.restype = I32
     I64, PG = ctypes.c_int64, ctypes.c_void_p
     lib.dsv4_gqa_store.argtypes = [P, I64, I64, P, I64, I64, I32, I32, P, P, PG, P, P, I64, P, P]
+    lib.dsv4_gqa_load.argtypes = [P, P, I32, PG, P, I64, I64, P, I64, I64, I32, P]
     lib.dsv4_gqa_decode.argtypes = [P, I64, I32, I32, I32, P, P, PG, I32, I32, P, F32, P, P, I64, F32,
                                     P, P, P, SZ, P]
     lib.dsv4_gqa_evict.argtypes = [I32, P, P, P, PG, I32, I32, I32, I32, P, P, P, P, I64, P, P, SZ, P]
-    for name in ("dsv4_gqa_store", "dsv4_gqa_decode", "dsv4_gqa_evict"):
+    for name in ("dsv4_gqa_store", "dsv4_gqa_load", "dsv4_gqa_decode", "dsv4_gqa_evict"):
         getattr(lib, name).restype = ctypes.c_int
     lib.dsv4_gqa_decode_workspace_size.argtypes = [PG, I32, I32, I32, I32]
     lib.dsv4_gqa_decode_workspace_size.restype = SZ
@@ -356,18 +363,26 @@ def dsv4_topk(scores, lengths, k, *, max_length=None, out=None, stream=None):
 
 
 # ---------------------------------------------------------------- the grouped-query cache
-_GQA_TYPES = {torch.bfloat16: DSV4_GQA_BF16, torch.float16: DSV4_GQA_F16, torch.float8_e4m3fn: DSV4_GQA_E4M3}
+_GQA_TYPES = {torch.bfloat16: DSV4_GQA_BF16, torch.float16: DSV4_GQA_F16, torch.float8_e4m3fn: DSV4_GQA_E4M3,
+              torch.uint8: DSV4_GQA_E2M1, torch.float4_e2m1fn_x2: DSV4_GQA_E2M1}
+_GQA_CODES = (DSV4_GQA_E4M3, DSV4_GQA_E2M1)
 
 
-def make_gqa_cache(k_pages, v_pages, page_table, *, k_scale=None, v_scale=None):
+def make_gqa_cache(k_pages, v_pages, page_table, *, k_scale=None, v_scale=None, k_blocks=None, v_blocks=None):
     """dsv4_gqa_cache for K and V pools [pages, KV heads, page_size, head_dim]
     (bf16, f16 or float8_e4m3fn; any strides whose rows are contiguous, so
     token-major pages are passed as pages.transpose(1, 2)) and their int32
-    page table [request rows, logical pages].  k_scale, v_scale: fp32
-    [KV heads] of an e4m3 cache.  Keep the descriptor as long as the pools:
-    building it costs more than passing it."""
+    page table [request rows, logical pages].  A 4-bit cache has pools
+    [pages, KV heads, page_size, head_dim / 2] of bytes (uint8 or
+    float4_e2m1fn_x2), two codes each, and float8_e4m3fn pools k_blocks,
+    v_blocks [pages, KV heads, page_size, head_dim / 16] with a scale for every
+    16 codes (any strides whose rows are contiguous).  k_scale, v_scale: fp32
+    [KV heads] of an e4m3 or 4-bit cache.  Keep the descriptor as long as the
+    pools: building it costs more than passing it."""
     if k_pages.dim() != 4 or k_pages.dtype not in _GQA_TYPES:
-        raise Dsv4Error("k_pages must be a [pages, KV heads, page_size, head_dim] tensor of bf16, f16 or float8_e4m3fn")
+        raise Dsv4Error("k_pages must be a [pages, KV heads, page_size, head_dim] tensor of bf16, f16 or float8_e4m3fn, "
+                        "or [pages, KV heads, page_size, head_dim / 2] bytes of 4-bit codes")
+    format_ = _GQA_TYPES[k_pages.dtype]
     if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or v_pages.stride() != k_pages.stride():
         raise Dsv4Error("v_pages must have the shape, type and strides of k_pages")
     if k_pages.stride(3) != 1:
@@ -375,14 +390,24 @@ def make_gqa_cache(k_pages, v_pages, page_table, *, k_scale=None, v_scale=None):
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
         raise Dsv4Error("page_table must be an int32 [request rows, logical pages] tensor with contiguous rows")
     pages, heads, page_size, dim = k_pages.shape
+    if format_ == DSV4_GQA_E2M1:
+        dim *= 2
+        shape = (pages, heads, page_size, dim // 16)
+        for name, x in (("k_blocks", k_blocks), ("v_blocks", v_blocks)):
+            if x is None or x.dtype != torch.float8_e4m3fn or x.shape != shape or x.stride(3) != 1:
+                raise Dsv4Error(f"{name} of a 4-bit cache must be a float8_e4m3fn {list(shape)} tensor with contiguous rows")
+        if k_blocks.stride() != v_blocks.stride():
+            raise Dsv4Error("v_blocks must have the strides of k_blocks")
+    elif k_blocks is not None or v_blocks is not None:
+        raise Dsv4Error("k_blocks and v_blocks go with a 4-bit cache")
     for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
         if x is None:
             continue
-        if k_pages.dtype != torch.float8_e4m3fn:
-            raise Dsv4Error(f"{name} goes with a float8_e4m3fn cache")
+        if format_ not in _GQA_CODES:
+            raise Dsv4Error(f"{name} goes with a float8_e4m3fn or 4-bit cache")
         if x.dtype != torch.float32 or x.shape != (heads,) or not x.is_contiguous():
             raise Dsv4Error(f"{name} must be a contiguous fp32 tensor of {heads} entries")
-    keep = (k_pages, v_pages, page_table, k_scale, v_scale)
+    keep = (k_pages, v_pages, page_table, k_scale, v_scale, k_blocks, v_blocks)
     if any(x is not None and x.device != k_pages.device for x in keep):
         raise Dsv4Error("the tensors of a cache must be on one device")
     es = k_pages.element_size()
@@ -396,7 +421,11 @@ def make_gqa_cache(k_pages, v_pages, page_table, *, k_scale=None, v_scale=None):
     c.page_table_rows, c.page_table_width = page_table.shape
     c.page_table_stride = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
     c.num_kv_heads, c.head_dim, c.page_size = heads, dim, page_size
-    c.format = _GQA_TYPES[k_pages.dtype]
+    c.format = format_
+    if format_ == DSV4_GQA_E2M1:
+        c.k_blocks, c.v_blocks = k_blocks.data_ptr(), v_blocks.data_ptr()
+        c.block_page_stride, c.block_head_stride, c.block_row_stride = (
+            k_blocks.stride(i) if k_blocks.shape[i] > 1 else 0 for i in range(3))
     c.k_scale = None if k_scale is None else k_scale.data_ptr()
     c.v_scale = None if v_scale is None else v_scale.data_ptr()
     c._keep = keep
@@ -450,16 +479,20 @@ def _scratch(workspace, need, cache, stream):
 
 def _gqa_type(x, cache):
     """The type code of q, k or v for this cache."""
-    t = _GQA_TYPES.get(x.dtype, DSV4_GQA_E4M3)
-    if t == DSV4_GQA_E4M3 or (cache.format != t and cache.format != DSV4_GQA_E4M3):
-        raise Dsv4Error("rows must be bf16 or f16, and have the cache's type unless that is float8_e4m3fn")
+    return _gqa_type_of(x.dtype, cache)
+
+
+def _gqa_type_of(dtype, cache):
+    t = _GQA_TYPES.get(dtype, DSV4_GQA_E4M3)
+    if t in _GQA_CODES or (cache.format != t and cache.format not in _GQA_CODES):
+        raise Dsv4Error("rows must be bf16 or f16, and have the cache's type unless that is float8_e4m3fn or 4-bit codes")
     return t
 
 
 def dsv4_gqa_store(k, v, req_rows, slots, cache, *, weights=None, positions=None, token_positions=None, stream=None):
     """Write new rows k, v ([n, KV heads, head_dim], bf16 or f16, rows
     contiguous) to slot slots[i] of page-table row req_rows[i] (int32 [n]
-    each), packed for an e4m3 cache.  weights (fp32 [request rows, KV heads,
+    each), packed for an e4m3 or 4-bit cache.  weights (fp32 [request rows, KV heads,
     width]) starts at 0 there, positions (int32, same shape) at
     token_positions[i]."""
     index = cache._index
@@ -497,6 +530,44 @@ def dsv4_gqa_store(k, v, req_rows, slots, cache, *, weights=None, positions=None
                              slots.data_ptr(), cache._ref, wp, pp, width, tp, _raw_stream(stream, index))
     if rc:
         _check(rc)
+
+
+def dsv4_gqa_load(req_rows, slots, cache, *, dtype=None, k=None, v=None, stream=None):
+    """Read cached rows back: row i of the [n, KV heads, head_dim] results is
+    what slot slots[i] of page-table row req_rows[i] (int32 [n] each) stands
+    for, in the cache's own type, or for an e4m3 or 4-bit cache in `dtype`
+    (bf16 unless it says f16).  k and v: tensors to write to (both or neither;
+    heads and tokens may have any strides, so both may be parts of one tensor).
+    Rows without a place become zeros and set LOAD_ROW.  Returns (k, v)."""
+    index = cache._index
+    n = slots.numel()
+    _need(req_rows, "req_rows", torch.int32, n, index)
+    _need(slots, "slots", torch.int32, n, index)
+    shape = (n, *cache._rows)
+    if k is None and v is None:
+        if dtype is None:
+            dtype = torch.float16 if cache.format == DSV4_GQA_F16 else torch.bfloat16
+        type_ = _gqa_type_of(dtype, cache)
+        k, v = (_new_output(shape, dtype, cache._keep[0].device, stream) for _ in range(2))
+    elif k is None or v is None:
+        raise Dsv4Error("k and v go together")
+    else:
+        type_ = _gqa_type(k, cache)
+        if k.shape != shape or v.shape != shape or v.dtype is not k.dtype or dtype not in (None, k.dtype) \
+                or k.stride(2) != 1 or v.stride(2) != 1 or k.get_device() != index or v.get_device() != index:
+            raise Dsv4Error(f"k and v must be {list(shape)} tensors of one type with contiguous rows on the cache's device")
+    if n == 0:
+        return k, v
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    if n <= 1 or cache.num_kv_heads == 1:         # a dimension of one entry may have any stride
+        kt, vt = (0, 0) if n <= 1 else (kt, vt)
+        kh, vh = (0, 0) if cache.num_kv_heads == 1 else (kh, vh)
+    rc = _lib.dsv4_gqa_load(req_rows.data_ptr(), slots.data_ptr(), n, cache._ref, k.data_ptr(), kt, kh, v.data_ptr(),
+                            vt, vh, type_, _raw_stream(stream, index))
+    if rc:
+        _check(rc)
+    return k, v
 
 
 def dsv4_gqa_decode_workspace_size(cache, batch, num_heads, max_len=None, weights=False):

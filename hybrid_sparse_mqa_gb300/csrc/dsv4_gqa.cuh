@@ -22,6 +22,9 @@ struct Cache {
     int kv_heads, page_shift;
     const float* k_scale;
     const float* v_scale;
+    uint8_t* kb;                           // block scales (E2M1)
+    uint8_t* vb;
+    long long b_page_stride, b_head_stride, b_row_stride;
 };
 
 // Request b as the kernels read it: its row of the tables and the number of
@@ -63,9 +66,25 @@ inline Cache device_cache(const dsv4_gqa_cache* c) {
     d.kv_heads = c->num_kv_heads;
     d.page_shift = 0;
     while ((1 << d.page_shift) < c->page_size) ++d.page_shift;
-    d.k_scale = c->format == DSV4_GQA_E4M3 ? c->k_scale : nullptr;
-    d.v_scale = c->format == DSV4_GQA_E4M3 ? c->v_scale : nullptr;
+    const bool coded = c->format == DSV4_GQA_E4M3 || c->format == DSV4_GQA_E2M1, blocks = c->format == DSV4_GQA_E2M1;
+    d.k_scale = coded ? c->k_scale : nullptr;
+    d.v_scale = coded ? c->v_scale : nullptr;
+    d.kb = blocks ? static_cast<uint8_t*>(c->k_blocks) : nullptr;
+    d.vb = blocks ? static_cast<uint8_t*>(c->v_blocks) : nullptr;
+    d.b_page_stride = blocks ? c->block_page_stride : 0;
+    d.b_head_stride = blocks ? c->block_head_stride : 0;
+    d.b_row_stride = blocks ? c->block_row_stride : 0;
     return d;
+}
+
+// Bytes of a row's values or codes.
+inline int row_bytes(const dsv4_gqa_cache* c) {
+    return c->format == DSV4_GQA_E2M1 ? c->head_dim / 2 : c->head_dim * (c->format == DSV4_GQA_E4M3 ? 1 : 2);
+}
+// Whether rows and queries of `type` go with the cache.
+inline bool type_fits(const dsv4_gqa_cache* c, int type) {
+    if (type != DSV4_GQA_BF16 && type != DSV4_GQA_F16) return false;
+    return c->format == type || c->format == DSV4_GQA_E4M3 || c->format == DSV4_GQA_E2M1;
 }
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -93,11 +112,19 @@ inline int check_cache(const dsv4_gqa_cache* c) {
     if (c->page_stride % 16 || c->head_stride % 16 || c->row_stride % 16 || c->page_stride < 0 || c->head_stride < 0 ||
         c->row_stride < 0)
         return DSV4_ERR_INVALID;
-    if (c->format != DSV4_GQA_BF16 && c->format != DSV4_GQA_F16 && c->format != DSV4_GQA_E4M3)
+    if (c->format != DSV4_GQA_BF16 && c->format != DSV4_GQA_F16 && c->format != DSV4_GQA_E4M3 &&
+        c->format != DSV4_GQA_E2M1)
         return DSV4_ERR_UNSUPPORTED;
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return DSV4_ERR_UNSUPPORTED;
     if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) || c->num_kv_heads > 256)
         return DSV4_ERR_UNSUPPORTED;
+    if (c->format == DSV4_GQA_E2M1) {
+        const int b = c->head_dim / 16;
+        if (!c->k_blocks || !c->v_blocks || !aligned16(c->k_blocks) || !aligned16(c->v_blocks)) return DSV4_ERR_INVALID;
+        if (c->block_page_stride % b || c->block_head_stride % b || c->block_row_stride % b || c->block_page_stride < 0 ||
+            c->block_head_stride < 0 || c->block_row_stride < 0)
+            return DSV4_ERR_INVALID;
+    }
     return DSV4_OK;
 }
 

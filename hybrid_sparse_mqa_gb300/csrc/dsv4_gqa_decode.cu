@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(kWeightThreads) dsv4_gqa_weight_kernel(const _
     }
 }
 
-int tile_slots(int format, int head_dim) {
-    const int rows = 4096 / (head_dim * (format == DSV4_GQA_E4M3 ? 1 : 2));
+int tile_slots(const dsv4_gqa_cache* c) {
+    const int rows = (c->format == DSV4_GQA_E2M1 ? 2048 : 4096) / row_bytes(c);
     return rows < 16 ? 16 : rows;
 }
 
@@ -309,12 +309,12 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
     if (pl.group > 64) return DSV4_ERR_UNSUPPORTED;
     pl.nt = pl.group > 8 ? 2 : 1;
     pl.chunks = (pl.group + 8 * pl.nt - 1) / (8 * pl.nt);
-    pl.tt = tile_slots(c->format, c->head_dim);
+    pl.tt = tile_slots(c);
     const long long segments = (long long)batch * c->num_kv_heads * pl.chunks;
     pl.tiles = segments * ((max_len + pl.tt - 1) / pl.tt);
     if (pl.tiles >= 1LL << 31 || segments > kMostSlots) return DSV4_ERR_UNSUPPORTED;
     // (512-byte rows: one CTA's ring fills an SM's shared memory)
-    const int most = c->head_dim * (c->format == DSV4_GQA_E4M3 ? 1 : 2) > 256 ? kMaxCtas / 2 : kMaxCtas;
+    const int most = row_bytes(c) > 256 ? kMaxCtas / 2 : kMaxCtas;
     pl.places = most;
     pl.min_tiles = (max_len + pl.tt - 1) / pl.tt <= kFewTiles ? 1 : 2;
     const long long want = pl.tiles / pl.min_tiles;
@@ -433,8 +433,7 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     Plan pl;
     int rc = make_plan(cache, batch, num_heads, max_len, weights_out != nullptr, pl);
     if (rc) return rc;
-    if (type != DSV4_GQA_BF16 && type != DSV4_GQA_F16) return DSV4_ERR_UNSUPPORTED;
-    if (cache->format != DSV4_GQA_E4M3 && cache->format != type) return DSV4_ERR_UNSUPPORTED;
+    if (!type_fits(cache, type)) return DSV4_ERR_UNSUPPORTED;
     if (!q || !out || !lens || !aligned16(q) || !aligned16(out) || q_stride % 8 || window < 0) return DSV4_ERR_INVALID;
     if (!weights != !weights_out || (weights && width < max_len)) return DSV4_ERR_INVALID;
     if (weights && !same_or_apart(weights, weights_out, row_array_bytes(cache, width))) return DSV4_ERR_INVALID;
@@ -486,8 +485,9 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     if (rc) return rc;
     rc = cache->format == DSV4_GQA_BF16  ? launch_decode_bf16(p, d, pl.nt, stream)
          : cache->format == DSV4_GQA_F16 ? launch_decode_f16(p, d, pl.nt, stream)
-         : p.q_bf16                      ? launch_decode_e4m3(p, d, pl.nt, stream)
-                                         : launch_decode_e4m3_f16(p, d, pl.nt, stream);
+         : cache->format == DSV4_GQA_E4M3
+             ? (p.q_bf16 ? launch_decode_e4m3(p, d, pl.nt, stream) : launch_decode_e4m3_f16(p, d, pl.nt, stream))
+             : (p.q_bf16 ? launch_decode_e2m1(p, d, pl.nt, stream) : launch_decode_e2m1_f16(p, d, pl.nt, stream));
     if (rc || p.cluster) return rc;
     if (d == 64)
         rc = pl.tt == 32 ? launch_join<64, 32>(p, pl.nt, stream) : launch_join<64, 64>(p, pl.nt, stream);

@@ -1,7 +1,7 @@
 // dsv4_gqa_decode.cuh - one-token attention over a paged grouped-query cache
 // (include/dsv4gqa.h states what is computed).  The kernel is a template over
 // the cache's element type, compiled once per type in
-// dsv4_gqa_decode_{bf16,f16,e4m3,e4m3_f16}.cu; dsv4_gqa_decode.cu holds the host side
+// dsv4_gqa_decode_{bf16,f16,e4m3,e4m3_f16,e2m1,e2m1_f16}.cu; dsv4_gqa_decode.cu holds the host side
 // and the kernels that join split requests and accumulate weights.
 //
 // Work: a segment is one (request, KV head, group of up to 8 NT query heads);
@@ -207,6 +207,43 @@ __device__ __forceinline__ uint32_t e4m3x2_hi_f16x2(uint32_t codes) {
     asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, hi;\n}\n" : "=r"(r) : "r"(codes));
     return r;
 }
+// Eight e2m1 codes -> four pairs of f16 values (byte i holds pair i, the low half first), exactly.
+__device__ __forceinline__ void e2m1x8_f16x2(uint32_t codes, uint32_t (&r)[4]) {
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(codes));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// (x & mask) | (y & ~mask)
+__device__ __forceinline__ uint32_t pick_bits(uint32_t x, uint32_t y, uint32_t mask) {
+    return (x & mask) | (y & ~mask);
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_shared_u2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if constexpr (BF16) {
@@ -249,6 +286,13 @@ __device__ __forceinline__ void cp_async_16_whole(uint32_t dst, const void* src,
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
                  : "memory");
 }
+// The same for N = 4, 8 or 16 bytes (block scales of a row).
+template <int N>
+__device__ __forceinline__ void cp_async_hint(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
+    asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %2, %3, %4;" ::"r"(dst), "l"(src), "n"(N),
+                 "r"(src_bytes), "l"(policy)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // Asks for a CTA of the grid that has not been launched; the answer's 16 bytes
@@ -281,21 +325,23 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
 }
 
 // ---------------------------------------------------------------- shape
-// KIND: DSV4_GQA_BF16 / F16 / E4M3; QKIND: of the queries and the output, BF16
-// or F16.  A warp's stage is TT rows of K and of V.
+// KIND: DSV4_GQA_BF16 / F16 / E4M3 / E2M1; QKIND: of the queries and the output,
+// BF16 or F16.  A warp's stage is TT rows of K and of V, and of their block scales
+// behind both (E2M1).
 template <int KIND_, int QKIND, int D_, int NT_>
 struct Shape {
     static constexpr int KIND = KIND_, D = D_, NT = NT_;
-    static constexpr bool FP8 = KIND == DSV4_GQA_E4M3;
-    static constexpr bool BF16 = KIND == DSV4_GQA_BF16;      // operand type of the MMAs (e4m3: f16)
+    static constexpr bool FP8 = KIND == DSV4_GQA_E4M3, FP4 = KIND == DSV4_GQA_E2M1, CODES = FP8 || FP4;
+    static constexpr bool BF16 = KIND == DSV4_GQA_BF16;      // operand type of the MMAs (codes: f16)
     static constexpr bool QBF16 = QKIND == DSV4_GQA_BF16;
-    static_assert(FP8 || QKIND == KIND, "only e4m3 rows are read by queries of another type");
+    static_assert(CODES || QKIND == KIND, "only rows of codes are read by queries of another type");
     // P in two pieces.  One f16 is off by 2^-12 of it, an eighth of a bf16 output's rounding but as much as an f16
     // output's: 8 x 1024..16384 e4m3 rows of 128, 32 / 4 heads, f16 out: an error of 5.7e-6 (rms) with one piece and of
     // 4.3e-6, the output's own rounding, with two
-    static constexpr bool TWO = !FP8 || !QBF16;
-    static constexpr int ROWB = D * (FP8 ? 1 : 2);           // bytes of a row
-    static constexpr int TT = 4096 / ROWB < 16 ? 16 : 4096 / ROWB;
+    static constexpr bool TWO = !CODES || !QBF16;
+    static constexpr int ROWB = FP4 ? D / 2 : D * (FP8 ? 1 : 2);       // bytes of a row
+    static constexpr int BLKB = FP4 ? D / 16 : 0;            // bytes of its block scales
+    static constexpr int TT = FP4 ? 2048 / ROWB : 4096 / ROWB < 16 ? 16 : 4096 / ROWB;
     static constexpr int MT = TT / 16;                       // 16-slot MMA tiles
     static constexpr int DT = D / 16;                        // 16-dim tiles
     static constexpr int HEADS = 8 * NT;                     // query heads of a segment (padded)
@@ -307,14 +353,17 @@ struct Shape {
     static constexpr float DROP = BF16 ? 0.f : 11.f, SLACK = BF16 ? 8.f : 4.f;
     static constexpr int W = kWarps;
     static constexpr int TILE_BYTES = TT * ROWB;             // K or V of a stage
-    static constexpr int STAGES = 3;
+    static constexpr int BLOCK_BYTES = TT * BLKB;            // their block scales
+    static constexpr int STAGES = FP4 ? 5 : 3;
+    static constexpr int STAGE_BYTES = 2 * (TILE_BYTES + BLOCK_BYTES);
     static constexpr int CTAS = TILE_BYTES > 4096 ? 1 : 2;   // per SM (what shared memory holds)
-    static constexpr int RING_BYTES = W * STAGES * 2 * TILE_BYTES;
+    static constexpr int WARP_RING = STAGES * STAGE_BYTES;
+    static constexpr int RING_BYTES = W * WARP_RING;
     // queries of a segment, a row per head (16 bytes of padding spread the rows over the banks where there is room)
     static constexpr int QROW = D * 2 + (NT == 1 ? 16 : 0);
     // (16 heads of 256 beside e4m3 rows: two CTAs fit an SM only without the buffers; 64 x 1024..16384 rows, 64 / 4
     // heads: 354 us with them and 246 without)
-    static constexpr int Q_BYTES = FP8 && D == 256 && NT == 2 ? 0 : HEADS * QROW;
+    static constexpr int Q_BYTES = CODES && D == 256 && NT == 2 ? 0 : HEADS * QROW;
     static constexpr int SMEM = RING_BYTES + W * Q_BYTES;
     static constexpr int PPR = ROWB / 16;                    // 16-byte pieces per row
     static constexpr int RPI = 32 / PPR;                     // rows per warp-wide copy
@@ -324,16 +373,18 @@ struct Shape {
 // swizzles spread what one phase of the readers' loads touches over all
 // banks: ldmatrix reads 8 rows of one piece; the e4m3 readers read rows
 // (g, g + 1) x pieces 4j .. 4j + 3 of K and rows 2t (t = 0..3) x two
-// neighbouring pieces of V.
+// neighbouring pieces of V; the e2m1 readers 128 bytes of neighbouring rows of
+// K (rows of 32 and 64 bytes lie as they are) and rows 2t x 32 bytes of V.
 template <class S>
 __device__ __forceinline__ uint32_t k_offset(int row, int piece) {
-    if constexpr (!S::FP8) return row * S::ROWB + ((piece ^ (row & 7)) << 4);
-    if constexpr (S::ROWB == 64) return row * 64 + (piece << 4);
+    if constexpr (!S::CODES) return row * S::ROWB + ((piece ^ (row & 7)) << 4);
+    if constexpr (S::ROWB <= 64) return row * S::ROWB + (piece << 4);
     return row * S::ROWB + ((piece ^ ((row & 1) << 2)) << 4);
 }
 template <class S>
 __device__ __forceinline__ uint32_t v_offset(int row, int piece) {
-    if constexpr (!S::FP8) return row * S::ROWB + ((piece ^ (row & 7)) << 4);
+    if constexpr (!S::CODES) return row * S::ROWB + ((piece ^ (row & 7)) << 4);
+    if constexpr (S::ROWB == 32) return (row >> 2) * 128 + (((((row & 3) << 1) | piece) ^ ((row >> 1) & 2)) << 4);
     const int f = ((row >> 1) & 3) << 1;
     if constexpr (S::ROWB == 64) return (row >> 1) * 128 + (((((row & 1) << 2) | piece) ^ f) << 4);
     return row * S::ROWB + ((piece ^ f) << 4);
@@ -556,13 +607,13 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     }
 
     // ---- the copying side ----
-    const uint32_t ring = smem_u32(smem) + warp * (S::STAGES * 2 * S::TILE_BYTES);
+    const uint32_t ring = smem_u32(smem) + warp * S::WARP_RING;
     const int lane_row = lane / S::PPR, lane_piece = lane % S::PPR;
     const long long lane_off = lane_row * p.c.row_stride + lane_piece * 16;
     const int page_mask = (1 << p.c.page_shift) - 1;
     const uint64_t policy = read_policy(p.chunks == 1);
     // the K scale of cons's KV head, loaded as soon as cons comes to it: ahead of the copies
-    auto load_kscale = [&]() { return S::FP8 && p.c.k_scale ? __ldg(p.c.k_scale + cons.hc / p.chunks) : 1.f; };
+    auto load_kscale = [&]() { return S::CODES && p.c.k_scale ? __ldg(p.c.k_scale + cons.hc / p.chunks) : 1.f; };
     float kscale = load_kscale();
     Cursor<TT> prod = cons;
     unsigned p1 = c1;
@@ -574,9 +625,13 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
     const uint32_t qbuf = smem_u32(smem) + S::RING_BYTES + warp * S::Q_BYTES;
     int pslot = 0;                                 // first slot of prod's tile
     long long phead = 0;                           // byte offset of its KV head, and of this lane's first piece
+    // block scales: lanes 0 .. 15 copy those of 16 rows of K, the others of V
+    const uint8_t* bhead = nullptr;
     auto come_to = [&]() {
         pslot = (prod.rg.lo / TT + static_cast<int>(prod.at - prod.seg)) * TT;
         phead = (prod.hc / p.chunks) * p.c.head_stride + lane_off;
+        if constexpr (S::FP4)
+            bhead = (lane < 16 ? p.c.kb : p.c.vb) + (prod.hc / p.chunks) * p.c.b_head_stride + (lane & 15) * p.c.b_row_stride;
     };
     come_to();
     int pieces = 0, piece = 0;                     // pieces (a share's part of a segment) that prod has come to; cons's
@@ -650,12 +705,20 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
             if (wanted && !ok) atomicOr(p.err, DSV4_DEV_ERR_GQA_PAGE);
             const unsigned okm = __ballot_sync(0xffffffffu, ok);
             if (lane == 0) s_ok[warp][stage] = okm;
-            const uint32_t kd = ring + stage * 2 * S::TILE_BYTES, vd = kd + S::TILE_BYTES;
+            const uint32_t kd = ring + stage * S::STAGE_BYTES, vd = kd + S::TILE_BYTES;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int pg = __shfl_sync(0xffffffffu, page, m);
                 const bool have = (okm >> m) & 1;
                 const int s = pslot + m * 16;
+                if constexpr (S::FP4) {
+                    const int r = s + (lane & 15);
+                    const bool in = have && r < prod.rg.n && r >= prod.rg.lo;
+                    const uint32_t bd = vd + S::TILE_BYTES + (lane >> 4) * S::BLOCK_BYTES + (m * 16 + (lane & 15)) * S::BLKB;
+                    cp_async_hint<S::BLKB>(
+                        bd, in ? bhead + pg * p.c.b_page_stride + (s & page_mask) * p.c.b_row_stride : p.c.kb,
+                        in ? S::BLKB : 0u, policy);
+                }
                 const long long base = have ? pg * p.c.page_stride + (s & page_mask) * p.c.row_stride + phead : 0;
                 const uint8_t *ks = p.c.k + base, *vs = p.c.v + base;
                 if (have && s >= prod.rg.lo && s + 16 <= prod.rg.n) {
@@ -712,7 +775,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         for (int nt = 0; nt < NT; ++nt) {
             const bool have = nt * 8 + g < nheads;
             const uint32_t* qr = reinterpret_cast<const uint32_t*>(qbase + (nt * 8 + g) * qrow);
-            if constexpr (!S::FP8) {
+            if constexpr (!S::CODES) {
 #pragma unroll
                 for (int kk = 0; kk < DT; ++kk) {
                     qf[kk][nt][0] = have ? qr[kk * 8 + t4] : 0u;
@@ -720,11 +783,13 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 }
                 smul[nt][0] = smul[nt][1] = p.scale_log2;
             } else {
-                // MMA kk = 4 j + i takes dims 16 (t + 4 j) + 4 i .. + 3 from the thread with that t
+                // MMA kk = 4 j + i takes dims 16 (t + 4 j) + 4 i .. + 3 from the thread with that t (e2m1 rows of 128
+                // and 256: kk = 8 j + i dims 32 (t + 4 j) + 4 i .. + 3)
+                constexpr int PER = S::FP4 && D > 64 ? 8 : 4;
                 float amax = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < DT; ++kk) {
-                    const int d2 = (16 * (t4 + 4 * (kk >> 2)) + 4 * (kk & 3)) / 2;
+                    const int d2 = (4 * PER * (t4 + 4 * (kk / PER)) + 4 * (kk % PER)) / 2;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         qf[kk][nt][u] = have ? qr[d2 + u] : 0u;
@@ -770,7 +835,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         for (unsigned tile = cons.at; tile < cons.end; ++tile) {
             cp_async_wait_group<S::STAGES - 1>();
             __syncwarp();
-            const uint32_t ks = ring + stage * 2 * S::TILE_BYTES, vs = ks + S::TILE_BYTES;
+            const uint32_t ks = ring + stage * S::STAGE_BYTES, vs = ks + S::TILE_BYTES;
             const unsigned okm = s_ok[warp][stage];
             const int slot0 = (cons.rg.lo / TT + static_cast<int>(tile - cons.seg)) * TT;
 
@@ -784,7 +849,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) s[m][nt][c] = 0.f;
-            if constexpr (!S::FP8) {
+            if constexpr (!S::CODES) {
                 const int mrow = lane & 15, mpiece = lane >> 4;
 #pragma unroll
                 for (int kk = 0; kk < DT; ++kk)
@@ -795,6 +860,55 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma16816<S::BF16>(kChains > 1 && kk & 1 ? s2[0][0] : s[m][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+                    }
+                if constexpr (kChains > 1)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[0][0][c] += s2[0][0][c];
+            } else if constexpr (S::FP4) {
+                // A thread's 16 bytes of rows g and g + 8 are two blocks (64 dims: 8 bytes, one).  Code times block scale
+                // is exact in f16: 2 + 4 significant bits, 2^-10 .. 2688
+                constexpr int WORDS = D == 64 ? 2 : 4;
+                const uint32_t kb = vs + S::TILE_BYTES;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < (D == 256 ? 2 : 1); ++j) {
+                        uint32_t w[2][WORDS], sc[2][2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int row = m * 16 + g + 8 * u;
+                            if constexpr (D == 64) {
+                                const uint2 x = ld_shared_u2(ks + row * S::ROWB + t4 * 8);
+                                w[u][0] = x.x; w[u][1] = x.y;
+                                const uint32_t b = e4m3x2_f16x2(ld_shared_u8(kb + row * S::BLKB + t4));
+                                sc[u][0] = sc[u][1] = __byte_perm(b, b, 0x1010);
+                            } else {
+                                const uint4 x = ld_shared_u4(ks + k_offset<S>(row, t4 + 4 * j));
+                                w[u][0] = x.x; w[u][1] = x.y; w[u][2] = x.z; w[u][3] = x.w;
+                                const uint32_t b = e4m3x2_f16x2(ld_shared_u16(kb + row * S::BLKB + 8 * j + 2 * t4));
+                                sc[u][0] = __byte_perm(b, b, 0x1010);
+                                sc[u][1] = __byte_perm(b, b, 0x3232);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < WORDS; ++i) {
+                            uint32_t x[4], y[4];
+                            e2m1x8_f16x2(w[0][i], x);
+                            e2m1x8_f16x2(w[1][i], y);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                x[k] = mul_f16x2(x[k], sc[0][i >> 1]);
+                                y[k] = mul_f16x2(y[k], sc[1][i >> 1]);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t a[4] = {x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1]};
+                                const int kk = 8 * j + 2 * i + k;
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma16816<false>(kChains > 1 && k ? s2[0][0] : s[m][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+                            }
+                        }
                     }
                 if constexpr (kChains > 1)
 #pragma unroll
@@ -888,7 +1002,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                             lo[nt][u] = transpose8x8(pack2<S::BF16>(x - r.x, y - r.y));
                         }
                     }
-                if constexpr (!S::FP8) {
+                if constexpr (!S::CODES) {
                     const int mrow = (lane & 7) + ((lane >> 4) << 3), mpiece = (lane >> 3) & 1;
 #pragma unroll
                     for (int j = 0; j < DT; ++j) {
@@ -898,6 +1012,47 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                         for (int nt = 0; nt < NT; ++nt) {
                             mma16816<S::BF16>(o[j][nt], a, hi[nt][0], hi[nt][1]);
                             mma16816<S::BF16>(o[j][nt], a, lo[nt][0], lo[nt][1]);
+                        }
+                    }
+                } else if constexpr (S::FP4) {
+                    // slots 2t, 2t + 1, 2t + 8, 2t + 9; the codes of a pair of slots become bytes of one dim each, whose
+                    // two halves convert to an A operand.  Dims as for e4m3 rows; a thread's 16 dims are one block (8 of
+                    // 64 dims: half of one)
+                    constexpr int WORDS = D == 64 ? 1 : 2;       // 32-bit words per thread, slot and half
+                    const uint32_t vb = vs + S::TILE_BYTES + S::BLOCK_BYTES;
+#pragma unroll
+                    for (int hh = 0; hh < (D == 256 ? 2 : 1); ++hh) {
+                        uint32_t v[4][WORDS], b[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const int row = m * 16 + 2 * t4 + (u & 1) + (u >> 1) * 8;
+                            if constexpr (D == 64) {
+                                v[u][0] = ld_shared_u32(vs + v_offset<S>(row, g >> 2) + (g & 3) * 4);
+                                b[u] = ld_shared_u8(vb + row * S::BLKB + (g >> 1));
+                            } else {
+                                const uint2 x = ld_shared_u2(vs + v_offset<S>(row, (g >> 1) + 4 * hh) + (g & 1) * 8);
+                                v[u][0] = x.x; v[u][1] = x.y;
+                                b[u] = ld_shared_u8(vb + row * S::BLKB + g + 8 * hh);
+                            }
+                        }
+                        const uint32_t s01 = e4m3x2_f16x2(b[0] | b[1] << 8), s23 = e4m3x2_f16x2(b[2] | b[3] << 8);
+#pragma unroll
+                        for (int w = 0; w < WORDS; ++w) {
+                            uint32_t a[4][4];
+                            e2m1x8_f16x2(pick_bits(v[0][w], v[1][w] << 4, 0x0f0f0f0fu), a[0]);
+                            e2m1x8_f16x2(pick_bits(v[0][w] >> 4, v[1][w], 0x0f0f0f0fu), a[1]);
+                            e2m1x8_f16x2(pick_bits(v[2][w], v[3][w] << 4, 0x0f0f0f0fu), a[2]);
+                            e2m1x8_f16x2(pick_bits(v[2][w] >> 4, v[3][w], 0x0f0f0f0fu), a[3]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t x[4] = {mul_f16x2(a[0][i], s01), mul_f16x2(a[1][i], s01),
+                                                       mul_f16x2(a[2][i], s23), mul_f16x2(a[3][i], s23)};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    mma16816<false>(o[hh * 8 + w * 4 + i][nt], x, hi[nt][0], hi[nt][1]);
+                                    if constexpr (S::TWO) mma16816<false>(o[hh * 8 + w * 4 + i][nt], x, lo[nt][0], lo[nt][1]);
+                                }
+                            }
                         }
                     }
                 } else {
@@ -951,7 +1106,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 lsum[nt][u] += __shfl_xor_sync(0xffffffffu, lsum[nt][u], 8);
                 lsum[nt][u] += __shfl_xor_sync(0xffffffffu, lsum[nt][u], 16);
             }
-        if constexpr (!S::FP8) {
+        if constexpr (!S::CODES) {
             // P's two parts times an infinite value can be inf - inf or 0 inf, which is NaN where the sum is infinite:
             // where a NaN comes of finite scores, the infinities are looked up
             bool odd = false;
@@ -991,10 +1146,10 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
         if constexpr (SEG) {
             // the warps' rings become their outputs, [HEADS][D] fp32 (padded rows), and the cluster adds them up
             constexpr int kRow = D + 4;
-            static_assert(HEADS * kRow * 4 <= S::STAGES * 2 * S::TILE_BYTES, "a warp's output fits its ring");
+            static_assert(HEADS * kRow * 4 <= S::WARP_RING, "a warp's output fits its ring");
             cp_async_wait_group<0>();
             __syncwarp();
-            float* mine = reinterpret_cast<float*>(smem + warp * (S::STAGES * 2 * S::TILE_BYTES));
+            float* mine = reinterpret_cast<float*>(smem + warp * S::WARP_RING);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1003,7 +1158,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                     if (g == 0) s_ml[warp][c] = make_float2(mref[nt][u], lsum[nt][u]);
 #pragma unroll
                     for (int j = 0; j < DT; ++j) {
-                        if constexpr (!S::FP8) {
+                        if constexpr (!S::CODES) {
                             mine[c * kRow + 16 * j + g] = o[j][nt][u];
                             mine[c * kRow + 16 * j + 8 + g] = o[j][nt][u + 2];
                         } else {
@@ -1014,7 +1169,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 }
             cluster_sync();
             const int rank = blockIdx.x % p.cluster;
-            const float vmul = S::FP8 && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
+            const float vmul = S::CODES && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
             const uint32_t ml0 = smem_u32(&s_ml[0][0]), o0 = smem_u32(smem);
             for (int e = rank * W * 32 + tid; e < nheads * D / 2; e += p.cluster * W * 32) {
                 const int c = e / (D / 2), d = e % (D / 2) * 2;
@@ -1025,7 +1180,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         ml[w] = ld_cluster_f2(mapa(ml0 + (w * HEADS + c) * 8, r));
-                        v[w] = ld_cluster_f2(mapa(o0 + w * (S::STAGES * 2 * S::TILE_BYTES) + (c * kRow + d) * 4, r));
+                        v[w] = ld_cluster_f2(mapa(o0 + w * S::WARP_RING + (c * kRow + d) * 4, r));
                     }
                     float top = mx;
 #pragma unroll
@@ -1130,7 +1285,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                     const int c = nt * 8 + 2 * t4 + u;
                     if (c >= nheads) continue;
                     float* to = p.part_o + ((size_t)entry * HEADS + c) * D;
-                    if constexpr (!S::FP8) {
+                    if constexpr (!S::CODES) {
 #pragma unroll
                         for (int j = 0; j < DT; ++j) {
                             to[16 * j + g] = o[j][nt][u];
@@ -1148,7 +1303,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 }
             continue;
         }
-        const float vmul = S::FP8 && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
+        const float vmul = S::CODES && p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
         const size_t row = (size_t)here_b * p.heads + head0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -1169,7 +1324,7 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 }
             }
             uint16_t* out = static_cast<uint16_t*>(p.out);
-            if constexpr (!S::FP8) {
+            if constexpr (!S::CODES) {
                 // pairs of heads to pairs of dims: this thread then holds head g, dims 2t and 2t + 1 of an 8-dim block
 #pragma unroll
                 for (int j = 0; j < DT; ++j)
@@ -1207,6 +1362,8 @@ int launch_decode_bf16(const DecodeParams& p, int head_dim, int nt, void* stream
 int launch_decode_f16(const DecodeParams& p, int head_dim, int nt, void* stream);
 int launch_decode_e4m3(const DecodeParams& p, int head_dim, int nt, void* stream);
 int launch_decode_e4m3_f16(const DecodeParams& p, int head_dim, int nt, void* stream);
+int launch_decode_e2m1(const DecodeParams& p, int head_dim, int nt, void* stream);
+int launch_decode_e2m1_f16(const DecodeParams& p, int head_dim, int nt, void* stream);
 
 template <class S>
 inline int launch_decode_shape(const DecodeParams& p, void* stream) {

@@ -53,6 +53,7 @@ struct EvictParams {
     int* movers;                           // [batch][KV heads][most] their slots
     int most;
     int row_pieces;                        // 16-byte pieces of a row
+    int block_bytes;                       // of its block scales: 4, 8 or 16 (E2M1), else 0
     int alone;                             // no request can be more than kFew rows over the bound: the select kernel
                                            // moves them itself and writes the new lengths
     unsigned int* err;
@@ -79,6 +80,16 @@ __device__ __forceinline__ uint4 ld_cluster_u4(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
+}
+
+// A row's block scales: 4, 8 or 16 bytes, aligned to as many.
+__device__ __forceinline__ void copy_blocks(uint8_t* to, const uint8_t* from, int bytes) {
+    if (bytes == 4)
+        *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
+    else if (bytes == 8)
+        *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
+    else
+        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
 }
 
 template <int WARPS>
@@ -311,6 +322,12 @@ __global__ void __launch_bounds__(THREADS, KEYS > 16 ? 1 : 1024 / THREADS) dsv4_
                                 (piece < p.row_pieces ? piece : piece - p.row_pieces) * 16;
                 *reinterpret_cast<uint4*>(pool + tp * p.c.page_stride + (dst & in_page) * p.c.row_stride) =
                     *reinterpret_cast<const uint4*>(pool + fp * p.c.page_stride + (src & in_page) * p.c.row_stride);
+                // a row's first thread takes its block scales along
+                if (p.block_bytes && (piece == 0 || piece == p.row_pieces)) {
+                    uint8_t* blocks = (piece ? p.c.vb : p.c.kb) + h * p.c.b_head_stride;
+                    copy_blocks(blocks + tp * p.c.b_page_stride + (dst & in_page) * p.c.b_row_stride,
+                                blocks + fp * p.c.b_page_stride + (src & in_page) * p.c.b_row_stride, p.block_bytes);
+                }
             }
             return;
         }
@@ -533,6 +550,12 @@ __global__ void __launch_bounds__(kMoveThreads, 8) dsv4_gqa_move_kernel(const __
         } else {
             to = tp * p.c.page_stride + (dst & mask) * p.c.row_stride + h * p.c.head_stride;
             of = fp * p.c.page_stride + (src & mask) * p.c.row_stride + h * p.c.head_stride;
+            if (p.block_bytes) {
+                const long long bt = tp * p.c.b_page_stride + (dst & mask) * p.c.b_row_stride + h * p.c.b_head_stride;
+                const long long bf = fp * p.c.b_page_stride + (src & mask) * p.c.b_row_stride + h * p.c.b_head_stride;
+                copy_blocks(p.c.kb + bt, p.c.kb + bf, p.block_bytes);
+                copy_blocks(p.c.vb + bt, p.c.vb + bf, p.block_bytes);
+            }
         }
     }
     // a warp-wide copy moves 32 / PIECES rows, or a part of one
@@ -639,7 +662,7 @@ int load_all() {
     static unsigned long long ready = 0;
     return once_per_device(ready, [] {
         return load_select_cluster<1>() && load_select_cluster<2>() && load_select_cluster<4>() && load_select_cluster<8>() &&
-               load_kernels(dsv4_gqa_select_kernel<256, 16, 1>, dsv4_gqa_select_kernel<512, 0, 8>, dsv4_gqa_move_kernel<8>,
+               load_kernels(dsv4_gqa_select_kernel<256, 16, 1>, dsv4_gqa_select_kernel<512, 0, 8>, dsv4_gqa_move_kernel<4>, dsv4_gqa_move_kernel<8>,
                             dsv4_gqa_move_kernel<16>, dsv4_gqa_move_kernel<32>, dsv4_gqa_move_kernel<64>);
     });
 }
@@ -696,7 +719,8 @@ int dsv4_gqa_evict(int32_t batch, const int32_t* lens, const int32_t* seq_lens, 
     p.holes = reinterpret_cast<int*>(ws + l.holes);
     p.movers = reinterpret_cast<int*>(ws + l.movers);
     p.most = most_moved(max_len, keep);
-    p.row_pieces = cache->head_dim * (cache->format == DSV4_GQA_E4M3 ? 1 : 2) / 16;
+    p.row_pieces = row_bytes(cache) / 16;
+    p.block_bytes = cache->format == DSV4_GQA_E2M1 ? cache->head_dim / 16 : 0;
     p.err = err;
 
     // (new lengths that replace the old ones, or the tokens seen, have to wait for every head's CTA to have read those:
@@ -707,6 +731,7 @@ int dsv4_gqa_evict(int32_t batch, const int32_t* lens, const int32_t* seq_lens, 
     r = launch_select(p, stream);
     if (r || p.alone) return r;
     switch (p.row_pieces) {
+        case 2: return launch_move<4>(p, stream);
         case 4: return launch_move<8>(p, stream);
         case 8: return launch_move<16>(p, stream);
         case 16: return launch_move<32>(p, stream);

@@ -46,6 +46,15 @@ __device__ __forceinline__ float2 widen(uint32_t w) {
     else
         return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
+template <int TYPE>
+__device__ __forceinline__ uint32_t narrow(float lo, float hi) {
+    if constexpr (TYPE == DSV4_GQA_BF16) {
+        return pack_bf16x2(lo, hi);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
 
 // Two fp32 values in one 64-bit register (each lane of a packed operation
 // rounds as the scalar one does).
@@ -95,12 +104,7 @@ struct Packer {
     __device__ __forceinline__ explicit Packer(float s) : scale(s) {
         fast = TYPE == DSV4_GQA_BF16 ? s >= 0x1p-60f && s <= 0x1p60f : s >= 0x1p-23f && s <= 127.f;
         const float y = -__frcp_rn(s), l = 512.f * s;
-        if constexpr (TYPE == DSV4_GQA_BF16) {
-            lim = pack_bf16x2(l, l);
-        } else {
-            const __half2 v = __floats2half2_rn(l, l);
-            lim = *reinterpret_cast<const uint32_t*>(&v);
-        }
+        lim = narrow<TYPE>(l, l);
         ny2 = f32x2(y, y);
         s2 = f32x2(s, s);
     }
@@ -140,7 +144,94 @@ struct Packer {
     }
 };
 
-template <int TYPE, bool PACK, int PIECES>
+// max(|x|, |y|) of two pairs, NaN kept.
+template <int TYPE>
+__device__ __forceinline__ uint32_t abs_max2(uint32_t x, uint32_t y) {
+    x &= 0x7fff7fffu;
+    y &= 0x7fff7fffu;
+    if constexpr (TYPE == DSV4_GQA_BF16) {
+        const __nv_bfloat162 m =
+            __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    } else {
+        const __half2 m = __hmax2_nan(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+}
+// Eight values -> eight e2m1 codes (to nearest, ties to even, saturating), the first in the lowest half byte.
+__device__ __forceinline__ uint32_t e2m1x8(const float2 (&v)[4]) {
+    uint32_t r;
+    asm("{\n .reg .b8 a, b, c, d;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        " mov.b32 %0, {a, b, c, d};\n}\n"
+        : "=r"(r)
+        : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
+    return r;
+}
+
+// The same for 4-bit codes: a thread's 16 values are one block.  The block's
+// scale by one division; the codes of the correctly rounded quotients by one
+// Markstein correction of x y, y = RN(1 / step), as above.  There the bounds on
+// the head's scale keep the step (2^-9 to 448 times it) where nothing over- or
+// underflows that a code depends on: values are clamped to 8 steps first (6.x
+// and more saturate), and quotients below 1/4 have code 0 either way.
+template <int TYPE>
+struct BlockPacker {
+    float scale;
+    bool fast;
+
+    __device__ __forceinline__ explicit BlockPacker(float s) : scale(s) {
+        fast = TYPE == DSV4_GQA_BF16 ? s >= 0x1p-60f && s <= 0x1p60f : s >= 0x1p-14f && s <= 16.f;
+    }
+    // codes of the block's 16 values; returns the e4m3 code of its scale
+    __device__ __forceinline__ uint32_t codes16(uint4 a, uint4 b, uint2& codes) const {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t m = abs_max2<TYPE>(w[0], w[1]);
+#pragma unroll
+        for (int j = 2; j < 8; ++j) m = abs_max2<TYPE>(m, w[j]);
+        const float2 top = widen<TYPE>(abs_max2<TYPE>(m, m >> 16));
+        const uint32_t code = e4m3x2(make_float2(__fdiv_rn(top.x, 6.f * scale), 0.f)) & 0xffu;
+        float f[4];
+        e4m3x4_to_f32(code, f);
+        const float step = f[0] * scale;
+        uint32_t c[2];
+        if (fast) {
+            const float y = __frcp_rn(step);
+            const uint32_t lim = narrow<TYPE>(8.f * step, 8.f * step);
+            const uint64_t ny2 = f32x2(-y, -y), s2 = f32x2(step, step);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float2 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 n = widen<TYPE>(clamp2<TYPE>(w[4 * i + j], lim) ^ 0x80008000u);
+                    const uint64_t n2 = f32x2(n.x, n.y);
+                    const uint64_t q0 = mul_f32x2(n2, ny2);
+                    const uint64_t q = fma_f32x2(fma_f32x2(q0, s2, n2), ny2, q0);
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(v[j].x), "=f"(v[j].y) : "l"(q));
+                }
+                c[i] = e2m1x8(v);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                float2 v[4];
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = widen<TYPE>(w[4 * i + j]);
+                    v[j] = make_float2(__fdiv_rn(x.x, step), __fdiv_rn(x.y, step));
+                }
+                c[i] = e2m1x8(v);
+            }
+        }
+        const bool any = step > 0.f;              // (no scale, or a NaN)
+        codes = make_uint2(any ? c[0] : 0u, any ? c[1] : 0u);
+        return code;
+    }
+};
+
+// FORMAT: of the cache; TYPE: of the rows (BF16 for a plain copy of either).
+template <int TYPE, int FORMAT, int PIECES>
 __global__ void __launch_bounds__(kStoreThreads) dsv4_gqa_store_kernel(const __grid_constant__ StoreParams p) {
     constexpr int kTokens = kStoreThreads / PIECES;          // of one item
     grid_dependency_wait();
@@ -172,12 +263,14 @@ __global__ void __launch_bounds__(kStoreThreads) dsv4_gqa_store_kernel(const __g
             page[k] = __ldg(p.c.table + (long long)r[k] * p.c.table_stride + lp);
     }
     float scale = 1.f;
-    if constexpr (PACK) {
+    if constexpr (FORMAT != TYPE) {
         const float* scales = which ? p.c.v_scale : p.c.k_scale;
         if (scales) scale = __ldg(scales + h);
     }
     const Packer<TYPE> pack(scale);
+    const BlockPacker<TYPE> pack_block(scale);
     uint8_t* pool = (which ? p.c.v : p.c.k) + h * p.c.head_stride;
+    uint8_t* blocks = (which ? p.c.vb : p.c.kb) + h * p.c.b_head_stride;
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
         const int i = i0 + k * kTokens;
@@ -186,9 +279,14 @@ __global__ void __launch_bounds__(kStoreThreads) dsv4_gqa_store_kernel(const __g
             if (piece == 0) atomicOr(p.err, DSV4_DEV_ERR_STORE_ROW);
             continue;
         }
-        uint4* dst = reinterpret_cast<uint4*>(pool + page[k] * p.c.page_stride +
-                                              (s[k] & ((1 << p.c.page_shift) - 1)) * p.c.row_stride);
-        if constexpr (PACK) {
+        const int in_page = s[k] & ((1 << p.c.page_shift) - 1);
+        uint4* dst = reinterpret_cast<uint4*>(pool + page[k] * p.c.page_stride + in_page * p.c.row_stride);
+        if constexpr (FORMAT == DSV4_GQA_E2M1) {
+            uint2 codes;
+            blocks[page[k] * p.c.b_page_stride + in_page * p.c.b_row_stride + piece] =
+                static_cast<uint8_t>(pack_block.codes16(a[k], b[k], codes));
+            reinterpret_cast<uint2*>(dst)[piece] = codes;
+        } else if constexpr (FORMAT == DSV4_GQA_E4M3) {
             dst[piece] = pack.codes16(a[k], b[k]);
         } else {
             dst[2 * piece] = a[k];
@@ -202,26 +300,28 @@ __global__ void __launch_bounds__(kStoreThreads) dsv4_gqa_store_kernel(const __g
     }
 }
 
-template <int TYPE, bool PACK>
+template <int TYPE, int FORMAT>
 int launch_store(const StoreParams& p, int head_dim, void* stream) {
     const int tokens = kStoreThreads / (head_dim / 16) * kItems;
     const long long blocks = ((long long)p.n + tokens - 1) / tokens * 2 * p.c.kv_heads;
     if (blocks > 0x7fffffffLL) return DSV4_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(blocks));
-    if (head_dim == 64) return launch(dsv4_gqa_store_kernel<TYPE, PACK, 4>, grid, kStoreThreads, 0, stream, 1, p);
-    if (head_dim == 128) return launch(dsv4_gqa_store_kernel<TYPE, PACK, 8>, grid, kStoreThreads, 0, stream, 1, p);
-    return launch(dsv4_gqa_store_kernel<TYPE, PACK, 16>, grid, kStoreThreads, 0, stream, 1, p);
+    if (head_dim == 64) return launch(dsv4_gqa_store_kernel<TYPE, FORMAT, 4>, grid, kStoreThreads, 0, stream, 1, p);
+    if (head_dim == 128) return launch(dsv4_gqa_store_kernel<TYPE, FORMAT, 8>, grid, kStoreThreads, 0, stream, 1, p);
+    return launch(dsv4_gqa_store_kernel<TYPE, FORMAT, 16>, grid, kStoreThreads, 0, stream, 1, p);
 }
 
-template <int TYPE, bool PACK>
+template <int TYPE, int FORMAT>
 bool load_store() {
-    return load_kernels(dsv4_gqa_store_kernel<TYPE, PACK, 4>, dsv4_gqa_store_kernel<TYPE, PACK, 8>,
-                        dsv4_gqa_store_kernel<TYPE, PACK, 16>);
+    return load_kernels(dsv4_gqa_store_kernel<TYPE, FORMAT, 4>, dsv4_gqa_store_kernel<TYPE, FORMAT, 8>,
+                        dsv4_gqa_store_kernel<TYPE, FORMAT, 16>);
 }
 int load_all() {
     static unsigned long long ready = 0;
     return once_per_device(ready, [] {
-        return load_store<DSV4_GQA_BF16, false>() && load_store<DSV4_GQA_BF16, true>() && load_store<DSV4_GQA_F16, true>();
+        return load_store<DSV4_GQA_BF16, DSV4_GQA_BF16>() && load_store<DSV4_GQA_BF16, DSV4_GQA_E4M3>() &&
+               load_store<DSV4_GQA_F16, DSV4_GQA_E4M3>() && load_store<DSV4_GQA_BF16, DSV4_GQA_E2M1>() &&
+               load_store<DSV4_GQA_F16, DSV4_GQA_E2M1>();
     });
 }
 
@@ -239,8 +339,7 @@ extern "C" int dsv4_gqa_store(const void* k, int64_t k_token_stride, int64_t k_h
     int rc = check_cache(cache);
     if (rc) return rc;
     if (n < 0 || n > kMostSlots) return DSV4_ERR_INVALID;
-    if (type != DSV4_GQA_BF16 && type != DSV4_GQA_F16) return DSV4_ERR_UNSUPPORTED;
-    if (cache->format != DSV4_GQA_E4M3 && cache->format != type) return DSV4_ERR_UNSUPPORTED;
+    if (!type_fits(cache, type)) return DSV4_ERR_UNSUPPORTED;
     if (n == 0) return DSV4_OK;
     if (!k || !v || !req_rows || !slots || !aligned16(k) || !aligned16(v)) return DSV4_ERR_INVALID;
     if (k_token_stride % 8 || k_head_stride % 8 || v_token_stride % 8 || v_head_stride % 8) return DSV4_ERR_INVALID;
@@ -267,7 +366,10 @@ extern "C" int dsv4_gqa_store(const void* k, int64_t k_token_stride, int64_t k_h
     rc = load_all();
     if (rc) return rc;
     const int d = cache->head_dim;
-    if (cache->format != DSV4_GQA_E4M3) return launch_store<DSV4_GQA_BF16, false>(p, d, stream);
-    return type == DSV4_GQA_BF16 ? launch_store<DSV4_GQA_BF16, true>(p, d, stream)
-                                 : launch_store<DSV4_GQA_F16, true>(p, d, stream);
+    if (cache->format == type) return launch_store<DSV4_GQA_BF16, DSV4_GQA_BF16>(p, d, stream);
+    if (cache->format == DSV4_GQA_E4M3)
+        return type == DSV4_GQA_BF16 ? launch_store<DSV4_GQA_BF16, DSV4_GQA_E4M3>(p, d, stream)
+                                     : launch_store<DSV4_GQA_F16, DSV4_GQA_E4M3>(p, d, stream);
+    return type == DSV4_GQA_BF16 ? launch_store<DSV4_GQA_BF16, DSV4_GQA_E2M1>(p, d, stream)
+                                 : launch_store<DSV4_GQA_F16, DSV4_GQA_E2M1>(p, d, stream);
 }

@@ -1,7 +1,7 @@
 /*
  * dsv4gqa.h - C ABI of the grouped-query cache operators: the write, the
- * one-token attention and the eviction of a paged cache with separate K and V
- * rows.
+ * reading back, the one-token attention and the eviction of a paged cache with
+ * separate K and V rows.
  *
  * They serve a model with ordinary grouped-query heads (num_kv_heads heads
  * with K and V rows of head_dim values, each shared by num_heads /
@@ -20,15 +20,38 @@
  *   row fits (head-major and token-major pages alike); the head_dim values of
  *   a row are contiguous.  A cache of E4M3 rows stands for
  *   code * k_scale[h] (v_scale[h]).
+ *   A row of an E2M1 cache (4.5 bits a value) is head_dim / 2 bytes of codes,
+ *   dim 2 i in the low and dim 2 i + 1 in the high half of byte i, and
+ *   head_dim / 16 e4m3 block scales, one for every 16 dims, in a pool of their
+ *   own: those of slot s start at byte
+ *     page * block_page_stride + h * block_head_stride
+ *     + (s % page_size) * block_row_stride
+ *   of k_blocks (v_blocks).  It stands for code * block scale * k_scale[h]
+ *   (v_scale[h]); a code is a sign (bit 3) and one of the sizes 0, 0.5, 1,
+ *   1.5, 2, 3, 4, 6.
  *
  * dsv4_gqa_store: for i = 0 .. n-1, r = req_rows[i], s = slots[i] and every
  *   KV head h: the K and V rows of token i go to slot s of request row r,
  *   unchanged, or for an E4M3 cache as the e4m3 code nearest to x / scale[h]
- *   (fp32 quotient, ties to even, saturating at +-448; NaN stays NaN).  With
+ *   (fp32 quotient, ties to even, saturating at +-448; NaN stays NaN).  For an
+ *   E2M1 cache, each block of 16 dims, in fp32:
+ *     block scale = the e4m3 value nearest to max |x| / (6 scale[h])
+ *     code        = the e2m1 value nearest to x / (block scale * scale[h])
+ *   (both: ties to even, saturating at 448 and at +-6, so an infinity reads
+ *   back as 6 * 448 * scale[h]).  A block whose scale is 0 has codes 0; one
+ *   that holds a NaN has a NaN for its scale and codes 0: all 16 values read
+ *   back as NaN.  With
  *   `weights`, weights[r][h][s] becomes 0; with `positions`,
  *   positions[r][h][s] becomes token_positions[i].  When two indices address
- *   the same slot, which of their values each 16-byte piece gets is not
- *   defined.
+ *   the same slot, which of their values each 16-byte piece (E2M1: the codes
+ *   and the scale of each block) gets is not defined.
+ *
+ * dsv4_gqa_load: the way back.  For i = 0 .. n-1, r = req_rows[i],
+ *   s = slots[i] and every KV head h: row i of k and of v becomes what slot s
+ *   of request row r stands for: the row unchanged (BF16, F16 caches), or the
+ *   code's value times its scales, in fp32 and rounded to the type of k and v.
+ *   A row that has no place (a request row, slot or page outside the table or
+ *   the pool) becomes zeros and sets DSV4_DEV_ERR_LOAD_ROW.
  *
  * dsv4_gqa_decode: request b (request row r) has n = lens[b] cached rows and
  *   one query row of num_heads heads.  For query head i of KV head
@@ -39,8 +62,8 @@
  *     out = sum_j exp(s_j) V_j / L       lse = ln L
  *   Scores, softmax statistics and sums are fp32, products of 16-bit values
  *   exact; the weight of a row enters its product with V with an error of at
- *   most 2^-17 of it, or 2^-12 where the cache is E4M3 and out bf16, and 2^-36
- *   of the largest weight (F16 and E4M3 caches).
+ *   most 2^-17 of it, or 2^-12 where the cache is E4M3 or E2M1 and out bf16,
+ *   and 2^-36 of the largest weight (F16, E4M3 and E2M1 caches).
  *   A request with no rows gets out = 0 and lse = sink[i] (or -inf).  An
  *   infinite value of an attended V row makes its dim of out infinite (NaN
  *   where both signs or a NaN meet), as the sum does; finite bf16 values must
@@ -123,10 +146,12 @@ extern "C" {
 #define DSV4_GQA_BF16  0
 #define DSV4_GQA_F16   1
 #define DSV4_GQA_E4M3  2   /* cache rows only */
+#define DSV4_GQA_E2M1  4   /* cache rows only: 4-bit codes with block scales */
 
 /* ---- device error bits (dsv4_attn_get_device_error) ---- */
 #define DSV4_DEV_ERR_GQA_PAGE    0x200u  /* a row on a page id outside the pool */
 #define DSV4_DEV_ERR_GQA_LENGTH  0x400u  /* a length outside 0..max_len */
+#define DSV4_DEV_ERR_LOAD_ROW    0x800u  /* dsv4_gqa_load: a row that has no place */
 
 typedef struct dsv4_gqa_cache {
     void*          k;                   /* device, 16-byte aligned */
@@ -142,13 +167,19 @@ typedef struct dsv4_gqa_cache {
     int32_t        num_kv_heads;        /* 1 .. 256 */
     int32_t        head_dim;            /* 64, 128 or 256 */
     int32_t        page_size;           /* a power of two, 16 .. 1024 */
-    int32_t        format;              /* DSV4_GQA_BF16, DSV4_GQA_F16 or DSV4_GQA_E4M3 */
-    const float*   k_scale;             /* device fp32 [num_kv_heads], > 0; E4M3 only, NULL = 1 */
+    int32_t        format;              /* DSV4_GQA_BF16, DSV4_GQA_F16, DSV4_GQA_E4M3 or DSV4_GQA_E2M1 */
+    const float*   k_scale;             /* device fp32 [num_kv_heads], > 0; E4M3 and E2M1 only, NULL = 1 */
     const float*   v_scale;
+    /* E2M1 only (other formats: not read) */
+    void*          k_blocks;            /* device, 16-byte aligned */
+    void*          v_blocks;            /* device, 16-byte aligned, same strides */
+    int64_t        block_page_stride;   /* bytes, multiples of head_dim / 16 */
+    int64_t        block_head_stride;
+    int64_t        block_row_stride;
 } dsv4_gqa_cache;
 
 /* k, v: n tokens (at most 2^30) of num_kv_heads rows, type BF16 or F16 (the cache's own type
-   unless that is E4M3); strides in elements, multiples of 8; 16-byte aligned.
+   unless that is E4M3 or E2M1); strides in elements, multiples of 8; 16-byte aligned.
    weights / positions may be NULL; token_positions int32 [n] goes with
    positions; width as above. */
 int dsv4_gqa_store(const void* k, int64_t k_token_stride, int64_t k_head_stride,
@@ -157,9 +188,17 @@ int dsv4_gqa_store(const void* k, int64_t k_token_stride, int64_t k_head_stride,
                    const dsv4_gqa_cache* cache, float* weights, int32_t* positions, int64_t width,
                    const int32_t* token_positions, void* stream);
 
+/* req_rows, slots: int32 [n], n at most 2^30, any rows and order.  k, v: room
+   for n tokens of num_kv_heads rows, type BF16 or F16 (the cache's own type
+   unless that is E4M3 or E2M1); strides in elements, multiples of 8; 16-byte
+   aligned.  Rows of k and v must not overlap each other or the cache. */
+int dsv4_gqa_load(const int32_t* req_rows, const int32_t* slots, int32_t n, const dsv4_gqa_cache* cache,
+                  void* k, int64_t k_token_stride, int64_t k_head_stride,
+                  void* v, int64_t v_token_stride, int64_t v_head_stride, int32_t type, void* stream);
+
 /* q: batch rows of num_heads * head_dim contiguous values, q_stride elements
    apart (a multiple of 8), type BF16 or F16 (the cache's own type unless that
-   is E4M3), 16-byte aligned.  out: the same type, [batch, num_heads, head_dim]
+   is E4M3 or E2M1), 16-byte aligned.  out: the same type, [batch, num_heads, head_dim]
    contiguous, 16-byte aligned.  sink fp32 [num_heads] or NULL; lse fp32
    [batch, num_heads] or NULL.  num_heads is a multiple of num_kv_heads, at
    most 64 times it.  weights and weights_out: both or neither; they may be

@@ -10,7 +10,62 @@ from __future__ import annotations
 
 import numpy as np
 
-ERR_REQ_ROW, ERR_STORE_ROW, ERR_GQA_PAGE, ERR_GQA_LENGTH = 0x40, 0x80, 0x200, 0x400
+ERR_REQ_ROW, ERR_STORE_ROW, ERR_GQA_PAGE, ERR_GQA_LENGTH, ERR_LOAD_ROW = 0x40, 0x80, 0x200, 0x400, 0x800
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+E4M3 = np.array([(m / 8 if e == 0 else 1 + m / 8) * 2.0 ** (max(e, 1) - 7) for e in range(16) for m in range(8)][:127])
+
+
+def _nearest(grid, x):
+    """Index of the ascending grid's value nearest to x >= 0 (ties to the even index, saturating)."""
+    i = np.clip(np.searchsorted(grid, x), 1, len(grid) - 1)
+    lo, hi = x - grid[i - 1], grid[i] - x
+    return np.where((lo < hi) | ((lo == hi) & (i % 2 == 1)), i - 1, i)
+
+
+def e2m1_pack(x, scale):
+    """(codes, block scales) of rows x [..., D]: bytes [..., D / 2] and e4m3 codes [..., D / 16], as the write defines
+    them: quotients in fp32, then the nearest value.  scale: fp32, broadcast against [..., D / 16]."""
+    x = np.asarray(x, np.float32)
+    x = x.reshape(*x.shape[:-1], -1, 16)
+    scale = np.asarray(scale, np.float32)
+    nan = np.isnan(x).any(-1)
+    top = np.abs(np.where(np.isnan(x), 0, x)).max(-1)
+    with np.errstate(over="ignore", divide="ignore", invalid="ignore"):
+        block = _nearest(E4M3, (top / (np.float32(6) * scale)).astype(np.float64)).astype(np.uint8)
+        step = (E4M3[block].astype(np.float32) * scale)[..., None]
+        q = np.where(step > 0, x / step, np.float32(0))
+        size = np.where(np.isnan(q), 0.0, np.abs(q).astype(np.float64))
+    code = _nearest(E2M1, size).astype(np.uint8) | (np.signbit(x) & (step > 0)).astype(np.uint8) << 3
+    code[nan] = 0
+    block = np.where(nan, 0x7f, block).astype(np.uint8)
+    code = code.reshape(*code.shape[:-2], -1)
+    return code[..., ::2] | code[..., 1::2] << 4, block
+
+
+def e2m1_values(codes, blocks):
+    """Float64 values [..., D] of bytes [..., D / 2] and block scales' e4m3 codes [..., D / 16] (no head's scale)."""
+    codes, blocks = np.asarray(codes), np.asarray(blocks)
+    c = np.stack([codes & 15, codes >> 4], -1).reshape(*blocks.shape, 16)
+    s = np.where(blocks & 127 == 127, np.nan, E4M3[np.minimum(blocks & 127, 126)]) * np.where(blocks & 128, -1.0, 1.0)
+    x = E2M1[c & 7] * np.where(c & 8, -1.0, 1.0) * s[..., None]
+    return x.reshape(*blocks.shape[:-1], -1)
+
+
+def gqa_load(req_rows, slots, cache):
+    """(k, v, error bits): float64 [n, KV heads, D] of what the named slots stand for, heads' scales included."""
+    table, ps = cache["table"], cache["k"].shape[2]
+    n, err = len(slots), 0
+    k, v = (np.zeros((n, cache["k"].shape[1], cache["k"].shape[3])) for _ in range(2))
+    for i, (r, s) in enumerate(zip(req_rows, slots)):
+        page = table[r, s // ps] if 0 <= r < table.shape[0] and 0 <= s < table.shape[1] * ps else -1
+        if not 0 <= page < cache["k"].shape[0]:
+            err = ERR_LOAD_ROW
+            continue
+        for out, pool in ((k, "k"), (v, "v")):
+            scale = cache[pool + "_scale"]
+            out[i] = cache[pool][page, :, s % ps] * (1.0 if scale is None else np.asarray(scale)[:, None])
+    return k, v, err
 
 
 def _request(lens, req, b, rows, max_len):
