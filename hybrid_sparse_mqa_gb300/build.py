@@ -19,7 +19,8 @@ SOURCES = [os.path.join(PKG, "csrc", name) for name in (
 DEPS = SOURCES + [os.path.join(PKG, "csrc", "dsv4_device.cuh"), os.path.join(PKG, "csrc", "dsv4_internal.h"),
                   os.path.join(ROOT, "include", "dsv4attn.h"), os.path.join(ROOT, "include", "dsv4kvstore.h"),
                   os.path.join(ROOT, "include", "dsv4topk.h"), os.path.join(ROOT, "include", "dsv4gqa.h"),
-                  os.path.join(PKG, "csrc", "dsv4_gqa.cuh"), os.path.join(PKG, "csrc", "dsv4_gqa_decode.cuh")]
+                  os.path.join(PKG, "csrc", "dsv4_gqa.cuh"), os.path.join(PKG, "csrc", "dsv4_gqa_decode.cuh"),
+                  os.path.join(PKG, "csrc", "dsv4_gqa_decode4.cuh")]
 LIB = os.path.join(PKG, "libdsv4attn.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

@@ -5,7 +5,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "dsv4_gqa_decode.cuh"
+#include "dsv4_gqa_decode4.cuh"
 
 namespace dsv4 {
 namespace gqa {
@@ -293,10 +293,12 @@ std::atomic<int> g_claim_ahead{kClaimAhead}, g_claim_polls{kWaitLimit};
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct Plan {
-    int group, nt, chunks, tt, min_tiles;
+    int group, nt, chunks, min_tiles;
+    int tt, list_tt;                       // slots of a tile: of a cluster's, of the list's
     long long tiles;                       // bound on the tile list
     int places;                            // CTAs that run at once
     int ctas, claims;                      // resident CTAs of the attention kernel, and claimable ones
+    int warps;                             // that take a share each (4-bit rows: CTAs)
     size_t part_o, part_ml, lse2, info, logits, bytes;      // offsets, size
 };
 
@@ -313,20 +315,26 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
     const long long segments = (long long)batch * c->num_kv_heads * pl.chunks;
     pl.tiles = segments * ((max_len + pl.tt - 1) / pl.tt);
     if (pl.tiles >= 1LL << 31 || segments > kMostSlots) return DSV4_ERR_UNSUPPORTED;
+    // (lists of rows of 4 bits, 8 heads at most: dsv4_gqa_decode4.cuh)
+    const bool four = c->format == DSV4_GQA_E2M1 && c->head_dim <= 128 && pl.nt == 1;
+    pl.list_tt = four ? kTile4 : pl.tt;
+    pl.tiles = segments * ((max_len + pl.list_tt - 1) / pl.list_tt);
     // (512-byte rows: one CTA's ring fills an SM's shared memory)
     const int most = row_bytes(c) > 256 ? kMaxCtas / 2 : kMaxCtas;
     pl.places = most;
-    pl.min_tiles = (max_len + pl.tt - 1) / pl.tt <= kFewTiles ? 1 : 2;
+    pl.min_tiles = four || (max_len + pl.tt - 1) / pl.tt <= kFewTiles ? 1 : 2;
+    const int list_most = four ? kMaxCtas : most;
     const long long want = pl.tiles / pl.min_tiles;
-    pl.ctas = want < 1 ? 1 : (want < most ? static_cast<int>(want) : most);
-    pl.claims = pl.ctas == most && pl.tiles >= (long long)most * kWarps * kClaimTiles ? most : 0;
-    const size_t entries = size_t(2) * (pl.ctas + pl.claims) * kWarps * 8 * pl.nt;
+    pl.ctas = want < 1 ? 1 : (want < list_most ? static_cast<int>(want) : list_most);
+    pl.claims = !four && pl.ctas == most && pl.tiles >= (long long)most * kWarps * kClaimTiles ? most : 0;
+    pl.warps = pl.ctas * (four ? 1 : kWarps);
+    const size_t entries = size_t(2) * (pl.warps + pl.claims * kWarps) * 8 * pl.nt;
     pl.part_o = 0;
     pl.part_ml = pl.part_o + up256(entries * c->head_dim * sizeof(float));
     pl.lse2 = pl.part_ml + up256(entries * sizeof(float2));
     pl.info = pl.lse2 + (weights ? up256(size_t(batch) * heads * sizeof(float)) : 0);
     pl.logits = pl.info + (weights ? up256(size_t(batch) * sizeof(int4)) : 0);
-    pl.bytes = pl.logits + (weights ? size_t(pl.tiles) * pl.tt * 8 * pl.nt * sizeof(float) : 0);
+    pl.bytes = pl.logits + (weights ? size_t(pl.tiles) * pl.list_tt * 8 * pl.nt * sizeof(float) : 0);
     return DSV4_OK;
 }
 
@@ -401,6 +409,7 @@ int load_join() {
     return once_per_device(ready, [] { return load_join_heads<D, TT, 8>() && load_join_heads<D, TT, 16>(); });
 }
 int load_joins(int d, int tt) {
+    if (tt == kTile4) return d == 64 ? load_join<64, kTile4>() : load_join<128, kTile4>();
     if (d == 64) return tt == 32 ? load_join<64, 32>() : load_join<64, 64>();
     if (d == 128) return tt == 16 ? load_join<128, 16>() : load_join<128, 32>();
     return load_join<256, 16>();
@@ -471,7 +480,7 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
     p.width = width;
     p.decay = decay;
     p.min_tiles = pl.min_tiles;
-    p.warps = pl.ctas * kWarps;
+    p.warps = pl.warps;
     p.claims = pl.claims;
     p.claim_ahead = g_claim_ahead.load(std::memory_order_relaxed);
     p.claim_polls = g_claim_polls.load(std::memory_order_relaxed);
@@ -482,6 +491,7 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
 
     const int d = cache->head_dim;
     rc = load_joins(d, pl.tt);
+    if (!rc && cache->format == DSV4_GQA_E2M1 && d <= 128) rc = load_joins(d, kTile4);
     if (rc) return rc;
     rc = cache->format == DSV4_GQA_BF16  ? launch_decode_bf16(p, d, pl.nt, stream)
          : cache->format == DSV4_GQA_F16 ? launch_decode_f16(p, d, pl.nt, stream)
@@ -489,16 +499,19 @@ int dsv4_gqa_decode(const void* q, int64_t q_stride, int32_t type, int32_t batch
              ? (p.q_bf16 ? launch_decode_e4m3(p, d, pl.nt, stream) : launch_decode_e4m3_f16(p, d, pl.nt, stream))
              : (p.q_bf16 ? launch_decode_e2m1(p, d, pl.nt, stream) : launch_decode_e2m1_f16(p, d, pl.nt, stream));
     if (rc || p.cluster) return rc;
-    if (d == 64)
+    if (pl.list_tt == kTile4)
+        rc = d == 64 ? launch_join<64, kTile4>(p, pl.nt, stream) : launch_join<128, kTile4>(p, pl.nt, stream);
+    else if (d == 64)
         rc = pl.tt == 32 ? launch_join<64, 32>(p, pl.nt, stream) : launch_join<64, 64>(p, pl.nt, stream);
     else if (d == 128)
         rc = pl.tt == 16 ? launch_join<128, 16>(p, pl.nt, stream) : launch_join<128, 32>(p, pl.nt, stream);
     else
         rc = launch_join<256, 16>(p, pl.nt, stream);
     if (rc || !weights) return rc;
-    return pl.tt == 16   ? launch_weights<16>(p, pl.nt, stream)
-           : pl.tt == 32 ? launch_weights<32>(p, pl.nt, stream)
-                         : launch_weights<64>(p, pl.nt, stream);
+    return pl.list_tt == kTile4 ? launch_weights<kTile4>(p, pl.nt, stream)
+           : pl.tt == 16        ? launch_weights<16>(p, pl.nt, stream)
+           : pl.tt == 32        ? launch_weights<32>(p, pl.nt, stream)
+                                : launch_weights<64>(p, pl.nt, stream);
 }
 
 }  // extern "C"

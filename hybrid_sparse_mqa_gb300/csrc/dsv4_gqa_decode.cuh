@@ -339,6 +339,7 @@ struct Shape {
     // output's: 8 x 1024..16384 e4m3 rows of 128, 32 / 4 heads, f16 out: an error of 5.7e-6 (rms) with one piece and of
     // 4.3e-6, the output's own rounding, with two
     static constexpr bool TWO = !CODES || !QBF16;
+    static constexpr bool LIST = !(FP4 && D <= 128 && NT == 1);      // else dsv4_gqa_decode4.cuh takes the lists
     static constexpr int ROWB = FP4 ? D / 2 : D * (FP8 ? 1 : 2);       // bytes of a row
     static constexpr int BLKB = FP4 ? D / 16 : 0;            // bytes of its block scales
     static constexpr int TT = FP4 ? 2048 / ROWB : 4096 / ROWB < 16 ? 16 : 4096 / ROWB;
@@ -1370,17 +1371,23 @@ inline int launch_decode_shape(const DecodeParams& p, void* stream) {
     if (p.cluster)
         return launch(dsv4_gqa_decode_kernel<S, true>, dim3(p.batch * p.c.kv_heads * p.chunks * p.cluster), S::W * 32,
                       S::SMEM, stream, p.cluster, p);
-    return launch(dsv4_gqa_decode_kernel<S, false>, dim3(p.warps / S::W + p.claims), S::W * 32, S::SMEM, stream, 1, p);
+    if constexpr (!S::LIST)
+        return DSV4_ERR_INVALID;
+    else
+        return launch(dsv4_gqa_decode_kernel<S, false>, dim3(p.warps / S::W + p.claims), S::W * 32, S::SMEM, stream, 1, p);
 }
 
 // shared memory beyond 48 KB is asked for once (which loads the kernel)
 template <class S>
 inline bool prepare_decode_shape() {
-    return cudaFuncSetAttribute(dsv4_gqa_decode_kernel<S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) ==
+    if constexpr (S::LIST)
+        if (cudaFuncSetAttribute(dsv4_gqa_decode_kernel<S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) !=
+                cudaSuccess ||
+            !load_kernels(dsv4_gqa_decode_kernel<S, false>))
+            return false;
+    return cudaFuncSetAttribute(dsv4_gqa_decode_kernel<S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) ==
                cudaSuccess &&
-           cudaFuncSetAttribute(dsv4_gqa_decode_kernel<S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) ==
-               cudaSuccess &&
-           load_kernels(dsv4_gqa_decode_kernel<S, false>, dsv4_gqa_decode_kernel<S, true>);
+           load_kernels(dsv4_gqa_decode_kernel<S, true>);
 }
 
 template <int KIND, int QKIND, int D>
