@@ -28,9 +28,9 @@
 // warps look through the scales of each tile; a NaN block is noted and its scale
 // zeroed, a negative scale's sign moves into its codes.
 //
-// Roles of the 10 warps: 0 .. 3 softmax and output (a thread is a slot of S, a
-// query dim and a dim of O), 4 .. 7 copy (cp.async into a ring whose entries are
-// K and V of a tile in turn), 8 issues S, 9 V^T and O.  Two CTAs an SM.
+// Roles of the 8 warps: 0 .. 3 softmax and output (a thread is a slot of S and
+// a dim of O), 4 and 5 copy (cp.async into a ring whose entries are K and V of a
+// tile in turn), 6 issues S, 7 V^T and O.  Two CTAs an SM.
 //
 // An MMA here costs 9 (tf32, N = 16), 17 (N = 32), 48 (4 bits, N = 64) and
 // 64 clk (identity, N = 128) when its issuer is one thread that elect.sync picked
@@ -46,7 +46,7 @@ namespace dsv4 {
 namespace gqa {
 
 constexpr int kTile4 = 128;                // slots
-constexpr int kThreads4 = 320;
+constexpr int kThreads4 = 256;
 constexpr int kRing4 = 16;                 // tiles whose notes are kept: more than the copies are ahead
 // Sums stay in the accumulator for so many tiles: it truncates, 16 times a tile, and what that loses is below 2^-16 of
 // the sum this way, however long the list.
@@ -170,16 +170,24 @@ __device__ __forceinline__ uint32_t to_tf32(float x) {
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
     return r;
 }
-// Eight values, integers of -4 .. 4, as e2m1 codes.
-__device__ __forceinline__ uint32_t digits_e2m1(const float (&v)[8]) {
-    uint32_t r;
-    asm("{\n .reg .b8 a, b, c, d;\n"
-        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
-        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
-        " mov.b32 %0, {a, b, c, d};\n}\n"
-        : "=r"(r)
-        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+__device__ __forceinline__ uint64_t f32_pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
     return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// An integer of -4 .. 4 as an e2m1 code.
+__device__ __forceinline__ uint32_t digit_e2m1(int d) {
+    const int a = abs(d);
+    return static_cast<uint32_t>(min(2 * a, a + 2)) | (static_cast<uint32_t>(d) >> 28 & 8u);
+}
+// 4-byte global -> shared copy; src_bytes = 0 writes zeros and reads nothing.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 
 // What a CTA's warps tell each other.
@@ -191,10 +199,10 @@ struct Notes {
     uint64_t drained;
     uint32_t tmem;
     int abort, fresh;                                        // P's tile begins a new sum in O
-    uint8_t ok[kRing4][4];                                   // of tiles: valid 16-slot groups, two bits for each copying warp
+    uint8_t ok[kRing4][2];                                   // of tiles: valid 16-slot groups, four bits for each copying warp
     uint16_t nan[kRing4];                                    // and blocks of V that hold a NaN
     alignas(16) float mul[2][S::HEADS];                      // score factors, by parity of the piece (read as float4)
-    alignas(16) float ref[S::HEADS];
+    float odd[2][S::HEADS];                                  // NaN for a head whose query is not finite, else 0
     float sum[4][S::HEADS], top[4][S::HEADS];
 };
 
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
     extern __shared__ __align__(1024) uint8_t smem4[];
     uint8_t* smem = smem4;
     using N = Notes<S>;
-    static_assert(sizeof(N) <= S::NOTES && offsetof(N, mul) % 16 == 0 && offsetof(N, ref) % 16 == 0 && S::O_NOTES % 16 == 0,
+    static_assert(sizeof(N) <= S::NOTES && offsetof(N, mul) % 16 == 0 && S::O_NOTES % 16 == 0,
                   "notes");
     N& notes = *reinterpret_cast<N*>(smem + S::O_NOTES);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -213,11 +221,11 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
     auto bar = [&](uint64_t& b) { return smem_u32(&b); };
 
     // ---- what does not depend on the call's data ----
-    if (warp == 9) tmem_alloc(smem_u32(&notes.tmem), S::COLS);
+    if (warp == 7) tmem_alloc(smem_u32(&notes.tmem), S::COLS);
     if (tid == 0) {
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-            mbar_init(bar(notes.full[e]), 128 + 4);
+            mbar_init(bar(notes.full[e]), 64 + 2);
             mbar_init(bar(notes.empty[e]), 1);
         }
         mbar_init(bar(notes.s_go), 128);
@@ -252,7 +260,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
     grid_dependents_go();
 
     // ---- this CTA's share ----
-    const int hcs = p.c.kv_heads * p.chunks;
+    const int hcs = p.c.kv_heads;              // (one group of query heads each)
     unsigned err = 0;
     auto request_of = [&](int b) {
         Request r{0, 0};
@@ -292,81 +300,102 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
         __syncwarp();
     };
 
-    if (warp >= 4 && warp < 8) {
+    if (warp == 4 || warp == 5) {
         // ============================================================ copies
+        // A warp copies 64 slots of every tile: four groups of 16, each on one page.
         if (tiles > 0) {
             const int w = warp - 4;
             constexpr int PPR = ROWB / 16, RPI = 32 / PPR;             // pieces of a row, rows per warp-wide copy
             const int lane_row = lane / PPR, lane_piece = lane % PPR;
             const int page_mask = (1 << p.c.page_shift) - 1;
-            const uint64_t policy = read_policy(p.chunks == 1);
+            const long long lane_off = lane_row * p.c.row_stride + lane_piece * 16, step = RPI * p.c.row_stride;
+            const long long lane_block = (lane & 15) * p.c.b_row_stride;
+            const uint32_t dst0 = 64 * w * ROWB + row_offset<ROWB>(lane_row, lane_piece * 16);
+            const uint32_t dst1 = kTile4 * ROWB + lane * 16 + w * 8;
             Cursor<kTile4> at;
             at.at = t0;
             at.locate(p, hcs, lane, early, request_of);
             at.bound(t1);
-            // lanes 0 and 1: the page of one 16-slot group of the tile, and whether it holds slots to attend
+            // lanes 0 .. 3: the page of a group of the tile, and whether it holds slots to attend
             int page = -1;
             bool wanted = false;
+            auto slot_of = [&]() { return (at.rg.lo / kTile4 + static_cast<int>(at.at - at.seg)) * kTile4 + 64 * w; };
             auto look = [&]() {
-                const int slot = (at.rg.lo / kTile4 + static_cast<int>(at.at - at.seg)) * kTile4 + (2 * w + lane) * 16;
+                const int slot = slot_of() + lane * 16;
                 page = -1;
-                wanted = lane < 2 && slot < at.rg.n && slot + 16 > at.rg.lo;
+                wanted = lane < 4 && slot < at.rg.n && slot + 16 > at.rg.lo;
                 if (wanted) page = __ldg(p.c.table + (long long)at.rq.row * p.c.table_stride + (slot >> p.c.page_shift));
             };
             look();
+            int e = 0;
+            uint32_t turn = 1;                     // parity that an entry's last reading has; 1: nothing was there
             for (int i = 0; i < tiles; ++i) {
-                const int slot0 = (at.rg.lo / kTile4 + static_cast<int>(at.at - at.seg)) * kTile4 + 32 * w;
-                const int lo = at.rg.lo, n = at.rg.n, h = at.hc / p.chunks;
+                const int slot0 = slot_of(), lo = at.rg.lo, n = at.rg.n;
                 const bool valid = page >= 0 && page < p.c.num_pages;
                 if (wanted && !valid) atomicOr(p.err, DSV4_DEV_ERR_GQA_PAGE);
                 const unsigned okm = __ballot_sync(0xffffffffu, wanted && valid);
-                int pg[2];
-                pg[0] = __shfl_sync(0xffffffffu, page, 0);
-                pg[1] = __shfl_sync(0xffffffffu, page, 1);
+                const int in_page = slot0 + lane * 16 & page_mask;
+                const long long off = valid ? page * p.c.page_stride + at.hc * p.c.head_stride + in_page * p.c.row_stride : 0;
+                const long long block_off =
+                    valid ? page * p.c.b_page_stride + at.hc * p.c.b_head_stride + in_page * p.c.b_row_stride : 0;
+                long long go[4], bo[2];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) go[g] = __shfl_sync(0xffffffffu, off, g) + lane_off;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) bo[u] = __shfl_sync(0xffffffffu, block_off, 2 * u + (lane >> 4)) + lane_block;
+                const bool whole = okm == 15u && slot0 >= lo && slot0 + 64 <= n;
                 // the next tile's pages are on their way while this one's entries are waited for
                 ++at.at;
                 if (at.at < at.end || at.next_segment(p, hcs, t1)) look();
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    const int e = (2 * i + kv) % NE, use = (2 * i + kv) / NE;
-                    if (use > 0) {
-                        warp_wait(notes.empty[e], (use - 1) & 1);
-                        fence_proxy_async();
-                    }
+                    warp_wait(notes.empty[e], turn);
+                    fence_proxy_async();
                     if (kv == 0 && lane == 0) *(volatile uint8_t*)&notes.ok[i % kRing4][w] = okm;
                     const uint32_t dst = ring + e * S::ENTRY;
-                    const uint8_t* pool = kv ? p.c.v : p.c.k;
-                    const uint8_t* blocks = kv ? p.c.vb : p.c.kb;
-                    {
-                        // a lane's row: its block scales, 4 of them to a line of each K step
-                        const int s = slot0 + lane, g = lane >> 4;
-                        const bool in = (okm >> g & 1) && s >= lo && s < n;
-                        const uint8_t* src =
-                            in ? blocks + (g ? pg[1] : pg[0]) * p.c.b_page_stride + h * p.c.b_head_stride +
-                                     (s & page_mask) * p.c.b_row_stride
-                               : blocks;
+                    const uint8_t *pool = kv ? p.c.v : p.c.k, *blocks = kv ? p.c.vb : p.c.kb;
+                    // lane's rows lane and 32 + lane: block scales, 4 of them to a line of each K step
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int s = slot0 + 32 * u + lane;
+                        const bool in = whole || ((okm >> (2 * u + (lane >> 4)) & 1) && s >= lo && s < n);
+                        const uint8_t* src = blocks + (in ? bo[u] : 0);
 #pragma unroll
                         for (int k = 0; k < KS; ++k)
-                            cp_async_hint<4>(dst + kTile4 * ROWB + 512 * k + lane * 16 + w * 4, src + (in ? 4 * k : 0),
-                                             in ? 4u : 0u, policy);
+                            cp_async_4(dst + dst1 + 512 * k + 4 * u, src + (in ? 4 * k : 0), in ? 4u : 0u);
                     }
+                    if (whole) {
 #pragma unroll
-                    for (int j = 0; j < 32 / RPI; ++j) {
-                        const int r = j * RPI + lane_row, g = j * RPI >> 4, s = slot0 + r;
-                        const bool in = (okm >> g & 1) && s >= lo && s < n;
-                        const uint8_t* src = in ? pool + pg[g] * p.c.page_stride + h * p.c.head_stride +
-                                                      (s & page_mask) * p.c.row_stride + lane_piece * 16
-                                                : pool;
-                        cp_async_16_hint(dst + row_offset<ROWB>(32 * w + r, lane_piece * 16), src, in ? 16u : 0u, policy);
+                        for (int g = 0; g < 4; ++g) {
+                            const uint8_t* src = pool + go[g];
+#pragma unroll
+                            for (int j = 0; j < 16 / RPI; ++j) {
+                                cp_async_16(dst + dst0 + (16 * g + j * RPI) * ROWB, src, 16u);
+                                src += step;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+#pragma unroll
+                            for (int j = 0; j < 16 / RPI; ++j) {
+                                const int s = slot0 + 16 * g + j * RPI + lane_row;
+                                const bool in = (okm >> g & 1) && s >= lo && s < n;
+                                cp_async_16(dst + dst0 + (16 * g + j * RPI) * ROWB, pool + (in ? go[g] + j * step : 0), in ? 16u : 0u);
+                            }
                     }
                     cp_async_arrive_noinc(bar(notes.full[e]));
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(notes.full[e]));
+                    if (++e == NE) {
+                        e = 0;
+                        turn ^= 1;
+                    }
                 }
             }
             cp_async_wait_all();
         }
-    } else if (warp == 8) {
+    } else if (warp == 6) {
         // ============================================================ S
         constexpr uint32_t idesc = idesc_e2m1(128, S::NS);
         for (int i = 0; i < tiles; ++i) {
@@ -409,7 +438,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
         }
         if (elect_one()) mma_commit(bar(notes.drained));
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 7) {
         // ============================================================ V^T and O
         constexpr uint32_t idesc_v = idesc_e2m1(128, kTile4), idesc_o = idesc_tf32(128, NP);
         for (int i = 0; i < tiles; ++i) {
@@ -474,7 +503,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
         __syncwarp();
     } else if (tiles > 0) {
         // ============================================================ softmax and output
-        const uint32_t lane_t = tmem + (warp * 32u << 16);
+        const uint32_t lane_t = tmem + (warp * 32u << 16), p_to = s_p + warp * NP * 128 + (lane & 3) * 4;
         Cursor<kTile4> at;
         at.at = t0;
         at.locate(p, hcs, lane, early, request_of);
@@ -486,10 +515,10 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
         const int q_head = tid / TPH, q_dim = tid % TPH * DP;
         float kscale = 1.f;
         auto load_q = [&](const Cursor<kTile4>& of) {
-            const int h = of.hc / p.chunks, chunk = of.hc % p.chunks;
-            const bool have = chunk * HEADS + q_head < p.group;
+            const int h = of.hc;
+            const bool have = q_head < p.group;
             const uint16_t* from = static_cast<const uint16_t*>(p.q) + of.b * p.q_stride +
-                                   (long long)(h * p.group + chunk * HEADS + q_head) * D + q_dim;
+                                   (long long)(h * p.group + q_head) * D + q_dim;
             if constexpr (NW == 2) {
                 const uint2 x = have ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0, 0);
                 qw[0] = x.x; qw[1] = x.y;
@@ -528,22 +557,24 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    float d[8];
+                    uint32_t codes = 0;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        d[j] = rintf(y[j]);
-                        y[j] = (y[j] - d[j]) * 8.f;
+                        const int d = __float2int_rn(y[j]);
+                        y[j] = (y[j] - static_cast<float>(d)) * 8.f;
+                        codes |= digit_e2m1(d) << 4 * j;
                     }
-                    const uint32_t codes = digits_e2m1(d);
                     uint8_t* to = smem + S::O_Q + row_offset<ROWB>(k * HEADS + q_head, (q_dim + 2 * k0) / 2);
                     if constexpr (NW == 2) *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(codes);
                     else *reinterpret_cast<uint32_t*>(to) = codes;
                 }
             }
-            // (a head with a value that is not finite has no finite score)
-            if (tid % TPH == 0)
+            // (a head with a value that is not finite has no finite score: its sums become NaN)
+            if (tid % TPH == 0) {
                 notes.mul[parity][q_head] =
-                    bad ? NAN : p.scale_log2 * kscale * __uint_as_float(static_cast<uint32_t>(126 + e) << 23);
+                    bad ? 0.f : p.scale_log2 * kscale * __uint_as_float(static_cast<uint32_t>(126 + e) << 23);
+                notes.odd[parity][q_head] = bad ? NAN : 0.f;
+            }
             fence_proxy_async();
         };
 
@@ -553,6 +584,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
         softmax_sync();                            // (factors)
 
         float o[HEADS], lsum[HEADS];               // sums taken out of the accumulator; of this thread's weights
+        float ref[HEADS];                          // the softmax's references, the same in all threads
         uint32_t nan = 0;
         int parity = 0, kept = 0;                  // kept: tiles in the accumulator
         bool starts = true;
@@ -573,26 +605,29 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
         for (int i = 0; i < tiles; ++i) {
             if (starts) {
 #pragma unroll
-                for (int c = 0; c < HEADS; ++c) o[c] = lsum[c] = 0.f;
+                for (int c = 0; c < HEADS; ++c) {
+                    o[c] = lsum[c] = 0.f;
+                    ref[c] = kNoMax;
+                }
                 nan = 0;
                 kept = 0;
             }
             const unsigned tile = at.at;
             const bool ends = tile + 1 == at.end;
-            Cursor<kTile4> next = at;
-            bool more = true;
+            const int slot = (at.rg.lo / kTile4 + static_cast<int>(tile - at.seg)) * kTile4 + tid, lo = at.rg.lo, n = at.rg.n;
+            Cursor<kTile4> next;                   // (read where the piece ends)
+            bool more = false;
             if (ends) {
+                next = at;
                 more = next.next_segment(p, hcs, t1);
                 if (more) load_q(next);
-            } else {
-                ++next.at;
             }
-            const int slot = (at.rg.lo / kTile4 + static_cast<int>(tile - at.seg)) * kTile4 + tid;
 
-            // S: the digits' columns, the smallest weight first
+            // S: the digits' columns, the smallest weight first, heads in pairs
             warp_wait(notes.s_full, i & 1);
             tc_fence_after();
-            float s[HEADS];
+            uint64_t s2[HEADS / 2];
+            const uint64_t eighth = f32_pair(0.125f, 0.125f);
 #pragma unroll
             for (int part = S::NS / 32 - 1; part >= 0; --part) {
                 float x[32];
@@ -600,38 +635,39 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
 #pragma unroll
                 for (int g = 32 / HEADS - 1; g >= 0; --g)
 #pragma unroll
-                    for (int c = 0; c < HEADS; ++c)
-                        s[c] = part == S::NS / 32 - 1 && g == 32 / HEADS - 1 ? x[g * HEADS + c]
-                                                                             : s[c] * 0.125f + x[g * HEADS + c];
+                    for (int c = 0; c < HEADS; c += 2) {
+                        const uint64_t y = f32_pair(x[g * HEADS + c], x[g * HEADS + c + 1]);
+                        s2[c / 2] = part == S::NS / 32 - 1 && g == 32 / HEADS - 1 ? y : fma_pair(s2[c / 2], eighth, y);
+                    }
             }
             tc_fence_before();
-            if (!more || !ends) {
-                mbar_arrive(bar(notes.s_go));
-            } else {
-                write_q(parity ^ 1);
-                mbar_arrive(bar(notes.s_go));
-            }
-            const bool in = slot >= at.rg.lo && slot < at.rg.n &&
-                            (*(volatile uint8_t*)&notes.ok[i % kRing4][warp] >> (lane >> 4) & 1);
+            if (more) write_q(parity ^ 1);
+            mbar_arrive(bar(notes.s_go));
+            // log2-unit scores below their reference
+            const bool in = slot >= lo && slot < n &&
+                            (*(volatile uint8_t*)&notes.ok[i % kRing4][warp >> 1] >> ((warp & 1) * 2 + (lane >> 4)) & 1);
+            float s[HEADS], x[HEADS], mul[HEADS];
             bool above = false;
-            float ref[HEADS];
 #pragma unroll
             for (int c = 0; c < HEADS; c += 4) {
                 const float4 m = *reinterpret_cast<const float4*>(&notes.mul[parity][c]);
-                const float4 r = starts ? make_float4(kNoMax, kNoMax, kNoMax, kNoMax)
-                                        : *reinterpret_cast<const float4*>(&notes.ref[c]);
-                const float mm[4] = {m.x, m.y, m.z, m.w}, rr[4] = {r.x, r.y, r.z, r.w};
+                mul[c] = m.x; mul[c + 1] = m.y; mul[c + 2] = m.z; mul[c + 3] = m.w;
+            }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    s[c + k] = in ? s[c + k] * mm[k] : -INFINITY;
-                    ref[c + k] = rr[k];
-                    above |= s[c + k] > __fadd_rd(rr[k], 8.f);
-                }
+            for (int c = 0; c < HEADS; ++c) {
+                asm("{\n .reg .b32 h;\n mov.b64 {%0, h}, %1;\n}\n" : "=f"(s[c]) : "l"(c & 1 ? s2[c / 2] >> 32 : s2[c / 2]));
+                x[c] = in ? fmaf(s[c], mul[c], -ref[c]) : -INFINITY;
+                above |= x[c] > 8.f;
             }
             if (p.logits) {
                 float4* to = reinterpret_cast<float4*>(p.logits + ((size_t)tile * kTile4 + tid) * HEADS);
 #pragma unroll
-                for (int c = 0; c < HEADS; c += 4) to[c / 4] = make_float4(s[c], s[c + 1], s[c + 2], s[c + 3]);
+                for (int c = 0; c < HEADS; c += 4) {
+                    float y[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k] = in ? s[c + k] * mul[c + k] : -INFINITY;
+                    to[c / 4] = make_float4(y[0], y[1], y[2], y[3]);
+                }
             }
             const bool moves = softmax_any(above);
             if (i > 0 && !starts) {
@@ -643,12 +679,12 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                 }
                 nan |= *(volatile uint16_t*)&notes.nan[(i - 1) % kRing4];
             }
-            if (moves || starts) {
+            if (moves) {
 #pragma unroll
                 for (int c = 0; c < HEADS; ++c) {
                     // the warp's largest score, as an integer of the same order (a NaN counts as -inf)
-                    const int x = __float_as_int(fmaxf(s[c], -INFINITY));
-                    const int m = __reduce_max_sync(0xffffffffu, x ^ (x >> 31 & 0x7fffffff));
+                    const int y = __float_as_int(in ? fmaxf(s[c] * mul[c], -INFINITY) : -INFINITY);
+                    const int m = __reduce_max_sync(0xffffffffu, y ^ (y >> 31 & 0x7fffffff));
                     if (lane == 0) notes.top[warp][c] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
                 }
                 softmax_sync();
@@ -659,26 +695,20 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                     ref[c] = r;
                     lsum[c] *= f;
                     o[c] *= f;
+                    x[c] = in ? fmaf(s[c], mul[c], -r) : -INFINITY;
                 }
-                if (lane < HEADS && warp == 0) {
-                    float r = 0.f;
-#pragma unroll
-                    for (int c = 0; c < HEADS; ++c) r = lane == c ? ref[c] : r;
-                    notes.ref[lane] = r;
-                }
-                softmax_sync();
+                // (the next tile's vote lies between this reading and the next writing)
             }
             // P, head by head a line of 32 slots
-            const uint32_t to = s_p + warp * NP * 128 + (lane & 3) * 4;
 #pragma unroll
             for (int c = 0; c < HEADS; ++c) {
-                const float x = fast_exp2(s[c] - ref[c]);
-                lsum[c] += x;
-                const uint32_t hi = to_tf32(x);
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + c * 128 + (((lane >> 2) ^ (c & 7)) << 4)), "r"(hi) : "memory");
+                const uint32_t to = p_to + c * 128 + (((lane >> 2) ^ c) << 4);
+                const float y = fast_exp2(x[c]);
+                lsum[c] += y;
+                const uint32_t hi = to_tf32(y);
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
                 if constexpr (S::TWO)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + (HEADS + c) * 128 + (((lane >> 2) ^ (c & 7)) << 4)),
-                                 "r"(__float_as_uint(x - __uint_as_float(hi)))
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + HEADS * 128), "r"(__float_as_uint(y - __uint_as_float(hi)))
                                  : "memory");
             }
             if (tid == 0) *(volatile int*)&notes.fresh = kept == 0;
@@ -687,15 +717,14 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             mbar_arrive(bar(notes.p_full));
             starts = ends;
             if (!ends) {
-                at = next;
+                ++at.at;
                 continue;
             }
 
             // ---- the piece's sums, and its output ----
             const bool cut = at.end != at.seg + at.rg.tiles || at.seg < t0;
             const bool begins = at.seg >= t0;
-            const int h = at.hc / p.chunks, chunk = at.hc % p.chunks;
-            const int head0 = h * p.group + chunk * HEADS, nheads = min(HEADS, p.group - chunk * HEADS);
+            const int h = at.hc, head0 = h * p.group, nheads = p.group;
 #pragma unroll
             for (int c = 0; c < HEADS; ++c) {
                 float x = lsum[c];
@@ -712,7 +741,8 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
 #pragma unroll
             for (int c = 0; c < HEADS; ++c) {
                 if (c >= nheads) break;
-                const float l = (notes.sum[0][c] + notes.sum[1][c]) + (notes.sum[2][c] + notes.sum[3][c]);
+                float l = (notes.sum[0][c] + notes.sum[1][c]) + (notes.sum[2][c] + notes.sum[3][c]);
+                if (l > 0.f) l += notes.odd[parity][c];
                 float inv = 1.f;
                 if (!cut) {
                     const float sk = p.sink ? __ldg(p.sink + head0 + c) * kLog2e : -INFINITY;
@@ -730,7 +760,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                     p.part_ml[(size_t)entry * HEADS + c] = make_float2(ref[c], l);
                 }
                 if (tid >= D) continue;
-                const float x = nan >> (tid >> 4) & 1 ? NAN : o[c] * inv;
+                const float x = nan >> (tid >> 4) & 1 || l != l ? NAN : o[c] * inv;
                 if (cut)
                     p.part_o[((size_t)entry * HEADS + c) * D + tid] = x;
                 else
@@ -745,7 +775,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
     }
 
     // every MMA and copy has ended before shared memory and TMEM go
-    if (warp == 9) {
+    if (warp == 7) {
         const uint64_t since = globaltimer_ns();
         while (!mbar_try(bar(notes.drained), 0))
             if (globaltimer_ns() - since > kWaitNs4) break;
@@ -754,7 +784,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tmem, S::COLS);
+    if (warp == 7) tmem_dealloc(tmem, S::COLS);
 }
 
 template <class S>
