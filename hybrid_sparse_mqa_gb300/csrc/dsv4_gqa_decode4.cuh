@@ -28,9 +28,12 @@
 // warps look through the scales of each tile; a NaN block is noted and its scale
 // zeroed, a negative scale's sign moves into its codes.
 //
-// Roles of the 8 warps: 0 .. 3 softmax and output (a thread is a slot of S and
-// a dim of O), 4 and 5 copy (cp.async into a ring whose entries are K and V of a
-// tile in turn), 6 issues S, 7 V^T and O.  Two CTAs an SM.
+// Roles of the 14 warps: 0 .. 3 and 4 .. 7 softmax of the even and of the odd
+// tiles (a thread is a slot of S and a dim of O), each with references, sums and
+// an O of its own, which meet at the end of a segment's part; 8 .. 11 copy
+// (cp.async into a ring whose entries are K and V of a tile in turn); 12 looks
+// through the scales and issues S, 13 V^T and O.  Two CTAs an SM.  (One softmax
+// group: a tile's chain of waits and steps took 2300 clk of it.)
 //
 // An MMA here costs 9 (tf32, N = 16), 17 (N = 32), 48 (4 bits, N = 64) and
 // 64 clk (identity, N = 128) when its issuer is one thread that elect.sync picked
@@ -46,7 +49,7 @@ namespace dsv4 {
 namespace gqa {
 
 constexpr int kTile4 = 128;                // slots
-constexpr int kThreads4 = 256;
+constexpr int kThreads4 = 448;
 constexpr int kRing4 = 16;                 // tiles whose notes are kept: more than the copies are ahead
 // Sums stay in the accumulator for so many tiles: it truncates, 16 times a tile, and what that loses is below 2^-16 of
 // the sum this way, however long the list.
@@ -58,32 +61,37 @@ struct Shape4 {
     static constexpr int D = D_, HEADS = 8;
     static constexpr bool QBF16 = QKIND == DSV4_GQA_BF16, TWO = !QBF16;
     static constexpr int KS = D / 64;                        // K steps of S, and of V^T
-    static constexpr int DIGITS = 8, NS = DIGITS * HEADS;    // columns of S
+    static constexpr int NS = 32;                            // columns of S: four pairs of digits of the heads
     static constexpr int USED = HEADS * (TWO ? 2 : 1);       // columns of O: heads, once for each piece of P
-    static constexpr int NP = 16;                            // and of its MMA, which takes 16 at least
-    // TMEM columns; block scales of K, V and (all 1) of the digits and the identity
-    static constexpr int T_V = 0, T_S = 128, T_O = T_S + NS, T_K = T_O + NP, T_VS = T_K + 4 * KS, T_ONE = T_VS + 4 * KS;
+    static constexpr int NO = 16;                            // and of its MMA, which takes 16 at least
+    // TMEM columns: V^T; S and O of each group; block scales of K (of each group) and V, of the digits and the identity
+    static constexpr int T_V = 0, T_S = 128, T_O = T_S + 2 * NS, T_K = T_O + 2 * NO, T_VS = T_K + 8 * KS,
+                         T_ONE = T_VS + 4 * KS, T_EIGHTH = T_ONE + 4;
     static constexpr int COLS = 256, CTAS = 2;
-    static_assert(T_ONE + 4 <= COLS, "TMEM");
+    static_assert(T_EIGHTH + 4 <= COLS, "TMEM");
     // shared memory
     static constexpr int ROWB = D / 2;                       // bytes of a row's codes
     static constexpr int SFB = kTile4 * D / 16;              // of a tile's block scales
     static constexpr int ENTRY = kTile4 * ROWB + SFB;
-    static constexpr int I_BYTES = 128 * ROWB, Q_BYTES = NS * ROWB, P_BYTES = kTile4 * NP * 4;
-    static constexpr int NOTES = 1280;                       // barriers and notes
-    static constexpr int FIT = (113 * 1024 - I_BYTES - Q_BYTES - P_BYTES - NOTES) / ENTRY / 2 * 2;
+    static constexpr int I_BYTES = 128 * ROWB, Q_SET = NS * ROWB, Q_BYTES = 2 * Q_SET, P_BYTES = kTile4 * NO * 4;
+    static constexpr int NOTES = 2048;                       // barriers and notes
+    static constexpr int FIT = (113 * 1024 - I_BYTES - 2 * Q_BYTES - 2 * P_BYTES - NOTES) / ENTRY / 2 * 2;
     static constexpr int ENTRIES = FIT < 16 ? FIT : 16;
-    static_assert(ENTRIES >= 4 && ENTRIES / 2 + 2 < kRing4, "the ring");
-    static constexpr int O_I = 0, O_Q = O_I + I_BYTES, O_P = O_Q + Q_BYTES, O_RING = O_P + P_BYTES,
+    static_assert(ENTRIES >= 4 && ENTRIES / 2 + 4 < kRing4, "the ring");
+    static constexpr int O_I = 0, O_Q = O_I + I_BYTES, O_P = O_Q + 2 * Q_BYTES, O_RING = O_P + 2 * P_BYTES,
                          O_NOTES = O_RING + ENTRIES * ENTRY, SMEM = O_NOTES + NOTES;
-    static_assert(O_P % 1024 == 0 && O_RING % 1024 == 0 && (kTile4 * ROWB) % 1024 == 0 && ENTRY % 512 == 0, "swizzle atoms");
+    static_assert(O_P % 1024 == 0 && O_RING % 1024 == 0 && P_BYTES % 1024 == 0 && Q_SET % 1024 == 0 && ENTRY % 512 == 0,
+                  "swizzle atoms");
 };
 
-// Shared memory matrix descriptor of a K-major operand with rows of `rowb` = 32, 64 or 128 bytes, swizzled over as many.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t start, int rowb) {
-    return (uint64_t)((start & 0x3FFFFu) >> 4) | 1ull << 16 | (uint64_t)(rowb * 8 >> 4) << 32 | 1ull << 46 |
+// Shared memory matrix descriptor of a K-major operand with rows of `rowb` = 32, 64 or 128 bytes, swizzled over as many,
+// groups of 8 rows `stride` bytes apart.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t start, int rowb, int stride) {
+    return (uint64_t)((start & 0x3FFFFu) >> 4) | 1ull << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 |
            (uint64_t)(rowb == 32 ? 6 : rowb == 64 ? 4 : 2) << 61;
 }
+// The same operand `bytes` (a constant) further on.
+__device__ __forceinline__ uint64_t desc_plus(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 // Of 128 rows' scales: 32 lines of 16 bytes, 4 bytes of rows i, i + 32, i + 64, i + 96 each.
 __device__ __forceinline__ uint64_t desc_scales(uint32_t start) {
     return (uint64_t)((start & 0x3FFFFu) >> 4) | 1ull << 16 | 8ull << 32 | 1ull << 46;
@@ -152,18 +160,18 @@ __device__ __forceinline__ void tmem_st1(uint32_t t, uint32_t v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\ntcgen05.wait::st.sync.aligned;\n" ::"r"(t), "r"(v)
                  : "memory");
 }
-// Whether any of the 128 softmax threads' `x` holds, on named barrier 1.
-__device__ __forceinline__ bool softmax_any(bool x) {
+// Whether any `x` of a softmax group's 128 threads holds, on its named barrier (1 or 2).
+__device__ __forceinline__ bool softmax_any(bool x, int group) {
     uint32_t r;
     asm volatile(
         "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-        " barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        " barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(x))
+        : "r"(static_cast<uint32_t>(x)), "r"(group + 1)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() { named_barrier_sync(1, 128); }
+__device__ __forceinline__ void softmax_sync(int group) { named_barrier_sync(group + 1, 128); }
 
 __device__ __forceinline__ uint32_t to_tf32(float x) {
     uint32_t r;
@@ -194,21 +202,25 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32
 template <class S>
 struct Notes {
     uint64_t full[S::ENTRIES], empty[S::ENTRIES];            // ring entries: rows have landed; MMAs have read them
-    uint64_t s_go, s_full;                                   // S may be written (q is there, the last S is read); is
-    uint64_t p_full, v_full, o_full;                         // P is written; V^T is; O's MMAs of the tile are done
+    uint64_t v_fit[S::ENTRIES / 2];                          // V's scales have been looked through
+    uint64_t q_full[2];                                      // digits of a piece are there (by its parity)
+    uint64_t s_full[2], s_free[2], p_full[2], o_full[2];     // by group: S is written; read; P is written; O's MMAs are done
+    uint64_t v_full;                                         // V^T is written
     uint64_t drained;
     uint32_t tmem;
-    int abort, fresh;                                        // P's tile begins a new sum in O
-    uint8_t ok[kRing4][2];                                   // of tiles: valid 16-slot groups, four bits for each copying warp
+    int abort, fresh[2];                                     // P's tile begins a new sum in the group's O
+    // of tiles: valid 16-slot groups, two bits for each copying warp; bit 4: begins a piece
+    uint8_t ok[kRing4][4];
     uint16_t nan[kRing4];                                    // and blocks of V that hold a NaN
+    uint32_t odd_nan;                                        // the same of the odd group's tiles of a piece
     alignas(16) float mul[2][S::HEADS];                      // score factors, by parity of the piece (read as float4)
     float odd[2][S::HEADS];                                  // NaN for a head whose query is not finite, else 0
-    float sum[4][S::HEADS], top[4][S::HEADS];
+    float top[2][4][S::HEADS], sum[2][4][S::HEADS], odd_ref[S::HEADS];
 };
 
 template <class S>
 __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(const __grid_constant__ DecodeParams p) {
-    constexpr int D = S::D, HEADS = S::HEADS, NP = S::NP, KS = S::KS, ROWB = S::ROWB, NE = S::ENTRIES;
+    constexpr int D = S::D, HEADS = S::HEADS, KS = S::KS, ROWB = S::ROWB, NE = S::ENTRIES;
     extern __shared__ __align__(1024) uint8_t smem4[];
     uint8_t* smem = smem4;
     using N = Notes<S>;
@@ -221,19 +233,24 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
     auto bar = [&](uint64_t& b) { return smem_u32(&b); };
 
     // ---- what does not depend on the call's data ----
-    if (warp == 7) tmem_alloc(smem_u32(&notes.tmem), S::COLS);
+    if (warp == 13) tmem_alloc(smem_u32(&notes.tmem), S::COLS);
     if (tid == 0) {
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-            mbar_init(bar(notes.full[e]), 64 + 2);
+            mbar_init(bar(notes.full[e]), 128 + 4);
             mbar_init(bar(notes.empty[e]), 1);
+            if (e & 1) mbar_init(bar(notes.v_fit[e / 2]), 1);
         }
-        mbar_init(bar(notes.s_go), 128);
-        mbar_init(bar(notes.s_full), 1);
-        mbar_init(bar(notes.p_full), 128);
         mbar_init(bar(notes.v_full), 1);
-        mbar_init(bar(notes.o_full), 1);
         mbar_init(bar(notes.drained), 2);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(bar(notes.q_full[g]), 128);
+            mbar_init(bar(notes.s_full[g]), 1);
+            mbar_init(bar(notes.s_free[g]), 128);
+            mbar_init(bar(notes.p_full[g]), 128);
+            mbar_init(bar(notes.o_full[g]), 1);
+        }
         notes.abort = 0;
         fence_mbar_init_cluster();
     }
@@ -251,7 +268,10 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
     const uint32_t tmem = notes.tmem;
     if (warp < 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_st1(tmem + (warp * 32u << 16) + S::T_ONE + i, 0x38383838u);       // (e4m3: 1)
+        for (int i = 0; i < 4; ++i) {
+            tmem_st1(tmem + (warp * 32u << 16) + S::T_ONE + i, 0x38383838u);             // e4m3: 1
+            tmem_st1(tmem + (warp * 32u << 16) + S::T_EIGHTH + i, 0x20202020u);          // 2^-3
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -300,73 +320,80 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
         __syncwarp();
     };
 
-    if (warp == 4 || warp == 5) {
+    if (warp >= 8 && warp < 12) {
         // ============================================================ copies
-        // A warp copies 64 slots of every tile: four groups of 16, each on one page.
+        // A warp copies 32 slots of every tile: two groups of 16, each on one page.
         if (tiles > 0) {
-            const int w = warp - 4;
+            const int w = warp - 8;
             constexpr int PPR = ROWB / 16, RPI = 32 / PPR;             // pieces of a row, rows per warp-wide copy
             const int lane_row = lane / PPR, lane_piece = lane % PPR;
             const int page_mask = (1 << p.c.page_shift) - 1;
             const long long lane_off = lane_row * p.c.row_stride + lane_piece * 16, step = RPI * p.c.row_stride;
             const long long lane_block = (lane & 15) * p.c.b_row_stride;
-            const uint32_t dst0 = 64 * w * ROWB + row_offset<ROWB>(lane_row, lane_piece * 16);
-            const uint32_t dst1 = kTile4 * ROWB + lane * 16 + w * 8;
+            const uint32_t dst0 = 32 * w * ROWB + row_offset<ROWB>(lane_row, lane_piece * 16);
+            const uint32_t dst1 = kTile4 * ROWB + lane * 16 + w * 4;
             Cursor<kTile4> at;
             at.at = t0;
             at.locate(p, hcs, lane, early, request_of);
             at.bound(t1);
-            // lanes 0 .. 3: the page of a group of the tile, and whether it holds slots to attend
+            // lanes 0 and 1: the page of a group of the tile, and whether it holds slots to attend
             int page = -1;
             bool wanted = false;
-            auto slot_of = [&]() { return (at.rg.lo / kTile4 + static_cast<int>(at.at - at.seg)) * kTile4 + 64 * w; };
+            auto slot_of = [&]() { return (at.rg.lo / kTile4 + static_cast<int>(at.at - at.seg)) * kTile4 + 32 * w; };
             auto look = [&]() {
                 const int slot = slot_of() + lane * 16;
                 page = -1;
-                wanted = lane < 4 && slot < at.rg.n && slot + 16 > at.rg.lo;
+                wanted = lane < 2 && slot < at.rg.n && slot + 16 > at.rg.lo;
                 if (wanted) page = __ldg(p.c.table + (long long)at.rq.row * p.c.table_stride + (slot >> p.c.page_shift));
             };
+            long long head = 0, block_head = 0;    // this lane's place in the KV head
+            auto come_to = [&]() {
+                head = at.hc * p.c.head_stride + lane_off;
+                block_head = at.hc * p.c.b_head_stride + lane_block;
+            };
+            come_to();
             look();
             int e = 0;
             uint32_t turn = 1;                     // parity that an entry's last reading has; 1: nothing was there
             for (int i = 0; i < tiles; ++i) {
                 const int slot0 = slot_of(), lo = at.rg.lo, n = at.rg.n;
+                const bool begins = i == 0 || at.at == at.seg;
                 const bool valid = page >= 0 && page < p.c.num_pages;
                 if (wanted && !valid) atomicOr(p.err, DSV4_DEV_ERR_GQA_PAGE);
                 const unsigned okm = __ballot_sync(0xffffffffu, wanted && valid);
                 const int in_page = slot0 + lane * 16 & page_mask;
-                const long long off = valid ? page * p.c.page_stride + at.hc * p.c.head_stride + in_page * p.c.row_stride : 0;
-                const long long block_off =
-                    valid ? page * p.c.b_page_stride + at.hc * p.c.b_head_stride + in_page * p.c.b_row_stride : 0;
-                long long go[4], bo[2];
+                const long long off = page * p.c.page_stride + in_page * p.c.row_stride;       // (used where valid)
+                const long long block_off = page * p.c.b_page_stride + in_page * p.c.b_row_stride;
+                long long go[2];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) go[g] = __shfl_sync(0xffffffffu, off, g) + lane_off;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) bo[u] = __shfl_sync(0xffffffffu, block_off, 2 * u + (lane >> 4)) + lane_block;
-                const bool whole = okm == 15u && slot0 >= lo && slot0 + 64 <= n;
+                for (int g = 0; g < 2; ++g) go[g] = __shfl_sync(0xffffffffu, off, g) + head;
+                const long long bo = __shfl_sync(0xffffffffu, block_off, lane >> 4) + block_head;
+                const bool whole = okm == 3u && slot0 >= lo && slot0 + 32 <= n;
                 // the next tile's pages are on their way while this one's entries are waited for
                 ++at.at;
-                if (at.at < at.end || at.next_segment(p, hcs, t1)) look();
+                if (at.at < at.end) {
+                    look();
+                } else if (at.next_segment(p, hcs, t1)) {
+                    come_to();
+                    look();
+                }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     warp_wait(notes.empty[e], turn);
-                    fence_proxy_async();
-                    if (kv == 0 && lane == 0) *(volatile uint8_t*)&notes.ok[i % kRing4][w] = okm;
+                    if (kv == 0 && lane == 0) *(volatile uint8_t*)&notes.ok[i % kRing4][w] = okm | (begins ? 16 : 0);
                     const uint32_t dst = ring + e * S::ENTRY;
                     const uint8_t *pool = kv ? p.c.v : p.c.k, *blocks = kv ? p.c.vb : p.c.kb;
-                    // lane's rows lane and 32 + lane: block scales, 4 of them to a line of each K step
+                    {
+                        // a lane's row: its block scales, 4 of them to a line of each K step
+                        const int s = slot0 + lane;
+                        const bool in = whole || ((okm >> (lane >> 4) & 1) && s >= lo && s < n);
+                        const uint8_t* src = blocks + (in ? bo : 0);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int s = slot0 + 32 * u + lane;
-                        const bool in = whole || ((okm >> (2 * u + (lane >> 4)) & 1) && s >= lo && s < n);
-                        const uint8_t* src = blocks + (in ? bo[u] : 0);
-#pragma unroll
-                        for (int k = 0; k < KS; ++k)
-                            cp_async_4(dst + dst1 + 512 * k + 4 * u, src + (in ? 4 * k : 0), in ? 4u : 0u);
+                        for (int k = 0; k < KS; ++k) cp_async_4(dst + dst1 + 512 * k, src + (in ? 4 * k : 0), in ? 4u : 0u);
                     }
                     if (whole) {
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
+                        for (int g = 0; g < 2; ++g) {
                             const uint8_t* src = pool + go[g];
 #pragma unroll
                             for (int j = 0; j < 16 / RPI; ++j) {
@@ -376,7 +403,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                         }
                     } else {
 #pragma unroll
-                        for (int g = 0; g < 4; ++g)
+                        for (int g = 0; g < 2; ++g)
 #pragma unroll
                             for (int j = 0; j < 16 / RPI; ++j) {
                                 const int s = slot0 + 16 * g + j * RPI + lane_row;
@@ -395,115 +422,140 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             }
             cp_async_wait_all();
         }
-    } else if (warp == 6) {
-        // ============================================================ S
-        constexpr uint32_t idesc = idesc_e2m1(128, S::NS);
-        for (int i = 0; i < tiles; ++i) {
-            const int e = 2 * i % NE, use = 2 * i / NE;
-            const uint32_t entry = ring + e * S::ENTRY, scales = entry + kTile4 * ROWB;
-            warp_wait(notes.full[e], use & 1);
-            bool odd = false;
-            for (int at = lane * 16; at < S::SFB; at += 512) {
-                const uint4 x = ld_shared_u4(scales + at);
-                odd |= ((x.x | x.y | x.z | x.w) & 0x80808080u) != 0;
+    } else if (warp == 12) {
+        // ============================================================ scales, and S
+        // Bit 7 where a lane's share of an entry's block scales has a NaN or a sign.
+        auto odd_scales = [&](uint32_t entry) {
+            uint32_t odd = 0;
+#pragma unroll
+            for (int at = 0; at < S::SFB; at += 512) {
+                const uint4 x = ld_shared_u4(entry + kTile4 * ROWB + at + lane * 16);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) odd |= ((w[k] & 0x7f7f7f7fu) + 0x01010101u) | w[k];
             }
-            if (__any_sync(0xffffffffu, odd)) {
-                // the signs of scales go to their codes
-                for (int at = lane; at < S::SFB; at += 32) {
-                    const int r = (at >> 4 & 31) + 32 * (at >> 2 & 3), block = 4 * (at >> 9) + (at & 3);
-                    uint8_t* sf = smem + (scales - base) + at;
-                    if (*sf & 0x80) {
-                        uint2* codes = reinterpret_cast<uint2*>(smem + (entry - base) + row_offset<ROWB>(r, 8 * block));
-                        *codes = make_uint2(codes->x ^ 0x88888888u, codes->y ^ 0x88888888u);
-                        *sf &= 0x7f;
-                    }
+            return odd & 0x80808080u;
+        };
+        // Signs go to the codes; of V, NaN scales become 0 and their blocks are returned (a bit each).
+        auto mend_scales = [&](uint32_t entry, bool is_v) {
+            uint32_t nan = 0;
+#pragma unroll 1
+            for (int at = lane; at < S::SFB; at += 32) {
+                const int r = (at >> 4 & 31) + 32 * (at >> 2 & 3), block = 4 * (at >> 9) + (at & 3);
+                uint8_t* sf = smem + (entry - base) + kTile4 * ROWB + at;
+                if (is_v && (*sf & 0x7f) == 0x7f) {
+                    nan |= 1u << block;
+                    *sf = 0;
+                } else if (*sf & 0x80) {
+                    uint2* codes = reinterpret_cast<uint2*>(smem + (entry - base) + row_offset<ROWB>(r, 8 * block));
+                    *codes = make_uint2(codes->x ^ 0x88888888u, codes->y ^ 0x88888888u);
+                    *sf &= 0x7f;
                 }
-                __syncwarp();
             }
-            warp_wait(notes.s_go, i & 1);
+            return __reduce_or_sync(0xffffffffu, nan);
+        };
+        constexpr uint32_t idesc = idesc_e2m1(128, S::NS);
+        int e = 0, piece = -1;
+        uint32_t turn = 0;
+        for (int i = 0; i < tiles; ++i) {
+            const int g = i & 1;
+            const uint32_t entry = ring + e * S::ENTRY, scales = entry + kTile4 * ROWB;
+            warp_wait(notes.full[e], turn);
+            warp_wait(notes.full[e + 1], turn);
+            uint32_t nan = 0;
+            if (__any_sync(0xffffffffu, (odd_scales(entry) | odd_scales(entry + S::ENTRY)) != 0)) {
+                mend_scales(entry, false);
+                nan = mend_scales(entry + S::ENTRY, true);
+            }
+            if (lane == 0) *(volatile uint16_t*)&notes.nan[i % kRing4] = nan;
             fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(notes.v_fit[e / 2]));
+            if (*(volatile uint8_t*)&notes.ok[i % kRing4][0] & 16) {
+                ++piece;
+                warp_wait(notes.q_full[piece & 1], piece >> 1 & 1);
+            }
+            warp_wait(notes.s_free[g], i >> 1 & 1 ^ 1);
             tc_fence_after();
             __syncwarp();
             if (elect_one()) {
+                const uint32_t t_k = tmem + S::T_K + g * 4 * KS, t_s = tmem + S::T_S + g * S::NS;
+                const uint64_t rows = desc_rows(entry, ROWB, 8 * ROWB), sf = desc_scales(scales);
+                const uint64_t digits = desc_rows(s_q + (piece & 1) * S::Q_BYTES, ROWB, 8 * ROWB);
 #pragma unroll
-                for (int k = 0; k < KS; ++k) tmem_copy_scales(tmem + S::T_K + 4 * k, desc_scales(scales + 512 * k));
+                for (int k = 0; k < KS; ++k) tmem_copy_scales(t_k + 4 * k, desc_plus(sf, 512 * k));
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
-                    mma_e2m1(tmem + S::T_S, desc_rows(entry + 32 * k, ROWB), desc_rows(s_q + 32 * k, ROWB), idesc,
-                             tmem + S::T_K + 4 * k, tmem + S::T_ONE, k);
-                mma_commit(bar(notes.s_full));
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        mma_e2m1(t_s, desc_plus(rows, 32 * k), desc_plus(digits, c * S::Q_SET + 32 * k), idesc, t_k + 4 * k,
+                                 tmem + (c ? S::T_EIGHTH : S::T_ONE), k || c);
+                mma_commit(bar(notes.s_full[g]));
                 mma_commit(bar(notes.empty[e]));
             }
             __syncwarp();
+            e += 2;
+            if (e == NE) {
+                e = 0;
+                turn ^= 1;
+            }
         }
         if (elect_one()) mma_commit(bar(notes.drained));
         __syncwarp();
-    } else if (warp == 7) {
+    } else if (warp == 13) {
         // ============================================================ V^T and O
-        constexpr uint32_t idesc_v = idesc_e2m1(128, kTile4), idesc_o = idesc_tf32(128, NP);
+        const uint64_t identity = desc_rows(s_i, ROWB, 8 * ROWB);
+        constexpr uint32_t idesc_v = idesc_e2m1(128, kTile4), idesc_o = idesc_tf32(128, S::NO);
+        int e = 0;
+        uint32_t turn = 0;
         for (int i = 0; i < tiles; ++i) {
-            const int e = (2 * i + 1) % NE, use = (2 * i + 1) / NE;
-            const uint32_t entry = ring + e * S::ENTRY, scales = entry + kTile4 * ROWB;
-            warp_wait(notes.full[e], use & 1);
-            bool odd = false;
-            for (int at = lane * 16; at < S::SFB; at += 512) {
-                const uint4 x = ld_shared_u4(scales + at);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) odd |= ((((w[k] & 0x7f7f7f7fu) + 0x01010101u) | w[k]) & 0x80808080u) != 0;
-            }
-            uint32_t nan = 0;
-            if (__any_sync(0xffffffffu, odd)) {
-                for (int at = lane; at < S::SFB; at += 32) {
-                    const int r = (at >> 4 & 31) + 32 * (at >> 2 & 3), block = 4 * (at >> 9) + (at & 3);
-                    uint8_t* sf = smem + (scales - base) + at;
-                    if ((*sf & 0x7f) == 0x7f) {
-                        nan |= 1u << block;
-                        *sf = 0;
-                    } else if (*sf & 0x80) {
-                        uint2* codes = reinterpret_cast<uint2*>(smem + (entry - base) + row_offset<ROWB>(r, 8 * block));
-                        *codes = make_uint2(codes->x ^ 0x88888888u, codes->y ^ 0x88888888u);
-                        *sf &= 0x7f;
-                    }
-                }
-                nan = __reduce_or_sync(0xffffffffu, nan);
-            }
-            if (lane == 0) *(volatile uint16_t*)&notes.nan[i % kRing4] = nan;
-            if (i > 0) warp_wait(notes.o_full, (i - 1) & 1);           // (V^T has been read)
-            fence_proxy_async();
+            const int g = i & 1;
+            const uint32_t entry = ring + (e + 1) * S::ENTRY, scales = entry + kTile4 * ROWB;
+            warp_wait(notes.v_fit[e / 2], turn);
+            if (i > 0) warp_wait(notes.o_full[g ^ 1], (i - 1) >> 1 & 1);         // (V^T has been read)
             tc_fence_after();
             __syncwarp();
             if (elect_one()) {
+                const uint64_t rows = desc_rows(entry, ROWB, 8 * ROWB), sf = desc_scales(scales);
 #pragma unroll
-                for (int k = 0; k < KS; ++k) tmem_copy_scales(tmem + S::T_VS + 4 * k, desc_scales(scales + 512 * k));
+                for (int k = 0; k < KS; ++k) tmem_copy_scales(tmem + S::T_VS + 4 * k, desc_plus(sf, 512 * k));
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
-                    mma_e2m1(tmem + S::T_V, desc_rows(s_i + 32 * k, ROWB), desc_rows(entry + 32 * k, ROWB), idesc_v,
-                             tmem + S::T_ONE, tmem + S::T_VS + 4 * k, k);
+                    mma_e2m1(tmem + S::T_V, desc_plus(identity, 32 * k), desc_plus(rows, 32 * k), idesc_v, tmem + S::T_ONE,
+                             tmem + S::T_VS + 4 * k, k);
                 mma_commit(bar(notes.v_full));
-                mma_commit(bar(notes.empty[e]));
+                mma_commit(bar(notes.empty[e + 1]));
             }
             __syncwarp();
-            warp_wait(notes.p_full, i & 1);
+            warp_wait(notes.p_full[g], i >> 1 & 1);
+            const uint32_t sum = *(volatile int*)&notes.fresh[g] ? 0u : 1u;
             warp_wait(notes.v_full, i & 1);
-            const uint32_t sum = *(volatile int*)&notes.fresh ? 0u : 1u;
-            fence_proxy_async();
             tc_fence_after();
             __syncwarp();
             if (elect_one()) {
+                const uint64_t weights = desc_rows(s_p + g * S::P_BYTES, 128, 1024);
+                const uint32_t t_o = tmem + S::T_O + g * S::NO;
+                // (bf16 outputs: rows 8 .. 15 hold anything, and nobody reads their columns of O)
+                mma_tf32_ts(t_o, tmem + S::T_V, weights, idesc_o, sum);
 #pragma unroll
-                for (int k = 0; k < kTile4 / 8; ++k)
-                    mma_tf32_ts(tmem + S::T_O, tmem + S::T_V + 8 * k,
-                                desc_rows(s_p + (k >> 2) * NP * 128 + (k & 3) * 32, 128), idesc_o, k ? 1u : sum);
-                mma_commit(bar(notes.o_full));
+                for (int k = 1; k < kTile4 / 8; ++k)
+                    mma_tf32_ts(t_o, tmem + S::T_V + 8 * k, desc_plus(weights, (k >> 2) * S::NO * 128 + (k & 3) * 32), idesc_o, 1u);
+                mma_commit(bar(notes.o_full[g]));
             }
             __syncwarp();
+            e += 2;
+            if (e == NE) {
+                e = 0;
+                turn ^= 1;
+            }
         }
         if (elect_one()) mma_commit(bar(notes.drained));
         __syncwarp();
     } else if (tiles > 0) {
         // ============================================================ softmax and output
-        const uint32_t lane_t = tmem + (warp * 32u << 16), p_to = s_p + warp * NP * 128 + (lane & 3) * 4;
+        const int g = warp >> 2, quad = warp & 3, gt = tid & 127;
+        const uint32_t lane_t = tmem + (quad * 32u << 16);
+        const uint32_t p_to = s_p + g * S::P_BYTES + quad * S::NO * 128 + (lane & 3) * 4;
         Cursor<kTile4> at;
         at.at = t0;
         at.locate(p, hcs, lane, early, request_of);
@@ -512,7 +564,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
         // q: a head to 128 / HEADS threads, of which each takes DP dims
         constexpr int TPH = 128 / HEADS, DP = D / TPH, NW = DP / 2;
         uint32_t qw[NW];
-        const int q_head = tid / TPH, q_dim = tid % TPH * DP;
+        const int q_head = gt / TPH, q_dim = gt % TPH * DP;
         float kscale = 1.f;
         auto load_q = [&](const Cursor<kTile4>& of) {
             const int h = of.hc;
@@ -531,7 +583,9 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             }
             kscale = p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.f;
         };
-        auto write_q = [&](int parity) {
+        // the digits of a piece and its factors
+        auto write_q = [&](int piece) {
+            const int parity = piece & 1;
             float amax = 0.f;
             bool bad = false;
 #pragma unroll
@@ -564,37 +618,36 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                         y[j] = (y[j] - static_cast<float>(d)) * 8.f;
                         codes |= digit_e2m1(d) << 4 * j;
                     }
-                    uint8_t* to = smem + S::O_Q + row_offset<ROWB>(k * HEADS + q_head, (q_dim + 2 * k0) / 2);
+                    uint8_t* to = smem + S::O_Q + parity * S::Q_BYTES + (k & 1) * S::Q_SET +
+                                  row_offset<ROWB>((k >> 1) * HEADS + q_head, (q_dim + 2 * k0) / 2);
                     if constexpr (NW == 2) *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(codes);
                     else *reinterpret_cast<uint32_t*>(to) = codes;
                 }
             }
             // (a head with a value that is not finite has no finite score: its sums become NaN)
-            if (tid % TPH == 0) {
+            if (gt % TPH == 0) {
                 notes.mul[parity][q_head] =
                     bad ? 0.f : p.scale_log2 * kscale * __uint_as_float(static_cast<uint32_t>(126 + e) << 23);
                 notes.odd[parity][q_head] = bad ? NAN : 0.f;
             }
             fence_proxy_async();
+            mbar_arrive(bar(notes.q_full[parity]));
         };
 
-        load_q(at);
-        write_q(0);
-        mbar_arrive(bar(notes.s_go));
-        softmax_sync();                            // (factors)
-
+        if (g == 0) {
+            load_q(at);
+            write_q(0);
+        }
         float o[HEADS], lsum[HEADS];               // sums taken out of the accumulator; of this thread's weights
-        float ref[HEADS];                          // the softmax's references, the same in all threads
+        float ref[HEADS];                          // the softmax's references, the same in all threads of the group
         uint32_t nan = 0;
-        int parity = 0, kept = 0;                  // kept: tiles in the accumulator
-        bool starts = true;
-        // O of the tiles up to i comes out of the accumulator
+        int kept = 0;                              // tiles in the accumulator
+        // the sums over the group's tiles up to i come out of the accumulator
         auto take_o = [&](int i) {
-            wait(notes.o_full, i & 1);
-            __syncwarp();
+            warp_wait(notes.o_full[g], i >> 1 & 1);
             tc_fence_after();
             float x[S::USED];
-            tmem_ld<S::USED>(lane_t + S::T_O, x);
+            tmem_ld<S::USED>(lane_t + S::T_O + g * S::NO, x);
 #pragma unroll
             for (int c = 0; c < HEADS; ++c) {
                 o[c] += x[c];
@@ -602,180 +655,192 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             }
             tc_fence_before();
         };
-        for (int i = 0; i < tiles; ++i) {
-            if (starts) {
-#pragma unroll
-                for (int c = 0; c < HEADS; ++c) {
-                    o[c] = lsum[c] = 0.f;
-                    ref[c] = kNoMax;
-                }
-                nan = 0;
-                kept = 0;
-            }
-            const unsigned tile = at.at;
-            const bool ends = tile + 1 == at.end;
-            const int slot = (at.rg.lo / kTile4 + static_cast<int>(tile - at.seg)) * kTile4 + tid, lo = at.rg.lo, n = at.rg.n;
-            Cursor<kTile4> next;                   // (read where the piece ends)
-            bool more = false;
-            if (ends) {
-                next = at;
-                more = next.next_segment(p, hcs, t1);
-                if (more) load_q(next);
-            }
-
-            // S: the digits' columns, the smallest weight first, heads in pairs
-            warp_wait(notes.s_full, i & 1);
-            tc_fence_after();
-            uint64_t s2[HEADS / 2];
-            const uint64_t eighth = f32_pair(0.125f, 0.125f);
-#pragma unroll
-            for (int part = S::NS / 32 - 1; part >= 0; --part) {
-                float x[32];
-                tmem_ld<32>(lane_t + S::T_S + 32 * part, x);
-#pragma unroll
-                for (int g = 32 / HEADS - 1; g >= 0; --g)
-#pragma unroll
-                    for (int c = 0; c < HEADS; c += 2) {
-                        const uint64_t y = f32_pair(x[g * HEADS + c], x[g * HEADS + c + 1]);
-                        s2[c / 2] = part == S::NS / 32 - 1 && g == 32 / HEADS - 1 ? y : fma_pair(s2[c / 2], eighth, y);
-                    }
-            }
-            tc_fence_before();
-            if (more) write_q(parity ^ 1);
-            mbar_arrive(bar(notes.s_go));
-            // log2-unit scores below their reference
-            const bool in = slot >= lo && slot < n &&
-                            (*(volatile uint8_t*)&notes.ok[i % kRing4][warp >> 1] >> ((warp & 1) * 2 + (lane >> 4)) & 1);
-            float s[HEADS], x[HEADS], mul[HEADS];
-            bool above = false;
-#pragma unroll
-            for (int c = 0; c < HEADS; c += 4) {
-                const float4 m = *reinterpret_cast<const float4*>(&notes.mul[parity][c]);
-                mul[c] = m.x; mul[c + 1] = m.y; mul[c + 2] = m.z; mul[c + 3] = m.w;
-            }
+        for (int i0 = 0, piece = 0; i0 < tiles; ++piece) {
+            const int count = static_cast<int>(at.end - at.at);        // tiles of the piece
+            Cursor<kTile4> next = at;
+            bool ask = next.next_segment(p, hcs, t1) && g == 0;        // the next piece's digits are still to be written
+            if (ask) load_q(next);
 #pragma unroll
             for (int c = 0; c < HEADS; ++c) {
-                asm("{\n .reg .b32 h;\n mov.b64 {%0, h}, %1;\n}\n" : "=f"(s[c]) : "l"(c & 1 ? s2[c / 2] >> 32 : s2[c / 2]));
-                x[c] = in ? fmaf(s[c], mul[c], -ref[c]) : -INFINITY;
-                above |= x[c] > 8.f;
+                o[c] = lsum[c] = 0.f;
+                ref[c] = kNoMax;
             }
-            if (p.logits) {
-                float4* to = reinterpret_cast<float4*>(p.logits + ((size_t)tile * kTile4 + tid) * HEADS);
+            nan = 0;
+            kept = 0;
+            const int slot_0 = (at.rg.lo / kTile4 + static_cast<int>(at.at - at.seg)) * kTile4 + gt;
+            int i = i0 + ((i0 ^ g) & 1);           // the group's first tile
+            for (; i < i0 + count; i += 2) {
+                const int k = i >> 1, slot = slot_0 + (i - i0) * kTile4;
+                // S: the columns of digits, the smallest weight first, heads in pairs
+                warp_wait(notes.s_full[g], k & 1);
+                tc_fence_after();
+                uint64_t s2[HEADS / 2];
+                {
+                    float x[32];
+                    tmem_ld<32>(lane_t + S::T_S + g * S::NS, x);
+                    const uint64_t step = f32_pair(0x1p-6f, 0x1p-6f);
+#pragma unroll
+                    for (int j = 32 / HEADS - 1; j >= 0; --j)
+#pragma unroll
+                        for (int c = 0; c < HEADS; c += 2) {
+                            const uint64_t y = f32_pair(x[j * HEADS + c], x[j * HEADS + c + 1]);
+                            s2[c / 2] = j == 32 / HEADS - 1 ? y : fma_pair(s2[c / 2], step, y);
+                        }
+                }
+                tc_fence_before();
+                mbar_arrive(bar(notes.s_free[g]));
+                // log2-unit scores below their reference
+                const bool in = slot >= at.rg.lo && slot < at.rg.n &&
+                                (*(volatile uint8_t*)&notes.ok[i % kRing4][quad] >> (lane >> 4) & 1);
+                float s[HEADS], x[HEADS];
+                bool above = false;
 #pragma unroll
                 for (int c = 0; c < HEADS; c += 4) {
-                    float y[4];
+                    const float4 m = *reinterpret_cast<const float4*>(&notes.mul[piece & 1][c]);
+                    const float mul[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) y[k] = in ? s[c + k] * mul[c + k] : -INFINITY;
-                    to[c / 4] = make_float4(y[0], y[1], y[2], y[3]);
+                    for (int j = 0; j < 4; ++j) {
+                        asm("{\n .reg .b32 h;\n mov.b64 {%0, h}, %1;\n}\n"
+                            : "=f"(s[c + j])
+                            : "l"(j & 1 ? s2[(c + j) / 2] >> 32 : s2[(c + j) / 2]));
+                        x[c + j] = in ? fmaf(s[c + j], mul[j], -ref[c + j]) : -INFINITY;
+                        above |= x[c + j] > 8.f;
+                    }
                 }
-            }
-            const bool moves = softmax_any(above);
-            if (i > 0 && !starts) {
-                if (moves || kept == kFlushTiles) {
-                    take_o(i - 1);
-                    kept = 0;
-                } else {
-                    warp_wait(notes.o_full, (i - 1) & 1);              // (P has been read)
+                if (p.logits) {
+                    float4* to = reinterpret_cast<float4*>(p.logits + ((size_t)(at.at + (i - i0)) * kTile4 + gt) * HEADS);
+#pragma unroll
+                    for (int c = 0; c < HEADS; c += 4) {
+                        float y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) y[j] = in ? s[c + j] * notes.mul[piece & 1][c + j] : -INFINITY;
+                        to[c / 4] = make_float4(y[0], y[1], y[2], y[3]);
+                    }
                 }
-                nan |= *(volatile uint16_t*)&notes.nan[(i - 1) % kRing4];
-            }
-            if (moves) {
+                const bool moves = softmax_any(above, g);
+                if (kept > 0) {
+                    // (P of the group's last tile has been read)
+                    if (moves || kept == kFlushTiles) {
+                        take_o(i - 2);
+                        kept = 0;
+                    } else {
+                        warp_wait(notes.o_full[g], (i - 2) >> 1 & 1);
+                    }
+                    nan |= *(volatile uint16_t*)&notes.nan[(i - 2) % kRing4];
+                }
+                if (moves) {
+#pragma unroll
+                    for (int c = 0; c < HEADS; ++c) {
+                        // the warp's largest score, as an integer of the same order (a NaN counts as -inf)
+                        const int y = __float_as_int(in ? fmaxf(s[c] * notes.mul[piece & 1][c], -INFINITY) : -INFINITY);
+                        const int m = __reduce_max_sync(0xffffffffu, y ^ (y >> 31 & 0x7fffffff));
+                        if (lane == 0) notes.top[g][quad][c] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
+                    }
+                    softmax_sync(g);
+#pragma unroll
+                    for (int c = 0; c < HEADS; ++c) {
+                        const float top = fmaxf(fmaxf(notes.top[g][0][c], notes.top[g][1][c]),
+                                                fmaxf(notes.top[g][2][c], notes.top[g][3][c]));
+                        const float r = fmaxf(ref[c], top), f = fast_exp2(ref[c] - r);
+                        ref[c] = r;
+                        lsum[c] *= f;
+                        o[c] *= f;
+                        x[c] = in ? fmaf(s[c], notes.mul[piece & 1][c], -r) : -INFINITY;
+                    }
+                    // (the next tile's vote lies between this reading and the next writing)
+                }
+                // P, head by head a line of 32 slots
 #pragma unroll
                 for (int c = 0; c < HEADS; ++c) {
-                    // the warp's largest score, as an integer of the same order (a NaN counts as -inf)
-                    const int y = __float_as_int(in ? fmaxf(s[c] * mul[c], -INFINITY) : -INFINITY);
-                    const int m = __reduce_max_sync(0xffffffffu, y ^ (y >> 31 & 0x7fffffff));
-                    if (lane == 0) notes.top[warp][c] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
+                    const uint32_t to = p_to + c * 128 + (((lane >> 2) ^ c) << 4);
+                    const float y = fast_exp2(x[c]);
+                    lsum[c] += y;
+                    const uint32_t hi = to_tf32(y);
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
+                    if constexpr (S::TWO)
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + HEADS * 128), "r"(__float_as_uint(y - __uint_as_float(hi)))
+                                     : "memory");
                 }
-                softmax_sync();
-#pragma unroll
-                for (int c = 0; c < HEADS; ++c) {
-                    const float top = fmaxf(fmaxf(notes.top[0][c], notes.top[1][c]), fmaxf(notes.top[2][c], notes.top[3][c]));
-                    const float r = fmaxf(ref[c], top), f = fast_exp2(ref[c] - r);
-                    ref[c] = r;
-                    lsum[c] *= f;
-                    o[c] *= f;
-                    x[c] = in ? fmaf(s[c], mul[c], -r) : -INFINITY;
+                if (gt == 0) *(volatile int*)&notes.fresh[g] = kept == 0;
+                ++kept;
+                fence_proxy_async();
+                mbar_arrive(bar(notes.p_full[g]));
+                if (ask) {
+                    write_q(piece + 1);
+                    ask = false;
                 }
-                // (the next tile's vote lies between this reading and the next writing)
             }
-            // P, head by head a line of 32 slots
-#pragma unroll
-            for (int c = 0; c < HEADS; ++c) {
-                const uint32_t to = p_to + c * 128 + (((lane >> 2) ^ c) << 4);
-                const float y = fast_exp2(x[c]);
-                lsum[c] += y;
-                const uint32_t hi = to_tf32(y);
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
-                if constexpr (S::TWO)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + HEADS * 128), "r"(__float_as_uint(y - __uint_as_float(hi)))
-                                 : "memory");
-            }
-            if (tid == 0) *(volatile int*)&notes.fresh = kept == 0;
-            ++kept;
-            fence_proxy_async();
-            mbar_arrive(bar(notes.p_full));
-            starts = ends;
-            if (!ends) {
-                ++at.at;
-                continue;
-            }
+            if (ask) write_q(piece + 1);
 
-            // ---- the piece's sums, and its output ----
-            const bool cut = at.end != at.seg + at.rg.tiles || at.seg < t0;
-            const bool begins = at.seg >= t0;
-            const int h = at.hc, head0 = h * p.group, nheads = p.group;
+            // ---- the piece's sums: the odd group's to the even one, which writes the output ----
 #pragma unroll
             for (int c = 0; c < HEADS; ++c) {
                 float x = lsum[c];
 #pragma unroll
                 for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-                if (lane == 0) notes.sum[warp][c] = x;
+                if (lane == 0) notes.sum[g][quad][c] = x;
             }
-            softmax_sync();
-            take_o(i);
-            nan |= *(volatile uint16_t*)&notes.nan[i % kRing4];
-            const float vmul = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
-            const size_t row = (size_t)at.b * p.heads + head0;
-            const int entry = piece_entry(share, begins);
+            if (kept > 0) {
+                take_o(i - 2);
+                nan |= *(volatile uint16_t*)&notes.nan[(i - 2) % kRing4];
+            }
+            float* others = reinterpret_cast<float*>(smem + S::O_P + S::P_BYTES);        // (the odd group's P has been read)
+            if (g == 1) {
 #pragma unroll
-            for (int c = 0; c < HEADS; ++c) {
-                if (c >= nheads) break;
-                float l = (notes.sum[0][c] + notes.sum[1][c]) + (notes.sum[2][c] + notes.sum[3][c]);
-                if (l > 0.f) l += notes.odd[parity][c];
-                float inv = 1.f;
-                if (!cut) {
-                    const float sk = p.sink ? __ldg(p.sink + head0 + c) * kLog2e : -INFINITY;
-                    const float top = fminf(fmaxf(ref[c], sk), 3e38f);         // (a sink of +inf: out = 0)
-                    const float f = fast_exp2(ref[c] - top);
-                    const float all = l * f + fast_exp2(sk - top);
-                    const bool some = all > 0.f || all != all;
-                    inv = some ? vmul * f / all : 0.f;
-                    if (tid == 0) {
-                        const float l2 = some ? top + log2f(all) : -INFINITY;
-                        if (p.lse) p.lse[row + c] = l2 * kLn2;
-                        if (p.lse2) p.lse2[row + c] = l2;
-                    }
-                } else if (tid == 0) {
-                    p.part_ml[(size_t)entry * HEADS + c] = make_float2(ref[c], l);
+                for (int c = 0; c < HEADS; ++c) {
+                    others[c * 128 + gt] = o[c];
+                    if (gt == 0) notes.odd_ref[c] = ref[c];
                 }
-                if (tid >= D) continue;
-                const float x = nan >> (tid >> 4) & 1 || l != l ? NAN : o[c] * inv;
-                if (cut)
-                    p.part_o[((size_t)entry * HEADS + c) * D + tid] = x;
-                else
-                    static_cast<uint16_t*>(p.out)[(row + c) * D + tid] = static_cast<uint16_t>(pack2<S::QBF16>(x, 0.f));
+                if (gt == 0) notes.odd_nan = nan;
             }
+            named_barrier_sync(3, 256);
+            if (g == 0) {
+                nan |= notes.odd_nan;
+                const bool begins = at.seg >= t0, cut = !begins || at.end != at.seg + at.rg.tiles;
+                const int h = at.hc, head0 = h * p.group;
+                const float vmul = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
+                const size_t row = (size_t)at.b * p.heads + head0;
+                const int entry = piece_entry(share, begins);
+#pragma unroll
+                for (int c = 0; c < HEADS; ++c) {
+                    if (c >= p.group) break;
+                    const float r = fmaxf(ref[c], notes.odd_ref[c]);
+                    const float f0 = fast_exp2(ref[c] - r), f1 = fast_exp2(notes.odd_ref[c] - r);
+                    float l = ((notes.sum[0][0][c] + notes.sum[0][1][c]) + (notes.sum[0][2][c] + notes.sum[0][3][c])) * f0 +
+                              ((notes.sum[1][0][c] + notes.sum[1][1][c]) + (notes.sum[1][2][c] + notes.sum[1][3][c])) * f1;
+                    if (l > 0.f) l += notes.odd[piece & 1][c];
+                    float inv = 1.f;
+                    if (!cut) {
+                        const float sk = p.sink ? __ldg(p.sink + head0 + c) * kLog2e : -INFINITY;
+                        const float top = fminf(fmaxf(r, sk), 3e38f);          // (a sink of +inf: out = 0)
+                        const float f = fast_exp2(r - top);
+                        const float all = l * f + fast_exp2(sk - top);
+                        const bool some = all > 0.f || all != all;
+                        inv = some ? vmul * f / all : 0.f;
+                        if (gt == 0) {
+                            const float l2 = some ? top + log2f(all) : -INFINITY;
+                            if (p.lse) p.lse[row + c] = l2 * kLn2;
+                            if (p.lse2) p.lse2[row + c] = l2;
+                        }
+                    } else if (gt == 0) {
+                        p.part_ml[(size_t)entry * HEADS + c] = make_float2(r, l);
+                    }
+                    if (gt >= D) continue;
+                    const float x = nan >> (gt >> 4) & 1 || l != l ? NAN : (o[c] * f0 + others[c * 128 + gt] * f1) * inv;
+                    if (cut)
+                        p.part_o[((size_t)entry * HEADS + c) * D + gt] = x;
+                    else
+                        static_cast<uint16_t*>(p.out)[(row + c) * D + gt] = static_cast<uint16_t>(pack2<S::QBF16>(x, 0.f));
+                }
+            }
+            named_barrier_sync(3, 256);            // (all of it has been read)
             at = next;
-            parity ^= 1;
-            softmax_sync();                        // (sums and references have been read)
+            i0 += count;
         }
-    } else {
-        // (no tiles: nothing is waited for)
     }
 
     // every MMA and copy has ended before shared memory and TMEM go
-    if (warp == 7) {
+    if (warp == 13) {
         const uint64_t since = globaltimer_ns();
         while (!mbar_try(bar(notes.drained), 0))
             if (globaltimer_ns() - since > kWaitNs4) break;
@@ -784,7 +849,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 7) tmem_dealloc(tmem, S::COLS);
+    if (warp == 13) tmem_dealloc(tmem, S::COLS);
 }
 
 template <class S>
