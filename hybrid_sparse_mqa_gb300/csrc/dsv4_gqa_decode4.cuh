@@ -183,6 +183,16 @@ __device__ __forceinline__ uint64_t f32_pair(float lo, float hi) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
     return r;
 }
+__device__ __forceinline__ float2 f32_of(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -339,24 +349,27 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             // lanes 0 and 1: the page of a group of the tile, and whether it holds slots to attend
             int page = -1;
             bool wanted = false;
-            auto slot_of = [&]() { return (at.rg.lo / kTile4 + static_cast<int>(at.at - at.seg)) * kTile4 + 32 * w; };
+            int slot = 0;                          // the first of the warp's slots of the tile
+            const int* table = nullptr;
             auto look = [&]() {
-                const int slot = slot_of() + lane * 16;
+                const int s = slot + lane * 16;
                 page = -1;
-                wanted = lane < 2 && slot < at.rg.n && slot + 16 > at.rg.lo;
-                if (wanted) page = __ldg(p.c.table + (long long)at.rq.row * p.c.table_stride + (slot >> p.c.page_shift));
+                wanted = lane < 2 && s < at.rg.n && s + 16 > at.rg.lo;
+                if (wanted) page = __ldg(table + (s >> p.c.page_shift));
             };
             long long head = 0, block_head = 0;    // this lane's place in the KV head
             auto come_to = [&]() {
                 head = at.hc * p.c.head_stride + lane_off;
                 block_head = at.hc * p.c.b_head_stride + lane_block;
+                slot = (at.rg.lo / kTile4 + static_cast<int>(at.at - at.seg)) * kTile4 + 32 * w;
+                table = p.c.table + (long long)at.rq.row * p.c.table_stride;
             };
             come_to();
             look();
             int e = 0;
             uint32_t turn = 1;                     // parity that an entry's last reading has; 1: nothing was there
             for (int i = 0; i < tiles; ++i) {
-                const int slot0 = slot_of(), lo = at.rg.lo, n = at.rg.n;
+                const int slot0 = slot, lo = at.rg.lo, n = at.rg.n;
                 const bool begins = i == 0 || at.at == at.seg;
                 const bool valid = page >= 0 && page < p.c.num_pages;
                 if (wanted && !valid) atomicOr(p.err, DSV4_DEV_ERR_GQA_PAGE);
@@ -372,6 +385,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                 // the next tile's pages are on their way while this one's entries are waited for
                 ++at.at;
                 if (at.at < at.end) {
+                    slot += kTile4;
                     look();
                 } else if (at.next_segment(p, hcs, t1)) {
                     come_to();
@@ -555,7 +569,8 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
         // ============================================================ softmax and output
         const int g = warp >> 2, quad = warp & 3, gt = tid & 127;
         const uint32_t lane_t = tmem + (quad * 32u << 16);
-        const uint32_t p_to = s_p + g * S::P_BYTES + quad * S::NO * 128 + (lane & 3) * 4;
+        // this slot's place in a line of P, of which piece c of 16 bytes lies at c ^ head
+        const uint32_t p_to = s_p + g * S::P_BYTES + quad * S::NO * 128 + lane * 4;
         Cursor<kTile4> at;
         at.at = t0;
         at.locate(p, hcs, lane, early, request_of);
@@ -638,8 +653,9 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             load_q(at);
             write_q(0);
         }
-        float o[HEADS], lsum[HEADS];               // sums taken out of the accumulator; of this thread's weights
-        float ref[HEADS];                          // the softmax's references, the same in all threads of the group
+        // Pairs of heads: sums taken out of the accumulator; of this thread's weights; and, the same in all threads of the
+        // group, the softmax's references, negated
+        uint64_t o[HEADS / 2], lsum[HEADS / 2], ref[HEADS / 2];
         uint32_t nan = 0;
         int kept = 0;                              // tiles in the accumulator
         // the sums over the group's tiles up to i come out of the accumulator
@@ -649,9 +665,9 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             float x[S::USED];
             tmem_ld<S::USED>(lane_t + S::T_O + g * S::NO, x);
 #pragma unroll
-            for (int c = 0; c < HEADS; ++c) {
-                o[c] += x[c];
-                if constexpr (S::TWO) o[c] += x[HEADS + c];
+            for (int c = 0; c < HEADS; c += 2) {
+                o[c / 2] = add_pair(o[c / 2], f32_pair(x[c], x[c + 1]));
+                if constexpr (S::TWO) o[c / 2] = add_pair(o[c / 2], f32_pair(x[HEADS + c], x[HEADS + c + 1]));
             }
             tc_fence_before();
         };
@@ -661,9 +677,9 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             bool ask = next.next_segment(p, hcs, t1) && g == 0;        // the next piece's digits are still to be written
             if (ask) load_q(next);
 #pragma unroll
-            for (int c = 0; c < HEADS; ++c) {
-                o[c] = lsum[c] = 0.f;
-                ref[c] = kNoMax;
+            for (int c = 0; c < HEADS / 2; ++c) {
+                o[c] = lsum[c] = 0;
+                ref[c] = f32_pair(-kNoMax, -kNoMax);
             }
             nan = 0;
             kept = 0;
@@ -692,29 +708,32 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                 // log2-unit scores below their reference
                 const bool in = slot >= at.rg.lo && slot < at.rg.n &&
                                 (*(volatile uint8_t*)&notes.ok[i % kRing4][quad] >> (lane >> 4) & 1);
-                float s[HEADS], x[HEADS];
-                bool above = false;
+                uint64_t x[HEADS / 2];
+                float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < HEADS; c += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(&notes.mul[piece & 1][c]);
-                    const float mul[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        asm("{\n .reg .b32 h;\n mov.b64 {%0, h}, %1;\n}\n"
-                            : "=f"(s[c + j])
-                            : "l"(j & 1 ? s2[(c + j) / 2] >> 32 : s2[(c + j) / 2]));
-                        x[c + j] = in ? fmaf(s[c + j], mul[j], -ref[c + j]) : -INFINITY;
-                        above |= x[c + j] > 8.f;
-                    }
+                for (int c = 0; c < HEADS / 2; c += 2) {
+                    const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(&notes.mul[piece & 1][2 * c]);
+                    x[c] = fma_pair(s2[c], m.x, ref[c]);
+                    x[c + 1] = fma_pair(s2[c + 1], m.y, ref[c + 1]);
                 }
+                const bool all_in = __all_sync(0xffffffffu, in);
+                if (!all_in) {
+#pragma unroll
+                    for (int c = 0; c < HEADS / 2; ++c) x[c] = in ? x[c] : f32_pair(-INFINITY, -INFINITY);
+                }
+#pragma unroll
+                for (int c = 0; c < HEADS / 2; ++c) {
+                    const float2 y = f32_of(x[c]);
+                    top = fmaxf(top, fmaxf(y.x, y.y));
+                }
+                const bool above = top > 8.f;
                 if (p.logits) {
-                    float4* to = reinterpret_cast<float4*>(p.logits + ((size_t)(at.at + (i - i0)) * kTile4 + gt) * HEADS);
+                    float2* to = reinterpret_cast<float2*>(p.logits + ((size_t)(at.at + (i - i0)) * kTile4 + gt) * HEADS);
 #pragma unroll
-                    for (int c = 0; c < HEADS; c += 4) {
-                        float y[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) y[j] = in ? s[c + j] * notes.mul[piece & 1][c + j] : -INFINITY;
-                        to[c / 4] = make_float4(y[0], y[1], y[2], y[3]);
+                    for (int c = 0; c < HEADS / 2; ++c) {
+                        const float2 y = f32_of(s2[c]);
+                        to[c] = in ? make_float2(y.x * notes.mul[piece & 1][2 * c], y.y * notes.mul[piece & 1][2 * c + 1])
+                                   : make_float2(-INFINITY, -INFINITY);
                     }
                 }
                 const bool moves = softmax_any(above, g);
@@ -729,37 +748,47 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                     nan |= *(volatile uint16_t*)&notes.nan[(i - 2) % kRing4];
                 }
                 if (moves) {
+                    const float* mul = notes.mul[piece & 1];
 #pragma unroll
                     for (int c = 0; c < HEADS; ++c) {
                         // the warp's largest score, as an integer of the same order (a NaN counts as -inf)
-                        const int y = __float_as_int(in ? fmaxf(s[c] * notes.mul[piece & 1][c], -INFINITY) : -INFINITY);
+                        const float2 y2 = f32_of(s2[c / 2]);
+                        const float z = (c & 1 ? y2.y : y2.x) * mul[c];
+                        const int y = __float_as_int(in ? fmaxf(z, -INFINITY) : -INFINITY);
                         const int m = __reduce_max_sync(0xffffffffu, y ^ (y >> 31 & 0x7fffffff));
                         if (lane == 0) notes.top[g][quad][c] = __int_as_float(m ^ (m >> 31 & 0x7fffffff));
                     }
                     softmax_sync(g);
 #pragma unroll
-                    for (int c = 0; c < HEADS; ++c) {
-                        const float top = fmaxf(fmaxf(notes.top[g][0][c], notes.top[g][1][c]),
-                                                fmaxf(notes.top[g][2][c], notes.top[g][3][c]));
-                        const float r = fmaxf(ref[c], top), f = fast_exp2(ref[c] - r);
-                        ref[c] = r;
-                        lsum[c] *= f;
-                        o[c] *= f;
-                        x[c] = in ? fmaf(s[c], notes.mul[piece & 1][c], -r) : -INFINITY;
+                    for (int c = 0; c < HEADS; c += 2) {
+                        const float2 was = f32_of(ref[c / 2]), y = f32_of(s2[c / 2]), ls = f32_of(lsum[c / 2]), os = f32_of(o[c / 2]);
+                        auto largest = [&](int k) {
+                            return fmaxf(fmaxf(notes.top[g][0][k], notes.top[g][1][k]), fmaxf(notes.top[g][2][k], notes.top[g][3][k]));
+                        };
+                        const float r0 = fmaxf(-was.x, largest(c)), r1 = fmaxf(-was.y, largest(c + 1));
+                        const float f0 = fast_exp2(-was.x - r0), f1 = fast_exp2(-was.y - r1);
+                        ref[c / 2] = f32_pair(-r0, -r1);
+                        lsum[c / 2] = f32_pair(ls.x * f0, ls.y * f1);
+                        o[c / 2] = f32_pair(os.x * f0, os.y * f1);
+                        x[c / 2] = in ? f32_pair(fmaf(y.x, mul[c], -r0), fmaf(y.y, mul[c + 1], -r1)) : f32_pair(-INFINITY, -INFINITY);
                     }
                     // (the next tile's vote lies between this reading and the next writing)
                 }
                 // P, head by head a line of 32 slots
-#pragma unroll
-                for (int c = 0; c < HEADS; ++c) {
-                    const uint32_t to = p_to + c * 128 + (((lane >> 2) ^ c) << 4);
-                    const float y = fast_exp2(x[c]);
-                    lsum[c] += y;
-                    const uint32_t hi = to_tf32(y);
+                auto put = [&](int c, float y) {
+                    const uint32_t to = (p_to ^ (c << 4)) + c * 128, hi = to_tf32(y);
                     asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
                     if constexpr (S::TWO)
                         asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + HEADS * 128), "r"(__float_as_uint(y - __uint_as_float(hi)))
                                      : "memory");
+                };
+#pragma unroll
+                for (int c = 0; c < HEADS; c += 2) {
+                    const float2 z = f32_of(x[c / 2]);
+                    const float y0 = fast_exp2(z.x), y1 = fast_exp2(z.y);
+                    lsum[c / 2] = add_pair(lsum[c / 2], f32_pair(y0, y1));
+                    put(c, y0);
+                    put(c + 1, y1);
                 }
                 if (gt == 0) *(volatile int*)&notes.fresh[g] = kept == 0;
                 ++kept;
@@ -775,7 +804,8 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             // ---- the piece's sums: the odd group's to the even one, which writes the output ----
 #pragma unroll
             for (int c = 0; c < HEADS; ++c) {
-                float x = lsum[c];
+                const float2 ls = f32_of(lsum[c / 2]);
+                float x = c & 1 ? ls.y : ls.x;
 #pragma unroll
                 for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
                 if (lane == 0) notes.sum[g][quad][c] = x;
@@ -788,8 +818,9 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             if (g == 1) {
 #pragma unroll
                 for (int c = 0; c < HEADS; ++c) {
-                    others[c * 128 + gt] = o[c];
-                    if (gt == 0) notes.odd_ref[c] = ref[c];
+                    const float2 os = f32_of(o[c / 2]), r = f32_of(ref[c / 2]);
+                    others[c * 128 + gt] = c & 1 ? os.y : os.x;
+                    if (gt == 0) notes.odd_ref[c] = c & 1 ? -r.y : -r.x;
                 }
                 if (gt == 0) notes.odd_nan = nan;
             }
@@ -804,8 +835,9 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
 #pragma unroll
                 for (int c = 0; c < HEADS; ++c) {
                     if (c >= p.group) break;
-                    const float r = fmaxf(ref[c], notes.odd_ref[c]);
-                    const float f0 = fast_exp2(ref[c] - r), f1 = fast_exp2(notes.odd_ref[c] - r);
+                    const float2 refs = f32_of(ref[c / 2]), os = f32_of(o[c / 2]);
+                    const float mine = c & 1 ? -refs.y : -refs.x, r = fmaxf(mine, notes.odd_ref[c]);
+                    const float f0 = fast_exp2(mine - r), f1 = fast_exp2(notes.odd_ref[c] - r);
                     float l = ((notes.sum[0][0][c] + notes.sum[0][1][c]) + (notes.sum[0][2][c] + notes.sum[0][3][c])) * f0 +
                               ((notes.sum[1][0][c] + notes.sum[1][1][c]) + (notes.sum[1][2][c] + notes.sum[1][3][c])) * f1;
                     if (l > 0.f) l += notes.odd[piece & 1][c];
@@ -826,7 +858,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                         p.part_ml[(size_t)entry * HEADS + c] = make_float2(r, l);
                     }
                     if (gt >= D) continue;
-                    const float x = nan >> (gt >> 4) & 1 || l != l ? NAN : (o[c] * f0 + others[c * 128 + gt] * f1) * inv;
+                    const float x = nan >> (gt >> 4) & 1 || l != l ? NAN : ((c & 1 ? os.y : os.x) * f0 + others[c * 128 + gt] * f1) * inv;
                     if (cut)
                         p.part_o[((size_t)entry * HEADS + c) * D + gt] = x;
                     else
