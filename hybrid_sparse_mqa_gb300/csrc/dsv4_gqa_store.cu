@@ -144,19 +144,15 @@ struct Packer {
     }
 };
 
-// max(|x|, |y|) of two pairs, NaN kept.
+// max(|x|, |y|) of two pairs, NaN kept; the sign is any.
 template <int TYPE>
 __device__ __forceinline__ uint32_t abs_max2(uint32_t x, uint32_t y) {
-    x &= 0x7fff7fffu;
-    y &= 0x7fff7fffu;
-    if constexpr (TYPE == DSV4_GQA_BF16) {
-        const __nv_bfloat162 m =
-            __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
-        return *reinterpret_cast<const uint32_t*>(&m);
-    } else {
-        const __half2 m = __hmax2_nan(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
-        return *reinterpret_cast<const uint32_t*>(&m);
-    }
+    uint32_t r;
+    if constexpr (TYPE == DSV4_GQA_BF16)
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    else
+        asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
 }
 // Eight values -> eight e2m1 codes (to nearest, ties to even, saturating), the first in the lowest half byte.
 __device__ __forceinline__ uint32_t e2m1x8(const float2 (&v)[4]) {
@@ -174,8 +170,9 @@ __device__ __forceinline__ uint32_t e2m1x8(const float2 (&v)[4]) {
 // scale by one division; the codes of the correctly rounded quotients by one
 // Markstein correction of x y, y = RN(1 / step), as above.  There the bounds on
 // the head's scale keep the step (2^-9 to 448 times it) where nothing over- or
-// underflows that a code depends on: values are clamped to 8 steps first (6.x
-// and more saturate), and quotients below 1/4 have code 0 either way.
+// underflows that a code depends on: a block's values are at most 9 steps, or
+// where the largest step is too small for them clamped to 8 first (6.x and more
+// saturate); quotients below 1/4 have code 0 either way.
 template <int TYPE>
 struct BlockPacker {
     float scale;
@@ -190,22 +187,29 @@ struct BlockPacker {
         uint32_t m = abs_max2<TYPE>(w[0], w[1]);
 #pragma unroll
         for (int j = 2; j < 8; ++j) m = abs_max2<TYPE>(m, w[j]);
-        const float2 top = widen<TYPE>(abs_max2<TYPE>(m, m >> 16));
-        const uint32_t code = e4m3x2(make_float2(__fdiv_rn(top.x, 6.f * scale), 0.f)) & 0xffu;
+        const float top = fabsf(widen<TYPE>(abs_max2<TYPE>(m, m >> 16)).x);
+        const uint32_t code = e4m3x2(make_float2(__fdiv_rn(top, 6.f * scale), 0.f)) & 0xffu;
         float f[4];
         e4m3x4_to_f32(code, f);
         const float step = f[0] * scale;
         uint32_t c[2];
         if (fast) {
             const float y = __frcp_rn(step);
-            const uint32_t lim = narrow<TYPE>(8.f * step, 8.f * step);
+            uint32_t x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = w[j];
+            if (code == 0x7eu) {                   // (else no value has more than 9 steps)
+                const uint32_t lim = narrow<TYPE>(8.f * step, 8.f * step);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = clamp2<TYPE>(w[j], lim);
+            }
             const uint64_t ny2 = f32x2(-y, -y), s2 = f32x2(step, step);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float2 v[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 n = widen<TYPE>(clamp2<TYPE>(w[4 * i + j], lim) ^ 0x80008000u);
+                    const float2 n = widen<TYPE>(x[4 * i + j] ^ 0x80008000u);
                     const uint64_t n2 = f32x2(n.x, n.y);
                     const uint64_t q0 = mul_f32x2(n2, ny2);
                     const uint64_t q = fma_f32x2(fma_f32x2(q0, s2, n2), ny2, q0);
