@@ -222,10 +222,10 @@ struct Notes {
     // of tiles: valid 16-slot groups, two bits for each copying warp; bit 4: begins a piece
     uint8_t ok[kRing4][4];
     uint16_t nan[kRing4];                                    // and blocks of V that hold a NaN
-    uint32_t odd_nan;                                        // the same of the odd group's tiles of a piece
+    uint32_t nans[2];                                        // the same of a group's tiles of a piece
     alignas(16) float mul[2][S::HEADS];                      // score factors, by parity of the piece (read as float4)
     float odd[2][S::HEADS];                                  // NaN for a head whose query is not finite, else 0
-    float top[2][4][S::HEADS], sum[2][4][S::HEADS], odd_ref[S::HEADS];
+    float top[2][4][S::HEADS], sum[2][4][S::HEADS], ref[2][S::HEADS];
 };
 
 template <class S>
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                     y[2 * k] = f.x * up;
                     y[2 * k + 1] = f.y * up;
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     uint32_t codes = 0;
 #pragma unroll
@@ -801,43 +801,52 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             }
             if (ask) write_q(piece + 1);
 
-            // ---- the piece's sums: the odd group's to the even one, which writes the output ----
-#pragma unroll
-            for (int c = 0; c < HEADS; ++c) {
-                const float2 ls = f32_of(lsum[c / 2]);
-                float x = c & 1 ? ls.y : ls.x;
-#pragma unroll
-                for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-                if (lane == 0) notes.sum[g][quad][c] = x;
+            // ---- the piece's sums meet in shared memory; its output, heads in turn to the groups ----
+            // (loops and not straight code: what runs once a piece comes from far away)
+            {
+                // a head's sum over the warp to lanes 4 head .. 4 head + 3
+                const bool up = lane & 16, mid = lane & 8, low = lane & 4;
+                auto across = [&](uint64_t x, int k) {
+                    const float2 y = f32_of(x);
+                    return f32_pair(__shfl_xor_sync(0xffffffffu, y.x, k), __shfl_xor_sync(0xffffffffu, y.y, k));
+                };
+                const uint64_t a0 = add_pair(up ? lsum[2] : lsum[0], across(up ? lsum[0] : lsum[2], 16));
+                const uint64_t a1 = add_pair(up ? lsum[3] : lsum[1], across(up ? lsum[1] : lsum[3], 16));
+                const float2 b = f32_of(add_pair(mid ? a1 : a0, across(mid ? a0 : a1, 8)));
+                float l = (low ? b.y : b.x) + __shfl_xor_sync(0xffffffffu, low ? b.x : b.y, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                if (!(lane & 3)) notes.sum[g][quad][lane >> 2] = l;
             }
             if (kept > 0) {
                 take_o(i - 2);
                 nan |= *(volatile uint16_t*)&notes.nan[(i - 2) % kRing4];
             }
-            float* others = reinterpret_cast<float*>(smem + S::O_P + S::P_BYTES);        // (the odd group's P has been read)
-            if (g == 1) {
+            float* const sums = reinterpret_cast<float*>(smem + S::O_P);         // (P of both has been read)
 #pragma unroll
-                for (int c = 0; c < HEADS; ++c) {
-                    const float2 os = f32_of(o[c / 2]), r = f32_of(ref[c / 2]);
-                    others[c * 128 + gt] = c & 1 ? os.y : os.x;
-                    if (gt == 0) notes.odd_ref[c] = c & 1 ? -r.y : -r.x;
+            for (int c = 0; c < HEADS; c += 2) {
+                const float2 os = f32_of(o[c / 2]), r = f32_of(ref[c / 2]);
+                float* to = sums + (g * S::P_BYTES + c * 512) / 4 + gt;
+                to[0] = os.x;
+                to[128] = os.y;
+                if (gt == 0) {
+                    notes.ref[g][c] = -r.x;
+                    notes.ref[g][c + 1] = -r.y;
                 }
-                if (gt == 0) notes.odd_nan = nan;
             }
+            if (gt == 0) notes.nans[g] = nan;
             named_barrier_sync(3, 256);
-            if (g == 0) {
-                nan |= notes.odd_nan;
+            {
+                nan |= notes.nans[g ^ 1];
                 const bool begins = at.seg >= t0, cut = !begins || at.end != at.seg + at.rg.tiles;
                 const int h = at.hc, head0 = h * p.group;
                 const float vmul = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
                 const size_t row = (size_t)at.b * p.heads + head0;
                 const int entry = piece_entry(share, begins);
-#pragma unroll
-                for (int c = 0; c < HEADS; ++c) {
-                    if (c >= p.group) break;
-                    const float2 refs = f32_of(ref[c / 2]), os = f32_of(o[c / 2]);
-                    const float mine = c & 1 ? -refs.y : -refs.x, r = fmaxf(mine, notes.odd_ref[c]);
-                    const float f0 = fast_exp2(mine - r), f1 = fast_exp2(notes.odd_ref[c] - r);
+#pragma unroll 1
+                for (int c = g; c < p.group; c += 2) {
+                    const float r0 = notes.ref[0][c], r1 = notes.ref[1][c], r = fmaxf(r0, r1);
+                    const float f0 = fast_exp2(r0 - r), f1 = fast_exp2(r1 - r);
                     float l = ((notes.sum[0][0][c] + notes.sum[0][1][c]) + (notes.sum[0][2][c] + notes.sum[0][3][c])) * f0 +
                               ((notes.sum[1][0][c] + notes.sum[1][1][c]) + (notes.sum[1][2][c] + notes.sum[1][3][c])) * f1;
                     if (l > 0.f) l += notes.odd[piece & 1][c];
@@ -858,7 +867,8 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                         p.part_ml[(size_t)entry * HEADS + c] = make_float2(r, l);
                     }
                     if (gt >= D) continue;
-                    const float x = nan >> (gt >> 4) & 1 || l != l ? NAN : ((c & 1 ? os.y : os.x) * f0 + others[c * 128 + gt] * f1) * inv;
+                    const float* from = sums + c * 128 + gt;
+                    const float x = nan >> (gt >> 4) & 1 || l != l ? NAN : (from[0] * f0 + from[S::P_BYTES / 4] * f1) * inv;
                     if (cut)
                         p.part_o[((size_t)entry * HEADS + c) * D + gt] = x;
                     else
