@@ -728,12 +728,13 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                 }
                 const bool above = top > 8.f;
                 if (p.logits) {
-                    float2* to = reinterpret_cast<float2*>(p.logits + ((size_t)(at.at + (i - i0)) * kTile4 + gt) * HEADS);
+                    float4* to = reinterpret_cast<float4*>(p.logits + ((size_t)(at.at + (i - i0)) * kTile4 + gt) * HEADS);
 #pragma unroll
-                    for (int c = 0; c < HEADS / 2; ++c) {
-                        const float2 y = f32_of(s2[c]);
-                        to[c] = in ? make_float2(y.x * notes.mul[piece & 1][2 * c], y.y * notes.mul[piece & 1][2 * c + 1])
-                                   : make_float2(-INFINITY, -INFINITY);
+                    for (int c = 0; c < HEADS; c += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(&notes.mul[piece & 1][c]);
+                        const float2 y = f32_of(s2[c / 2]), z = f32_of(s2[c / 2 + 1]);
+                        to[c / 4] = in ? make_float4(y.x * m.x, y.y * m.y, z.x * m.z, z.y * m.w)
+                                       : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
                     }
                 }
                 const bool moves = softmax_any(above, g);
