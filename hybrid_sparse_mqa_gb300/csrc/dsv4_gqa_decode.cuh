@@ -335,7 +335,7 @@ struct Shape {
     static constexpr bool BF16 = KIND == DSV4_GQA_BF16;      // operand type of the MMAs (codes: f16)
     static constexpr bool QBF16 = QKIND == DSV4_GQA_BF16;
     static_assert(CODES || QKIND == KIND, "only rows of codes are read by queries of another type");
-    // P in two pieces.  One f16 is off by 2^-12 of it, an eighth of a bf16 output's rounding but as much as an f16
+    // P in two pieces.  One f16 is off by up to 2^-11 of it, a quarter of a bf16 output's rounding but as much as an f16
     // output's: 8 x 1024..16384 e4m3 rows of 128, 32 / 4 heads, f16 out: an error of 5.7e-6 (rms) with one piece and of
     // 4.3e-6, the output's own rounding, with two
     static constexpr bool TWO = !CODES || !QBF16;
