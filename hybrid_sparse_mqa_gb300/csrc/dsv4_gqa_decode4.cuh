@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
     const uint32_t s_i = base + S::O_I, s_q = base + S::O_Q, s_p = base + S::O_P, ring = base + S::O_RING;
     auto bar = [&](uint64_t& b) { return smem_u32(&b); };
 
-    // ---- what does not depend on the call's data ----
+    // ---- what does not depend on the call's data (TMEM before the next kernel may start, which could take it first) ----
     if (warp == 13) tmem_alloc(smem_u32(&notes.tmem), S::COLS);
     if (tid == 0) {
 #pragma unroll

@@ -23,6 +23,10 @@ namespace {
 
 constexpr int kStoreThreads = 128;
 constexpr int kItems = 2;                  // tokens per thread
+// Blocks of 16 values of a token that a thread takes: two of a 4-bit cache, whose codes cost the issue slots so much that
+// the token's addresses should not be worked out for every block (PLACEHOLDER).
+template <int FORMAT>
+constexpr int kBlocks = FORMAT == DSV4_GQA_E2M1 ? 2 : 1;
 
 struct StoreParams {
     Cache c;
@@ -154,6 +158,12 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t x, uint32_t y) {
         asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
     return r;
 }
+// An e4m3 code -> float, exactly.
+__device__ __forceinline__ float e4m3_f32(uint32_t code) {
+    uint32_t h;
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(h) : "r"(code));
+    return __low2float(*reinterpret_cast<const __half2*>(&h));
+}
 // Eight values -> eight e2m1 codes (to nearest, ties to even, saturating), the first in the lowest half byte.
 __device__ __forceinline__ uint32_t e2m1x8(const float2 (&v)[4]) {
     uint32_t r;
@@ -189,9 +199,7 @@ struct BlockPacker {
         for (int j = 2; j < 8; ++j) m = abs_max2<TYPE>(m, w[j]);
         const float top = fabsf(widen<TYPE>(abs_max2<TYPE>(m, m >> 16)).x);
         const uint32_t code = e4m3x2(make_float2(__fdiv_rn(top, 6.f * scale), 0.f)) & 0xffu;
-        float f[4];
-        e4m3x4_to_f32(code, f);
-        const float step = f[0] * scale;
+        const float step = e4m3_f32(code) * scale;
         uint32_t c[2];
         if (fast) {
             const float y = __frcp_rn(step);
@@ -237,14 +245,14 @@ struct BlockPacker {
 // FORMAT: of the cache; TYPE: of the rows (BF16 for a plain copy of either).
 template <int TYPE, int FORMAT, int PIECES>
 __global__ void __launch_bounds__(kStoreThreads) dsv4_gqa_store_kernel(const __grid_constant__ StoreParams p) {
-    constexpr int kTokens = kStoreThreads / PIECES;          // of one item
+    constexpr int kB = kBlocks<FORMAT>, kLanes = PIECES / kB, kTokens = kStoreThreads / kLanes;        // of one item
     grid_dependency_wait();
     grid_dependents_go();
     const int heads2 = 2 * p.c.kv_heads;
     const int hw = blockIdx.x % heads2, which = hw & 1, h = hw >> 1;
-    const int piece = threadIdx.x % PIECES;
-    const int i0 = blockIdx.x / heads2 * (kTokens * kItems) + threadIdx.x / PIECES;
-    uint4 a[kItems], b[kItems];
+    const int piece = threadIdx.x % kLanes;      // and those kLanes further on
+    const int i0 = blockIdx.x / heads2 * (kTokens * kItems) + threadIdx.x / kLanes;
+    uint4 a[kItems][kB], b[kItems][kB];
     int r[kItems], s[kItems], page[kItems];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
@@ -255,8 +263,11 @@ __global__ void __launch_bounds__(kStoreThreads) dsv4_gqa_store_kernel(const __g
                                                               h * p.head_stride[which]) + 2 * piece;
             r[k] = __ldg(p.req_rows + i);
             s[k] = __ldg(p.slots + i);
-            a[k] = __ldcs(src);
-            b[k] = __ldcs(src + 1);
+#pragma unroll
+            for (int u = 0; u < kB; ++u) {
+                a[k][u] = __ldcs(src + 2 * kLanes * u);
+                b[k][u] = __ldcs(src + 2 * kLanes * u + 1);
+            }
         }
     }
 #pragma unroll
@@ -286,15 +297,18 @@ __global__ void __launch_bounds__(kStoreThreads) dsv4_gqa_store_kernel(const __g
         const int in_page = s[k] & ((1 << p.c.page_shift) - 1);
         uint4* dst = reinterpret_cast<uint4*>(pool + page[k] * p.c.page_stride + in_page * p.c.row_stride);
         if constexpr (FORMAT == DSV4_GQA_E2M1) {
-            uint2 codes;
-            blocks[page[k] * p.c.b_page_stride + in_page * p.c.b_row_stride + piece] =
-                static_cast<uint8_t>(pack_block.codes16(a[k], b[k], codes));
-            reinterpret_cast<uint2*>(dst)[piece] = codes;
+            uint8_t* scales = blocks + page[k] * p.c.b_page_stride + in_page * p.c.b_row_stride + piece;
+#pragma unroll
+            for (int u = 0; u < kB; ++u) {
+                uint2 codes;
+                scales[kLanes * u] = static_cast<uint8_t>(pack_block.codes16(a[k][u], b[k][u], codes));
+                reinterpret_cast<uint2*>(dst)[piece + kLanes * u] = codes;
+            }
         } else if constexpr (FORMAT == DSV4_GQA_E4M3) {
-            dst[piece] = pack.codes16(a[k], b[k]);
+            dst[piece] = pack.codes16(a[k][0], b[k][0]);
         } else {
-            dst[2 * piece] = a[k];
-            dst[2 * piece + 1] = b[k];
+            dst[2 * piece] = a[k][0];
+            dst[2 * piece + 1] = b[k][0];
         }
         if (piece == 0 && which == 0) {
             const long long t = ((long long)r[k] * p.c.kv_heads + h) * p.width + s[k];
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(kStoreThreads) dsv4_gqa_store_kernel(const __g
 
 template <int TYPE, int FORMAT>
 int launch_store(const StoreParams& p, int head_dim, void* stream) {
-    const int tokens = kStoreThreads / (head_dim / 16) * kItems;
+    const int tokens = kStoreThreads / (head_dim / 16) * kBlocks<FORMAT> * kItems;
     const long long blocks = ((long long)p.n + tokens - 1) / tokens * 2 * p.c.kv_heads;
     if (blocks > 0x7fffffffLL) return DSV4_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(blocks));
