@@ -328,7 +328,7 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
 // KIND: DSV4_GQA_BF16 / F16 / E4M3 / E2M1; QKIND: of the queries and the output,
 // BF16 or F16.  A warp's stage is TT rows of K and of V, and of their block scales
 // behind both (E2M1).
-template <int KIND_, int QKIND, int D_, int NT_>
+template <int KIND_, int QKIND, int D_, int NT_, bool MANY = false>
 struct Shape {
     static constexpr int KIND = KIND_, D = D_, NT = NT_;
     static constexpr bool FP8 = KIND == DSV4_GQA_E4M3, FP4 = KIND == DSV4_GQA_E2M1, CODES = FP8 || FP4;
@@ -355,9 +355,12 @@ struct Shape {
     static constexpr int W = kWarps;
     static constexpr int TILE_BYTES = TT * ROWB;             // K or V of a stage
     static constexpr int BLOCK_BYTES = TT * BLKB;            // their block scales
-    static constexpr int STAGES = FP4 ? 5 : 3;
+    // MANY (rows of 4 bits, a CTA per segment, more of them than run at once): shallower rings, so that more CTAs do.
+    // 128 x 1..1000 rows, 8 KV heads of 128: 39.4 us without and 34.0 with, 48 x 1..1000, 16 of 64: 23.6 and 21.5; where all
+    // run at once anyway, 32 x 500..1000 rows: 15.0 and 17.7
+    static constexpr int STAGES = FP4 && !MANY ? 5 : 3;
     static constexpr int STAGE_BYTES = 2 * (TILE_BYTES + BLOCK_BYTES);
-    static constexpr int CTAS = TILE_BYTES > 4096 ? 1 : 2;   // per SM (what shared memory holds)
+    static constexpr int CTAS = TILE_BYTES > 4096 ? 1 : !MANY ? 2 : D == 64 ? 4 : 3;     // per SM (what shared memory holds)
     static constexpr int WARP_RING = STAGES * STAGE_BYTES;
     static constexpr int RING_BYTES = W * WARP_RING;
     // queries of a segment, a row per head (16 bytes of padding spread the rows over the banks where there is room)

@@ -910,12 +910,16 @@ inline int launch_decode4_dim(const DecodeParams& p, int nt, void* stream) {
     using S = Shape4<QKIND, D>;
     using One = Shape<DSV4_GQA_E2M1, QKIND, D, 1>;
     using Two = Shape<DSV4_GQA_E2M1, QKIND, D, 2>;
+    using Many = Shape<DSV4_GQA_E2M1, QKIND, D, 1, true>;
     const int rc = once_per_device(ready, [] {
-        return prepare_decode_shape<One>() && prepare_decode_shape<Two>() && prepare_decode4_shape<S>();
+        return prepare_decode_shape<One>() && prepare_decode_shape<Many>() && prepare_decode_shape<Two>() &&
+               prepare_decode4_shape<S>();
     });
     if (rc) return rc;
     if (nt == 2) return launch_decode_shape<Two>(p, stream);
-    if (p.cluster) return launch_decode_shape<One>(p, stream);
+    if (p.cluster)
+        return (long long)p.batch * p.c.kv_heads > kMaxCtas ? launch_decode_shape<Many>(p, stream)
+                                                            : launch_decode_shape<One>(p, stream);
     return launch(dsv4_gqa_decode4_kernel<S>, dim3(p.warps), kThreads4, S::SMEM, stream, 1, p);
 }
 

@@ -44,6 +44,16 @@ def test_more_segments_than_ctas(A, q, dim, group):  # noqa: F811
     check_decode(A, c, lens, 7 * group, weights=True, req=[int(x) for x in torch.randperm(70, generator=gen)])
 
 
+@pytest.mark.parametrize("q,dim,group", [(BF, 128, 8), (HF, 64, 1), (HF, 128, 3), (BF, 64, 8)])
+def test_more_short_segments_than_ctas(A, q, dim, group):  # noqa: F811
+    # a CTA each, in several waves, with weights and without
+    gen = torch.Generator().manual_seed(group)
+    lens = [int(x) for x in torch.randint(0, 700, (60,), generator=gen)]
+    c = Cache4(q=q, hkv=6, dim=dim, page=16, rows=60, slots=700, seed=dim + group, token_major=True)
+    c.poison(lens)
+    check_decode(A, c, lens, 6 * group, weights=True, window=500, sink=torch.randn(6 * group, generator=c.gen))
+
+
 @pytest.mark.parametrize("q,dim", [(BF, 128), (HF, 64)])
 def test_references_that_move(A, q, dim):  # noqa: F811
     # scores that grow along the slots (most tiles move the reference, back and forth over tiles of both groups), then
