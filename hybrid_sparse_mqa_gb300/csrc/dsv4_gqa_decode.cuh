@@ -340,6 +340,10 @@ struct Shape {
     // 4.3e-6, the output's own rounding, with two
     static constexpr bool TWO = !CODES || !QBF16;
     static constexpr bool LIST = !(FP4 && D <= 128 && NT == 1);      // else dsv4_gqa_decode4.cuh takes the lists
+    // Queries as B operands in shared memory and not in registers: 16 heads of 256 beside 4-bit rows would want 64 of them
+    // beside the output's 128 (64 x 1024..16384 rows, 32 / 2 heads: 141 us with
+    // them in registers, some spilled, and 125 without).
+    static constexpr bool QSMEM = FP4 && D == 256 && NT == 2;
     static constexpr int ROWB = FP4 ? D / 2 : D * (FP8 ? 1 : 2);       // bytes of a row
     static constexpr int BLKB = FP4 ? D / 16 : 0;            // bytes of its block scales
     static constexpr int TT = FP4 ? 2048 / ROWB : 4096 / ROWB < 16 ? 16 : 4096 / ROWB;
@@ -358,7 +362,7 @@ struct Shape {
     // MANY (rows of 4 bits, a CTA per segment, more of them than run at once): shallower rings, so that more CTAs do.
     // 128 x 1..1000 rows, 8 KV heads of 128: 39.4 us without and 34.0 with, 48 x 1..1000, 16 of 64: 23.6 and 21.5; where all
     // run at once anyway, 32 x 500..1000 rows: 15.0 and 17.7
-    static constexpr int STAGES = FP4 && !MANY ? 5 : 3;
+    static constexpr int STAGES = QSMEM ? 4 : FP4 && !MANY ? 5 : 3;
     static constexpr int STAGE_BYTES = 2 * (TILE_BYTES + BLOCK_BYTES);
     static constexpr int CTAS = TILE_BYTES > 4096 ? 1 : !MANY ? 2 : D == 64 ? 4 : 3;     // per SM (what shared memory holds)
     static constexpr int WARP_RING = STAGES * STAGE_BYTES;
@@ -368,7 +372,8 @@ struct Shape {
     // (16 heads of 256 beside e4m3 rows: two CTAs fit an SM only without the buffers; 64 x 1024..16384 rows, 64 / 4
     // heads: 354 us with them and 246 without)
     static constexpr int Q_BYTES = CODES && D == 256 && NT == 2 ? 0 : HEADS * QROW;
-    static constexpr int SMEM = RING_BYTES + W * Q_BYTES;
+    static constexpr int OPERAND_BYTES = QSMEM ? D / 16 * NT * 256 : 0;
+    static constexpr int SMEM = RING_BYTES + W * (Q_BYTES + OPERAND_BYTES);
     static constexpr int PPR = ROWB / 16;                    // 16-byte pieces per row
     static constexpr int RPI = 32 / PPR;                     // rows per warp-wide copy
 };
@@ -773,7 +778,8 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                                          : static_cast<const uint8_t*>(p.q) +
                                                (cons.b * p.q_stride + (long long)head0 * D) * 2;
         const int qrow = in_buffer ? S::QROW : D * 2;
-        uint32_t qf[DT][NT][2];
+        uint32_t qf[S::QSMEM ? 1 : DT][NT][2];
+        const uint32_t q_operands = smem_u32(smem) + S::RING_BYTES + W * S::Q_BYTES + warp * S::OPERAND_BYTES + lane * 16;
         float smul[NT][2];                         // score factor of the two heads whose columns this thread holds
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -791,16 +797,19 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 // and 256: kk = 8 j + i dims 32 (t + 4 j) + 4 i .. + 3)
                 constexpr int PER = S::FP4 && D > 64 ? 8 : 4;
                 float amax = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < DT; ++kk) {
+                auto word = [&](int kk, int u) {
                     const int d2 = (4 * PER * (t4 + 4 * (kk / PER)) + 4 * (kk % PER)) / 2;
+                    return have ? qr[d2 + u] : 0u;
+                };
+#pragma unroll
+                for (int kk = 0; kk < DT; ++kk)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        qf[kk][nt][u] = have ? qr[d2 + u] : 0u;
-                        const float2 f = unpack2<S::QBF16>(qf[kk][nt][u]);
+                        const uint32_t w = word(kk, u);
+                        if constexpr (!S::QSMEM) qf[kk][nt][u] = w;
+                        const float2 f = unpack2<S::QBF16>(w);
                         amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
-                }
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 // 2^e with amax 2^e in [2^14, 2^15); exponents kept where 2^-e and 2^e are normal
@@ -809,12 +818,22 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-                for (int kk = 0; kk < DT; ++kk)
+                for (int kk = 0; kk < DT; ++kk) {
+                    uint32_t w[2];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const float2 f = unpack2<S::QBF16>(qf[kk][nt][u]);
-                        qf[kk][nt][u] = pack2<false>(f.x * up, f.y * up);
+                        uint32_t raw;
+                        if constexpr (S::QSMEM) raw = word(kk, u);
+                        else raw = qf[kk][nt][u];
+                        const float2 f = unpack2<S::QBF16>(raw);
+                        w[u] = pack2<false>(f.x * up, f.y * up);
+                        if constexpr (!S::QSMEM) qf[kk][nt][u] = w[u];
                     }
+                    // (read by the lane that writes it)
+                    if constexpr (S::QSMEM)
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_operands + kk * 512 + nt * 8), "r"(w[0]), "r"(w[1])
+                                     : "memory");
+                }
                 const float mul = p.scale_log2 * kscale * down;
                 smul[nt][0] = __shfl_sync(0xffffffffu, mul, 8 * t4);
                 smul[nt][1] = __shfl_sync(0xffffffffu, mul, 8 * t4 + 4);
@@ -908,9 +927,15 @@ __global__ void __launch_bounds__(S::W * 32, S::CTAS) dsv4_gqa_decode_kernel(con
                             for (int k = 0; k < 2; ++k) {
                                 const uint32_t a[4] = {x[2 * k], y[2 * k], x[2 * k + 1], y[2 * k + 1]};
                                 const int kk = 8 * j + 2 * i + k;
+                                if constexpr (S::QSMEM) {
+                                    const uint4 q = ld_shared_u4(q_operands + kk * 512);
+                                    mma16816<false>(s[m][0], a, q.x, q.y);
+                                    mma16816<false>(s[m][1], a, q.z, q.w);
+                                } else {
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma16816<false>(kChains > 1 && k ? s2[0][0] : s[m][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        mma16816<false>(kChains > 1 && k ? s2[0][0] : s[m][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+                                }
                             }
                         }
                     }
