@@ -7,8 +7,9 @@
 //
 // The instructions that turn codes into 16-bit operands bound a kernel on
 // mma.sync (two conversions and two products for every 4 codes of K and of V
-// and 16 slots; 4.5 bits a value come in faster than that: 48 % of the memory's
-// rate).  Here no thread touches a code:
+// and 16 slots; 4.5 bits a value come in faster than that: 32 x 2048..32768 rows,
+// 32 / 8 heads of 128, 187 us for 659 MB, 2 x 131072 rows 89 us for 302 MB; this
+// kernel: 125 and 61 us, 5.3 and 5.0 TB/s).  Here no thread touches a code:
 //   S   K is the A operand of a 4-bit MMA as it lies in the cache, block scales
 //       and all.  q becomes a B operand of 4 bits without losing any: eight
 //       digits of base 8,
@@ -35,11 +36,13 @@
 // through the scales and issues S, 13 V^T and O.  Two CTAs an SM.  (One softmax
 // group: a tile's chain of waits and steps took 2300 clk of it.)
 //
-// An MMA here costs 9 (tf32, N = 16), 17 (N = 32), 48 (4 bits, N = 64) and
-// 64 clk (identity, N = 128) when its issuer is one thread that elect.sync picked
-// in a converged warp, and 88 clk of issue for each where the thread is picked by
-// its index.  A tile of 8 heads of 128 takes the tensor pipe 370 clk, and its 18
-// KB take an SM 780 clk at the memory's rate.
+// An MMA here costs 9 (tf32, N = 16), 40 (4 bits, N = 32) and 64 clk (identity, N
+// = 128) when its issuer is one thread that elect.sync picked in a converged
+// warp, and 88 clk of issue for each where the thread is picked by its index.  A
+// tile of 8 heads of 128 takes the tensor pipe 440 clk, and its 18 KB take an SM
+// 780 clk at the memory's rate.  Bound by instruction issue (2400 of a tile, 64 %
+// of the slots) and the fetch of five roles' code, beside a start and a join of
+// 12 us together.
 #pragma once
 #include <cstddef>
 
