@@ -11,13 +11,12 @@
 // 32 / 8 heads of 128, 187 us for 659 MB, 2 x 131072 rows 89 us for 302 MB; this
 // kernel: 125 and 61 us, 5.3 and 5.0 TB/s).  Here no thread touches a code:
 //   S   K is the A operand of a 4-bit MMA as it lies in the cache, block scales
-//       and all.  q becomes a B operand of 4 bits without losing any: eight
-//       digits of base 8,
+//       and all.  q becomes a B operand of 4 bits, in eight digits of base 8,
 //         q = 2^(E - 1) sum_k 8^-k d_k,   d_k = -4 .. 4,
-//       each an e2m1 code (E: exponent of the head's largest value; what is left
-//       out lies 2^-24 below that value).  Digits are columns, of which CH in a row are
-//       summed by the accumulator, their weights being B's block scales (1, 2^-3,
-//       2^-6, 2^-9); the softmax adds up the others.
+//       each an e2m1 code (E: exponent of the head's largest value, of which what
+//       is left out is 2^-23 at most).  Digits are columns; the accumulator sums
+//       pairs of them, B's block scales being their weights (1, 2^-3), and the
+//       softmax adds up the four sums.
 //   V   its blocks run along the dims, not along the slots that O sums over, so
 //       an MMA with the identity as A and V as B writes V^T, block scales
 //       included, to TMEM as fp32 (every value exact), where it lies as the A

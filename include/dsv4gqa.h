@@ -61,7 +61,7 @@
  *     L   = exp(sink[i]) + sum_j exp(s_j)          (no sink: that term is 0)
  *     out = sum_j exp(s_j) V_j / L       lse = ln L
  *   Scores, softmax statistics and sums are fp32, products of 16-bit values
- *   exact (E2M1 caches: of q every value to within 2^-24 of its head's largest);
+ *   exact (E2M1 caches: of q every value to within 2^-23 of its head's largest);
  *   the weight of a row enters its product with V with an error of at most
  *   2^-17 of it, or 2^-11 where the cache is E4M3 or E2M1 and out bf16, and
  *   2^-36 of the largest weight (F16, E4M3 and E2M1 caches).  Beside an E2M1
