@@ -78,7 +78,9 @@ struct Shape4 {
     static constexpr int I_BYTES = 128 * ROWB, Q_SET = NS * ROWB, Q_BYTES = 2 * Q_SET, P_BYTES = kTile4 * NO * 4;
     static constexpr int NOTES = 2048;                       // barriers and notes
     static constexpr int FIT = (113 * 1024 - I_BYTES - 2 * Q_BYTES - 2 * P_BYTES - NOTES) / ENTRY / 2 * 2;
-    static constexpr int ENTRIES = FIT < 16 ? FIT : 16;
+    // (f16, 128 dims: 6 and not 8, which leaves the L1 cache more: 32 x 2048..32768 rows 134 us either way, with weights 181
+    // and 191; bf16: 128 and 124, with weights 174 and 179; 64 dims: 206 with 6 and 192 with 16)
+    static constexpr int ENTRIES = TWO && D == 128 ? 6 : FIT < 16 ? FIT : 16;
     static_assert(ENTRIES >= 4 && ENTRIES / 2 + 4 < kRing4, "the ring");
     static constexpr int O_I = 0, O_Q = O_I + I_BYTES, O_P = O_Q + 2 * Q_BYTES, O_RING = O_P + 2 * P_BYTES,
                          O_NOTES = O_RING + ENTRIES * ENTRY, SMEM = O_NOTES + NOTES;
