@@ -39,9 +39,10 @@
 // = 128) when its issuer is one thread that elect.sync picked in a converged
 // warp, and 88 clk of issue for each where the thread is picked by its index.  A
 // tile of 8 heads of 128 takes the tensor pipe 440 clk, and its 18 KB take an SM
-// 780 clk at the memory's rate.  Bound by instruction issue (2400 of a tile, 64 %
-// of the slots) and the fetch of five roles' code, beside a start and a join of
-// 12 us together.
+// 780 clk at the memory's rate.  Bound by the instructions of the copying
+// warps (without the copies of codes the same call takes 51 us for 57, without a
+// part of the MMAs, the votes or the look through the scales no less), beside a
+// start and a join of 12 us together.
 #pragma once
 #include <cstddef>
 
