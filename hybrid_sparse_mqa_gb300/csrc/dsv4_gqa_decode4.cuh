@@ -208,9 +208,10 @@ __device__ __forceinline__ uint32_t digit_e2m1(int d) {
     const int a = abs(d);
     return static_cast<uint32_t>(min(2 * a, a + 2)) | (static_cast<uint32_t>(d) >> 28 & 8u);
 }
-// 4-byte global -> shared copy; src_bytes = 0 writes zeros and reads nothing.
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+// Global -> shared copy of N = 4 or 8 bytes; src_bytes = 0 writes zeros and reads nothing.
+template <int N>
+__device__ __forceinline__ void cp_async_few(uint32_t dst, const void* src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(src_bytes) : "memory");
 }
 
 // What a CTA's warps tell each other.
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             const long long lane_off = lane_row * p.c.row_stride + lane_piece * 16, step = RPI * p.c.row_stride;
             const long long lane_block = (lane & 15) * p.c.b_row_stride;
             const uint32_t dst0 = 32 * w * ROWB + row_offset<ROWB>(lane_row, lane_piece * 16);
-            const uint32_t dst1 = kTile4 * ROWB + lane * 16 + w * 4;
+            const uint32_t dst1 = kTile4 * ROWB + (KS == 1 ? lane * 16 + w * 4 : (32 * w + lane) * 8);
             Cursor<kTile4> at;
             at.at = t0;
             at.locate(p, hcs, lane, early, request_of);
@@ -403,12 +404,10 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
                     const uint32_t dst = ring + e * S::ENTRY;
                     const uint8_t *pool = kv ? p.c.v : p.c.k, *blocks = kv ? p.c.vb : p.c.kb;
                     {
-                        // a lane's row: its block scales, 4 of them to a line of each K step
+                        // a lane's row: its block scales (128 dims: as they lie; warp 12 puts them where the MMA wants them)
                         const int s = slot0 + lane;
                         const bool in = whole || ((okm >> (lane >> 4) & 1) && s >= lo && s < n);
-                        const uint8_t* src = blocks + (in ? bo : 0);
-#pragma unroll
-                        for (int k = 0; k < KS; ++k) cp_async_4(dst + dst1 + 512 * k, src + (in ? 4 * k : 0), in ? 4u : 0u);
+                        cp_async_few<4 * KS>(dst + dst1, blocks + (in ? bo : 0), in ? 4u * KS : 0u);
                     }
                     if (whole) {
 #pragma unroll
@@ -443,21 +442,32 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
         }
     } else if (warp == 12) {
         // ============================================================ scales, and S
-        // Bit 7 where a lane's share of an entry's block scales has a NaN or a sign.
+        // An entry's block scales to the order of desc_scales, 512 bytes for each K step; bit 7 where a lane's have a NaN or a
+        // sign.
         auto odd_scales = [&](uint32_t entry) {
+            const uint32_t at = entry + kTile4 * ROWB;
+            uint4 x, y = make_uint4(0, 0, 0, 0);
+            if constexpr (KS == 1) {
+                x = ld_shared_u4(at + lane * 16);
+            } else {
+                const uint2 a = ld_shared_u2(at + lane * 8), b = ld_shared_u2(at + 256 + lane * 8);
+                const uint2 c = ld_shared_u2(at + 512 + lane * 8), d = ld_shared_u2(at + 768 + lane * 8);
+                x = make_uint4(a.x, b.x, c.x, d.x);
+                y = make_uint4(a.y, b.y, c.y, d.y);
+                __syncwarp();
+                st_shared_v4(at + lane * 16, x.x, x.y, x.z, x.w);
+                st_shared_v4(at + 512 + lane * 16, y.x, y.y, y.z, y.w);
+            }
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
             uint32_t odd = 0;
 #pragma unroll
-            for (int at = 0; at < S::SFB; at += 512) {
-                const uint4 x = ld_shared_u4(entry + kTile4 * ROWB + at + lane * 16);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) odd |= ((w[k] & 0x7f7f7f7fu) + 0x01010101u) | w[k];
-            }
+            for (int k = 0; k < 4 * KS; ++k) odd |= ((w[k] & 0x7f7f7f7fu) + 0x01010101u) | w[k];
             return odd & 0x80808080u;
         };
         // Signs go to the codes; of V, NaN scales become 0 and their blocks are returned (a bit each).
         auto mend_scales = [&](uint32_t entry, bool is_v) {
             uint32_t nan = 0;
+            __syncwarp();                          // (the lanes' lines are there)
 #pragma unroll 1
             for (int at = lane; at < S::SFB; at += 32) {
                 const int r = (at >> 4 & 31) + 32 * (at >> 2 & 3), block = 4 * (at >> 9) + (at & 3);
@@ -482,7 +492,8 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             warp_wait(notes.full[e], turn);
             warp_wait(notes.full[e + 1], turn);
             uint32_t nan = 0;
-            if (__any_sync(0xffffffffu, (odd_scales(entry) | odd_scales(entry + S::ENTRY)) != 0)) {
+            const uint32_t odd = odd_scales(entry) | odd_scales(entry + S::ENTRY);
+            if (__any_sync(0xffffffffu, odd != 0)) {
                 mend_scales(entry, false);
                 nan = mend_scales(entry + S::ENTRY, true);
             }
