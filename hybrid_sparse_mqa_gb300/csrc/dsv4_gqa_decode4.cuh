@@ -629,7 +629,9 @@ __global__ void __launch_bounds__(kThreads4, S::CTAS) dsv4_gqa_decode4_kernel(co
             for (int k = 1; k < TPH; k <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, k));
             bad = (__ballot_sync(0xffffffffu, bad) >> (lane & ~(TPH - 1)) & ((1u << TPH) - 1u)) != 0;
             int e = static_cast<int>(__float_as_uint(amax) >> 23 & 255u) - 127;
-            e = e < -100 ? -100 : e;
+            // (held where 2^(1 - e) and the score's factor are normal; a smaller head loses nothing by it: bf16's values are
+            // multiples of 2^-133, and the last digit counts 2^-147)
+            e = e < -125 ? -125 : e;
             const float up = __uint_as_float(static_cast<uint32_t>(128 - (bad ? 0 : e)) << 23);      // 2^(1 - e)
 #pragma unroll
             for (int k0 = 0; k0 < NW; k0 += 4) {
