@@ -364,7 +364,9 @@ def dsv4_topk(scores, lengths, k, *, max_length=None, out=None, stream=None):
 
 # ---------------------------------------------------------------- the grouped-query cache
 _GQA_TYPES = {torch.bfloat16: DSV4_GQA_BF16, torch.float16: DSV4_GQA_F16, torch.float8_e4m3fn: DSV4_GQA_E4M3,
-              torch.uint8: DSV4_GQA_E2M1, torch.float4_e2m1fn_x2: DSV4_GQA_E2M1}
+              torch.uint8: DSV4_GQA_E2M1}
+if hasattr(torch, "float4_e2m1fn_x2"):
+    _GQA_TYPES[torch.float4_e2m1fn_x2] = DSV4_GQA_E2M1
 _GQA_CODES = (DSV4_GQA_E4M3, DSV4_GQA_E2M1)
 
 
