@@ -323,9 +323,8 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
     const int most = row_bytes(c) > 256 ? kMaxCtas / 2 : kMaxCtas;
     pl.places = most;
     pl.min_tiles = four || (max_len + pl.tt - 1) / pl.tt <= kFewTiles ? 1 : 2;
-    const int list_most = four ? kMaxCtas : most;
     const long long want = pl.tiles / pl.min_tiles;
-    pl.ctas = want < 1 ? 1 : (want < list_most ? static_cast<int>(want) : list_most);
+    pl.ctas = want < 1 ? 1 : (want < most ? static_cast<int>(want) : most);
     pl.claims = !four && pl.ctas == most && pl.tiles >= (long long)most * kWarps * kClaimTiles ? most : 0;
     pl.warps = pl.ctas * (four ? 1 : kWarps);
     const size_t entries = size_t(2) * (pl.warps + pl.claims * kWarps) * 8 * pl.nt;
@@ -386,17 +385,21 @@ int launch_join_heads(const DecodeParams& p, void* stream) {
     return launch(dsv4_gqa_join_kernel<D, TT, HEADS, 1, 1>, dim3(segments, HEADS / 8), 256, 0, stream, 1, p);
 }
 
+// (lists in tiles of kTile4 slots: 8 heads at most)
 template <int D, int TT>
 int launch_join(const DecodeParams& p, int nt, void* stream) {
-    return nt == 1 ? launch_join_heads<D, TT, 8>(p, stream) : launch_join_heads<D, TT, 16>(p, stream);
+    if constexpr (TT != kTile4)
+        if (nt == 2) return launch_join_heads<D, TT, 16>(p, stream);
+    return launch_join_heads<D, TT, 8>(p, stream);
 }
 
 template <int TT>
 int launch_weights(const DecodeParams& p, int nt, void* stream) {
     constexpr int kSlots = kWeightThreads * kWeightSlots;
     const dim3 grid((p.max_len + kSlots - 1) / kSlots, p.batch * p.c.kv_heads);
-    return nt == 1 ? launch(dsv4_gqa_weight_kernel<TT, 8>, grid, kWeightThreads, 0, stream, 1, p)
-                   : launch(dsv4_gqa_weight_kernel<TT, 16>, grid, kWeightThreads, 0, stream, 1, p);
+    if constexpr (TT != kTile4)
+        if (nt == 2) return launch(dsv4_gqa_weight_kernel<TT, 16>, grid, kWeightThreads, 0, stream, 1, p);
+    return launch(dsv4_gqa_weight_kernel<TT, 8>, grid, kWeightThreads, 0, stream, 1, p);
 }
 
 template <int D, int TT, int HEADS>
@@ -411,7 +414,11 @@ bool load_join_heads() {
 template <int D, int TT>
 int load_join() {
     static unsigned long long ready = 0;
-    return once_per_device(ready, [] { return load_join_heads<D, TT, 8>() && load_join_heads<D, TT, 16>(); });
+    return once_per_device(ready, [] {
+        if constexpr (TT != kTile4)
+            if (!load_join_heads<D, TT, 16>()) return false;
+        return load_join_heads<D, TT, 8>();
+    });
 }
 int load_joins(int d, int tt) {
     if (tt == kTile4) return d == 64 ? load_join<64, kTile4>() : load_join<128, kTile4>();
