@@ -4,7 +4,7 @@ With 64 and 128 dims and up to 8 query heads per KV head the list is that of the
 import pytest
 import torch
 
-from tests._gqa4 import BF, Cache4
+from tests._gqa4 import BF, F8, HF, Cache4
 from tests._launches import kernels
 from tests.test_gpu_gqa4 import A, check_decode, i32  # noqa: F401
 
@@ -26,6 +26,105 @@ def test_kernels_are_counted(A):  # noqa: F811
     assert kernels(lambda: A.dsv4_gqa_decode(x, n, cache, max_len=90)) == 1
     assert kernels(lambda: A.dsv4_gqa_decode(x, n, cache)) == 2
     assert kernels(lambda: A.dsv4_gqa_decode(x, n, cache, weights=w, weights_out=w)) == 3
+
+
+def test_strided_queries_on_lists(A):  # noqa: F811
+    for q, dim, slots in ((BF, 128, 9000), (HF, 64, 17000)):
+        c = Cache4(q=q, hkv=3, dim=dim, rows=4, slots=slots, seed=5)
+        cache = c.handle(A)
+        wide = torch.randn(4, 40, dim, generator=c.gen).to(q).cuda()
+        n, close = i32([slots, 3000, 0, slots - 1]), wide[:, 3:18].contiguous()
+        want = on_list(lambda: A.dsv4_gqa_decode(close, n, cache))
+        got = on_list(lambda: A.dsv4_gqa_decode(wide[:, 3:18], n, cache))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert A.dsv4_attn_get_device_error() == 0
+
+
+def test_lists_on_streams_at_once(A):  # noqa: F811
+    # calls that share the SMs and their tensor memory, each stream with a form of its own
+    forms = []
+    for q, dim, slots in ((BF, 128, 17000), (HF, 128, 17000), (BF, 64, 33000)):
+        c = Cache4(q=q, hkv=4, dim=dim, page=64, rows=8, slots=slots, seed=6)
+        cache, x, n = c.handle(A), c.query(8, 32).cuda(), i32([slots - 700 * i for i in range(8)])
+        call = lambda x=x, n=n, cache=cache: A.dsv4_gqa_decode(x, n, cache)      # noqa: E731
+        forms.append((torch.cuda.Stream(), call, on_list(call), []))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for stream, call, _, got in forms:
+            with torch.cuda.stream(stream):
+                got.append(call())
+    torch.cuda.synchronize()
+    for _, _, want, got in forms:
+        for out, lse in got:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert A.dsv4_attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("q", [BF, HF])
+@pytest.mark.parametrize("dim,slots", [(64, 17000), (128, 9000)])
+def test_blocks_without_a_value_on_lists(A, q, dim, slots):  # noqa: F811
+    # NaN blocks behind the last rows change nothing; one of an attended V row makes its 16 dims NaN and leaves the others
+    # as they are; of K, everything of the KV head's queries
+    lens = [slots, slots // 2 + 1, 40]
+    c = Cache4(q=q, hkv=2, dim=dim, page=64, rows=3, slots=slots, seed=dim)
+    x, n = c.query(3, 8).cuda(), i32(lens)
+    decode = lambda cache: on_list(lambda: A.dsv4_gqa_decode(x, n, cache, max_len=slots))      # noqa: E731
+    plain = decode(c.handle(A))
+    c.poison(lens)
+    place = lambda b, s: (int(c.table[b, s // c.page]), s % c.page)      # noqa: E731
+    for b, length in enumerate(lens):
+        p, o = place(b, length // 2)
+        c.vb[p, 1, o, b] = 0xff if b == 1 else 0x7f
+    out, lse = decode(c.handle(A))
+    assert torch.equal(lse, plain[1])
+    for b in range(3):
+        nan = slice(16 * b, 16 * b + 16)
+        assert out[b, 4:, nan].isnan().all()
+        out[b, 4:, nan] = plain[0][b, 4:, nan]
+    assert torch.equal(out, plain[0])
+    p, o = place(0, slots - 1)
+    c.kb[p, 0, o, dim // 16 - 1] = 0xff
+    out, lse = decode(c.handle(A))
+    assert out[0, :4].isnan().all() and lse[0, :4].isnan().all() and torch.equal(lse[0, 4:], plain[1][0, 4:])
+    assert torch.equal(lse[1:], plain[1][1:])
+    assert A.dsv4_attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("q", [BF, HF])
+def test_signs_and_sizes_of_block_scales_on_lists(A, q):  # noqa: F811
+    for dim, slots in ((64, 17000), (128, 9000)):
+        c = Cache4(q=q, dim=dim, page=128, rows=2, slots=slots, seed=dim, wide_scales=True)
+        c.kb[..., 1] = c.kb[..., 1] ^ 0x80
+        c.vb[..., ::3, 2] = c.vb[..., ::3, 2] ^ 0x80
+        c.vb[..., ::2, 3] = 0x7e                     # 448
+        c.vb[..., 1::2, 0] = 0x01                    # the smallest
+        x, n, cache = c.query(2, 8).cuda(), i32([slots, 4007]), c.handle(A)
+        on_list(lambda: A.dsv4_gqa_decode(x, n, cache, max_len=slots))
+        check_decode(A, c, [slots, 4007], 8, max_len=slots)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_offsets_beyond_32_bits_on_lists(A, dim):  # noqa: F811
+    # codes and, behind them in the same page, block scales of a pool larger than 4 GB; the request's pages at its end
+    page, size = 1024, dim // 2 * 1024 + dim // 16 * 1024
+    width = 9 if dim == 128 else 17
+    pages = (1 << 32) // size + 2 * width + 8
+    few = Cache4(hkv=1, dim=dim, page=page, rows=1, slots=width * page, seed=1)
+    pool = torch.zeros(pages, size, dtype=torch.uint8, device="cuda")
+    codes = pool[:, : dim // 2 * page].view(pages, 1, page, dim // 2)
+    blocks = pool[:, dim // 2 * page:].view(pages, 1, page, dim // 16)
+    table = torch.tensor([[pages - 1 - 2 * i for i in range(width)]], dtype=torch.int32)
+    for i, p in enumerate(table[0].tolist()):
+        codes[p], blocks[p] = few.k[int(few.table[0, i])].cuda(), few.kb[int(few.table[0, i])].cuda()
+    assert int(table.min()) * size > 1 << 32
+    cache = A.make_gqa_cache(codes, codes, table.cuda(), k_blocks=blocks.view(F8), v_blocks=blocks.view(F8),
+                             k_scale=few.ks.cuda(), v_scale=few.ks.cuda())
+    few.v, few.vb, few.vs = few.k, few.kb, few.ks
+    x, n, small = few.query(1, 8).cuda(), i32([width * page - 100]), few.handle(A)
+    want = on_list(lambda: A.dsv4_gqa_decode(x, n, small))
+    got = on_list(lambda: A.dsv4_gqa_decode(x, n, cache))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert A.dsv4_attn_get_device_error() == 0
 
 
 @pytest.mark.parametrize("size", [2.0 ** -124, 2.0 ** -118, 2.0 ** -112, 2.0 ** -101, 2.0 ** 120])
