@@ -1,6 +1,10 @@
 """Attention over 4-bit rows on the kernel that each test names: a call that gives every segment a cluster is one launch,
 one that shares out the list of tiles is two (with weights three), and every test asserts which of them its calls take.
 With 64 and 128 dims and up to 8 query heads per KV head the list is that of the block-scaled tensor cores."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -137,3 +141,80 @@ def test_smallest_and_largest_queries_on_lists(A, dim, slots, size):  # noqa: F8
     on_list(lambda: A.dsv4_gqa_decode(x, n, cache, max_len=slots))
     check_decode(A, c, lens, 8, spread=size, scale=scale, max_len=slots)
     check_decode(A, c, [60, 33], 8, spread=size, scale=scale, max_len=60)          # and on a cluster
+
+
+_CAPTURE = """
+import torch
+from hybrid_sparse_mqa_gb300 import attn as A
+from tests._launches import kernels
+BF, HF, F8 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+gen = torch.Generator(device="cuda").manual_seed(1)
+def rand(*shape):
+    return torch.randn(*shape, generator=gen, device="cuda").to({q})
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+pages, hkv, page, dim = 140, 2, 256, {dim}
+k, v = (torch.randint(0, 256, (pages, hkv, page, dim // 2), generator=gen, device="cuda", dtype=torch.uint8) for _ in range(2))
+kb, vb = ((0.2 + 0.3 * torch.rand(pages, hkv, page, dim // 16, generator=gen, device="cuda")).to(F8) for _ in range(2))
+cache = A.make_gqa_cache(k, v, torch.arange(pages, device="cuda", dtype=torch.int32).view(2, 70), k_blocks=kb, v_blocks=vb)
+pools = [x.view(torch.uint8) for x in (k, v, kb, vb)]
+bits = lambda: [x.clone() for x in pools]
+q, wide, many = rand(2, 4, dim), rand(2, 32, dim), rand(160, 4, dim)
+lens, rows = ints(17500, 17000), ints(1, 0)
+w = torch.rand(2, hkv, 70 * page, generator=gen, device="cuda")
+new, slots = rand(2, 2 * hkv, dim), ints(17500, 17000)
+crowd, short = ints(*[i % 2 for i in range(160)]), ints(*[1 + i % 100 for i in range(160)])
+w_out = lambda: torch.zeros_like(w)
+order = ints(0, 1)
+def store():
+    A.dsv4_gqa_store(new[:, :hkv], new[:, hkv:], order, slots, cache)
+    return bits()
+calls = dict(
+    long=lambda: A.dsv4_gqa_decode(q, lens, cache),
+    kept=lambda: A.dsv4_gqa_decode(q, lens, cache, weights=w, weights_out=w_out(), req_pool_indices=rows),
+    wide=lambda: A.dsv4_gqa_decode(wide, lens, cache),
+    wide_short=lambda: A.dsv4_gqa_decode(wide, short[:2], cache, max_len=100),
+    many=lambda: A.dsv4_gqa_decode(many, short, cache, max_len=100, req_pool_indices=crowd),
+    evict=lambda: [A.dsv4_gqa_evict(lens, cache, w, 1000, weights_out=w_out()), *bits()],
+    load=lambda: A.dsv4_gqa_load(order, slots, cache), load_f16=lambda: A.dsv4_gqa_load(rows, slots, cache, dtype=HF),
+    store=store,
+)
+# one short call of each function, of the forms with the fewest launches, is what was made before the captures
+A.dsv4_gqa_decode(q, ints(3, 2), cache, max_len=100)
+A.dsv4_gqa_store(new[:, :hkv], new[:, hkv:], ints(0, 1), slots, cache)
+A.dsv4_gqa_load(ints(0, 1), slots, cache)
+A.dsv4_gqa_evict(ints(3, 2), cache, w, 100, max_len=100)
+A.dsv4_attn_get_device_error()
+before = bits()
+def restore():
+    for x, y in zip(pools, before):
+        x.copy_(y)
+torch.cuda.synchronize()
+graphs = dict()
+for name, call in calls.items():
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    graphs[name] = (graph, got)
+for name, call in calls.items():
+    for again in range(2):
+        restore()
+        graphs[name][0].replay()
+        torch.cuda.synchronize()
+        first = [x.clone() for x in graphs[name][1] if x is not None]
+        restore()
+        assert all(torch.equal(x, y) for x, y in zip(first, [x for x in call() if x is not None])), name
+assert A.dsv4_attn_get_device_error() == 0
+assert kernels(calls["long"]) == 2 and kernels(calls["wide"]) == 2 and kernels(calls["many"]) == 1
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("q", ["BF", "HF"])
+def test_captures_after_one_call_of_each_function(A, q, dim):  # noqa: F811
+    # in a process of its own: what an earlier test has launched is loaded already
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", _CAPTURE.format(q=q, dim=dim)], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
