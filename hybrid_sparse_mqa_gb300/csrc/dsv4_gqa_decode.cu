@@ -352,9 +352,11 @@ int make_plan(const dsv4_gqa_cache* c, int batch, int heads, int max_len, bool w
 //   1..2048 rows 85.5 and 96.6; 48 x 16 heads of 64, up to 1024 rows 31.5 and 34.2
 //   with weights, 1 x 333 rows 6.2 and 8.8, 8 x 500..1000 rows 9.3 and 14.6
 // Where the list is one of 4-bit rows on dsv4_gqa_decode4.cuh's kernel (device time, 8 KV heads of 128): 1 x 2000 rows 7.3
-// and 8.3, 1 x 12000 (not taken) 15.2 and 13.6, 8 x 1000..2000 10.0 and 13.7, 64 x 100..2000 34.9 and 48.8, 64 x 1000..2000
-// 43.5 and 41.5, 64 x 3000..3500 (not taken: 20 in several waves) 80 and 61, with weights 16 x 1000..2000 18.6 and 21.4; 48 x
-// 16 heads of 64, up to 1000 rows 21.5 and 39.9, 64 x 4 heads of 64, 1000..4000 rows, 30.1 and 29.7.
+// and 8.3, 1 x 12000 (not taken) 15.2 and 13.8, 8 x 1000..2000 10.0 and 13.7, 64 x 100..2000 35.1 and 49.4, 64 x 1000..2000
+// 43.7 and 41.8, 64 x 2000 48.7 and 47.0 (only max_len is known here, the same for these three: clusters lose 2 us where the
+// lengths are even and win 14 where they are not), 64 x 3000..3500 (not taken: 20 in several waves) 80 and 60, 128 x 1..1000
+// 34.0 and 65.5, with weights 16 x 1000..2000 18.6 and 21.4; 48 x 16 heads of 64, up to 1000 rows 21.6 and 40.0, 64 x 4 heads
+// of 64, 1000..4000 rows, 30.1 and 29.7.
 int segment_cluster(const DecodeParams& p, const Plan& pl) {
     const long long segments = (long long)p.batch * p.c.kv_heads * p.chunks;
     const int span = p.window > 0 ? std::min<long long>(p.max_len, (long long)p.window + pl.tt) : p.max_len;

@@ -9,7 +9,7 @@
 // mma.sync (two conversions and two products for every 4 codes of K and of V
 // and 16 slots; 4.5 bits a value come in faster than that: 32 x 2048..32768 rows,
 // 32 / 8 heads of 128, 187 us for 659 MB, 2 x 131072 rows 89 us for 302 MB; this
-// kernel: 125 and 61 us, 5.3 and 5.0 TB/s).  Here no thread touches a code:
+// kernel, with the join: 124 and 60 us of device time, 5.3 and 5.0 TB/s).  Here no thread touches a code:
 //   S   K is the A operand of a 4-bit MMA as it lies in the cache, block scales
 //       and all.  q becomes a B operand of 4 bits, in eight digits of base 8,
 //         q = 2^(E - 1) sum_k 8^-k d_k,   d_k = -4 .. 4,
@@ -22,7 +22,10 @@
 //       included, to TMEM as fp32 (every value exact), where it lies as the A
 //       operand of
 //   O^T += V^T P^T, a tf32 MMA.  Values have 6 bits; P is rounded to tf32's 11,
-//       or is two of them where the output is f16.
+//       or is two of them where the output is f16.  (bf16 outputs of those two
+//       calls with one piece are off by 1.67e-3 and 1.66e-3, relative rms, of
+//       which their own rounding is 1.66e-3 and 1.65e-3; two pieces take 134 and
+//       65 us.)
 // A NaN among the block scales of V would reach all dims of its row through the
 // identity's zeros, and the MMA takes scales without a sign.  So the issuing
 // warps look through the scales of each tile; a NaN block is noted and its scale
@@ -79,8 +82,9 @@ struct Shape4 {
     static constexpr int I_BYTES = 128 * ROWB, Q_SET = NS * ROWB, Q_BYTES = 2 * Q_SET, P_BYTES = kTile4 * NO * 4;
     static constexpr int NOTES = 2048;                       // barriers and notes
     static constexpr int FIT = (113 * 1024 - I_BYTES - 2 * Q_BYTES - 2 * P_BYTES - NOTES) / ENTRY / 2 * 2;
-    // (f16, 128 dims: 6 and not 8, which leaves the L1 cache more: 32 x 2048..32768 rows 134 us either way, with weights 181
-    // and 191; bf16: 128 and 124, with weights 174 and 179; 64 dims: 206 with 6 and 192 with 16)
+    // (f16, 128 dims: 6 and not 8, which leaves the L1 cache more.  Device time of 32 x 2048..32768 rows, 32 / 8 heads of 128:
+    // f16 133 us with 6 and 131 with 8, with weights kept 180 and 188; bf16 127 and 124, with weights 174 and 180.  The same
+    // rows of 64 / 16 heads of 64, as many bytes: bf16 206 with 6 and 191 with 16, f16 211 and 197)
     static constexpr int ENTRIES = TWO && D == 128 ? 6 : FIT < 16 ? FIT : 16;
     static_assert(ENTRIES >= 4 && ENTRIES / 2 + 4 < kRing4, "the ring");
     static constexpr int O_I = 0, O_Q = O_I + I_BYTES, O_P = O_Q + 2 * Q_BYTES, O_RING = O_P + 2 * P_BYTES,
