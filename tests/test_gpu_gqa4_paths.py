@@ -64,6 +64,28 @@ def test_lists_on_streams_at_once(A):  # noqa: F811
     assert A.dsv4_attn_get_device_error() == 0
 
 
+def test_lists_beside_the_sparse_attention(A):  # noqa: F811
+    # the draft's cache on one stream and the verified model's on another: both kernels use tensor memory
+    from hybrid_sparse_mqa_gb300 import synth
+    inp = synth.make_inputs(synth.Workload("beside", batch=8, heads=64, ratio=4, seq_lens=(900, 3000, 70, 5000, 2600, 4000, 1, 128),
+                                           seed=5), device="cuda")
+    c = Cache4(hkv=4, dim=128, page=64, rows=8, slots=17000, seed=6)
+    cache, x, n = c.handle(A), c.query(8, 32).cuda(), i32([17000 - 900 * i for i in range(8)])
+    calls = (lambda: A.dsv4_gqa_decode(x, n, cache), lambda: A.run_inputs(inp))
+    want = (on_list(calls[0]), calls[1]())
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in calls], ([], [])
+    for _ in range(20):
+        for stream, call, mine in zip(streams, calls, got):
+            with torch.cuda.stream(stream):
+                mine.append(call())
+    torch.cuda.synchronize()
+    for first, mine in zip(want, got):
+        for out, lse in mine:
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert A.dsv4_attn_get_device_error() == 0
+
+
 @pytest.mark.parametrize("q", [BF, HF])
 @pytest.mark.parametrize("dim,slots", [(64, 17000), (128, 9000)])
 def test_blocks_without_a_value_on_lists(A, q, dim, slots):  # noqa: F811
